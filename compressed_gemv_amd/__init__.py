@@ -1,6 +1,6 @@
 """Python binding of libqgemv (the MI355X compressed-weight product).
 
-Thin marshalling over the C ABI in include/qgemv.h: every function here has
+Thin marshalling over the C ABI in include/qgemv.h and include/qcache.h: every function here has
 the name of the C entry point it calls, takes torch tensors that already
 live on the GPU, allocates outputs with torch when none are given, passes
 raw device pointers and torch's current HIP stream, and raises QError on a
@@ -23,6 +23,8 @@ __all__ = [
     "qtq_centroids", "qtq_rotation", "qtq_quant_keys", "qtq_project", "qtq_logits", "qtq_quant_values", "qtq_attend",
     "qbinlr_sizes", "qpack_binlr", "qunpack_binlr", "qgemv_binlr", "qgemv_binlr_noalloc",
     "qstream_read", "qgemm_prefill_ws", "qgemm_prefill", "Q_F32", "Q_BF16", "Q_FMT_GROUP", "Q_FMT_BINLR",
+    "qcache_sizes", "make_qcache", "qcache_write", "qcache_read", "qcache_attend_ws", "qcache_attend",
+    "qcache_attend_shared",
 ]
 
 Q_OK, Q_EINVAL, Q_EALIGN, Q_EUNSUPPORTED, Q_ERANGE, Q_EWORKSPACE, Q_EHIP = 0, -1, -2, -3, -4, -5, -6
@@ -58,6 +60,22 @@ class qweight(ctypes.Structure):
 class qgroup_mat(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("meta", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("y", ctypes.c_void_p)]
+
+
+class qcache(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("bits", ctypes.c_int),
+        ("k_codes", ctypes.c_void_p), ("k_meta", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+    ]
+
+
+class qseqs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+        ("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+    ]
 
 
 def load() -> ctypes.CDLL:
@@ -104,6 +122,15 @@ def load() -> ctypes.CDLL:
         "qgemm_prefill_ws": (I32, [ctypes.POINTER(qweight), I64, SZ]),
         "qgemm_prefill": (I32, [ctypes.POINTER(qweight), P, I32, I64, P, I32, P, ctypes.c_size_t, P]),
     }
+    CA, SQ, U64, F32 = ctypes.POINTER(qcache), ctypes.POINTER(qseqs), ctypes.c_size_t, ctypes.c_float
+    sig.update({
+        "qcache_sizes": (I32, [I64, I32, I32, I32, I32, SZ, SZ]),
+        "qcache_write": (I32, [CA, SQ, P, I64, P, I64, I32, P]),
+        "qcache_read": (I32, [CA, SQ, P, I64, P, I64, I32, P]),
+        "qcache_attend_ws": (I32, [CA, SQ, I32, I64, SZ]),
+        "qcache_attend": (I32, [CA, SQ, P, I64, I32, F32, P, I64, I32, P, U64, P]),
+        "qcache_attend_shared": (I32, [CA, SQ, P, I64, P, I64, I32, F32, P, I64, I32, P, U64, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -653,3 +680,220 @@ def qgemm_prefill(w: qweight, X: torch.Tensor, Y: Optional[torch.Tensor] = None,
     _check(load().qgemm_prefill(ctypes.byref(w), _ptr(X), _dtype_code(X), M, _ptr(Y), _dtype_code(Y),
                                 _ptr(ws), nbytes, _stream(stream)), "qgemm_prefill")
     return Y
+
+
+# ------------------------------------------------- quantized, paged KV cache
+def qcache_sizes(n_pages: int, page_size: int, heads: int, head_dim: int, bits: int):
+    """(codes, meta) bytes of one buffer each; K and V have one of both."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().qcache_sizes(n_pages, page_size, heads, head_dim, bits, ctypes.byref(a), ctypes.byref(b)),
+           "qcache_sizes")
+    return a.value, b.value
+
+
+def make_qcache(n_pages: int, page_size: int, heads: int, head_dim: int, bits: int, k_codes=None, k_meta=None,
+                v_codes=None, v_meta=None, device=None) -> qcache:
+    """A cache descriptor over the given buffers, or over new ones (zeros) on
+    device when none are given; it keeps references to the tensors it points
+    into (._tensors: k_codes, k_meta, v_codes, v_meta)."""
+    cb, mb = qcache_sizes(n_pages, page_size, heads, head_dim, bits)
+    given = (k_codes, k_meta, v_codes, v_meta)
+    if all(t is None for t in given):
+        device = torch.device("cuda") if device is None else device
+        given = tuple(torch.zeros(n, dtype=d, device=device)
+                      for n, d in ((cb, torch.uint8), (mb // 4, torch.int32)) * 2)
+    for t, n, what in zip(given, (cb, mb, cb, mb), ("k_codes", "k_meta", "v_codes", "v_meta")):
+        _need_bytes(t, n, what)
+    _need_cuda(*given)
+    _one_device(*given)
+    c = qcache(n_pages, page_size, heads, head_dim, bits, *(t.data_ptr() for t in given))
+    c._tensors = given
+    c._device = given[0].device
+    return c
+
+
+def _one_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def _cache_seqs(cache: qcache, T: int, pages, lens, starts) -> qseqs:
+    if pages.dim() != 2 or pages.dtype != torch.int32:
+        raise ValueError("pages must be int32 [B][max_pages]")
+    B = pages.shape[0]
+    _need_numel(lens, B, "lens", (torch.int32,))
+    if starts is not None:
+        _need_numel(starts, B + 1, "starts", (torch.int32,))
+    elif T != B:
+        raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} sequences")
+    return qseqs(B, T, pages.shape[1], pages.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr())
+
+
+def _cache_rows(t: torch.Tensor, heads: int, D: int, dtypes, what: str) -> int:
+    """Token stride (elements) of rows [T][heads][D]: dense within a token,
+    any stride between tokens that keeps 16-byte alignment."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{what}: expected [T][{heads}][{D}], got shape {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {dtypes}")
+    T = t.shape[0]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < heads * D):
+        raise ValueError(f"{what}: the rows of one token must be contiguous, got strides {t.stride()}")
+    return t.stride(0) if T > 1 else heads * D
+
+
+def _cache_call(cache: qcache, stream, fresh, tensors, call, what):
+    """call(stream pointer) on the cache's device; every tensor lives there.
+    fresh: tensors this binding allocated, which a stream other than the
+    current one must be recorded on before they can be reused."""
+    dev = cache._device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        cur = torch.cuda.current_stream()
+        if stream is None or stream == cur:
+            return _check(call(ctypes.c_void_p(cur.cuda_stream)), what)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    for t in fresh:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.device(dev):
+        _check(call(ctypes.c_void_p(stream.cuda_stream)), what)
+
+
+def _need_cuda_rows(*ts):
+    """Row tensors may be strided between tokens, so only the place is checked."""
+    if not all(t.is_cuda for t in ts):
+        raise ValueError("tensors must be CUDA (HIP) tensors")
+
+
+def qcache_write(cache: qcache, K: torch.Tensor, V: torch.Tensor, pages, lens, starts=None, stream=None) -> None:
+    """Quantize rows K, V [T][heads][head_dim] (bf16 or fp32) into the cache:
+    the newest tokens of sequences with page tables pages int32
+    [B][max_pages] and lengths lens int32 [B] (the new tokens included); rows
+    starts[b] .. starts[b+1]-1 are sequence b's, one row each without starts."""
+    ks = _cache_rows(K, cache.heads, cache.head_dim, _OUT, "K")
+    vs = _cache_rows(V, cache.heads, cache.head_dim, (K.dtype,), "V")
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
+    seqs = _cache_seqs(cache, T, pages, lens, starts)
+    _need_cuda(pages, lens, starts)
+    _need_cuda_rows(K, V)
+    if T == 0:
+        return
+    lib = load()
+    _cache_call(cache, stream, (), (K, V, pages, lens, starts),
+                lambda st: lib.qcache_write(ctypes.byref(cache), ctypes.byref(seqs), K.data_ptr(), ks, V.data_ptr(), vs,
+                                            _dtype_code(K), st), "qcache_write")
+
+
+def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = None, K: Optional[torch.Tensor] = None,
+                V: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None):
+    """(K, V) [rows][heads][head_dim] of the cache as values: the last
+    starts[b+1] - starts[b] tokens of each sequence, the last one without
+    starts.  rows: starts[B] when no outputs are given (host knowledge; the
+    call does not look at device data).  Rows no sequence owns are not
+    written."""
+    fresh = ()
+    if K is None and V is None:
+        if rows is None:
+            if starts is not None:
+                raise ValueError("rows: missing, and no outputs given")
+            rows = pages.shape[0]
+        K = torch.empty((rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device)
+        V = torch.empty((rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device)
+        fresh = (K, V)
+    elif K is None or V is None:
+        raise ValueError("K and V: both outputs or neither")
+    ks = _cache_rows(K, cache.heads, cache.head_dim, _OUT, "K")
+    vs = _cache_rows(V, cache.heads, cache.head_dim, (K.dtype,), "V")
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
+    seqs = _cache_seqs(cache, T, pages, lens, starts)
+    _need_cuda(pages, lens, starts)
+    _need_cuda_rows(K, V)
+    if T == 0:
+        return K, V
+    lib = load()
+    _cache_call(cache, stream, fresh, (K, V, pages, lens, starts),
+                lambda st: lib.qcache_read(ctypes.byref(cache), ctypes.byref(seqs), K.data_ptr(), ks, V.data_ptr(), vs,
+                                           _dtype_code(K), st), "qcache_read")
+    return K, V
+
+
+def qcache_attend_ws(cache: qcache, B: int, T: int, max_pages: int, q_heads: int, prefix_len: int = 0) -> int:
+    """Workspace bytes for B sequences with T rows and page tables of
+    max_pages entries (prefix_len: of qcache_attend_shared)."""
+    n = ctypes.c_size_t()
+    seqs = qseqs(B, T, max_pages, None, None, None)
+    _check(load().qcache_attend_ws(ctypes.byref(cache), ctypes.byref(seqs), q_heads, prefix_len, ctypes.byref(n)),
+           "qcache_attend_ws")
+    return n.value
+
+
+def _cache_attend(what, cache, Q, prefix_pages, prefix_len, pages, lens, starts, scale, out, out_dtype, ws, stream):
+    if Q.dim() != 3 or Q.shape[1] < 1 or Q.shape[1] % cache.heads:
+        raise ValueError(f"Q: expected [T][q_heads][{cache.head_dim}] with q_heads a multiple of {cache.heads}, "
+                         f"got shape {tuple(Q.shape)}")
+    T, q_heads, D = Q.shape
+    qs = _cache_rows(Q, q_heads, cache.head_dim, (torch.bfloat16,), "Q")
+    seqs = _cache_seqs(cache, T, pages, lens, starts)
+    fresh_out = out is None
+    if fresh_out:
+        out = torch.empty((T, q_heads, D), dtype=out_dtype, device=Q.device)
+    os_ = _cache_rows(out, q_heads, cache.head_dim, _OUT, "out")
+    if out.shape[0] != T:
+        raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
+    _need_cuda(pages, lens, starts, prefix_pages, ws)
+    _need_cuda_rows(Q, out)
+    if T == 0:
+        return out
+    lib = load()
+    need = ctypes.c_size_t()
+    _check(lib.qcache_attend_ws(ctypes.byref(cache), ctypes.byref(seqs), q_heads, prefix_len, ctypes.byref(need)), what)
+    fresh_ws = ws is None
+    if fresh_ws:
+        ws = torch.empty(need.value, dtype=torch.uint8, device=Q.device)
+    _need_bytes(ws, need.value, "ws")
+    scale = D ** -0.5 if scale is None else float(scale)
+    rest = (Q.data_ptr(), qs, q_heads, scale, out.data_ptr(), os_, _dtype_code(out), ws.data_ptr(), _nbytes(ws))
+    if prefix_pages is None:
+        call = lambda st: lib.qcache_attend(ctypes.byref(cache), ctypes.byref(seqs), *rest, st)   # noqa: E731
+    else:
+        call = lambda st: lib.qcache_attend_shared(ctypes.byref(cache), ctypes.byref(seqs), prefix_pages.data_ptr(),   # noqa: E731
+                                                   prefix_len, *rest, st)
+    _cache_call(cache, stream, (out if fresh_out else None, ws if fresh_ws else None),
+                (Q, out, ws, pages, lens, starts, prefix_pages), call, what)
+    return out
+
+
+def qcache_attend(cache: qcache, Q: torch.Tensor, pages, lens, starts=None, scale: Optional[float] = None,
+                  out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None,
+                  stream=None):
+    """out [T][q_heads][head_dim] (bf16 or fp32): causal attention of rows Q
+    (bf16) over the cached tokens of their sequences; pages, lens and starts
+    as qcache_write's, whose rows these are.  scale: head_dim^-1/2 by
+    default.  Calls that may overlap need a workspace each."""
+    return _cache_attend("qcache_attend", cache, Q, None, 0, pages, lens, starts, scale, out, out_dtype, ws, stream)
+
+
+def qcache_attend_shared(cache: qcache, Q: torch.Tensor, prefix_pages, prefix_len: int, pages, lens, starts=None,
+                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                         out_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None, stream=None):
+    """qcache_attend behind a prefix of prefix_len tokens (pages prefix_pages,
+    int32) that all rows see, read once for the whole batch.  pages and lens
+    describe the sequences' own tokens only."""
+    if prefix_pages is None or prefix_pages.dtype != torch.int32:
+        raise ValueError("prefix_pages must be int32")
+    if prefix_len < 1:
+        raise ValueError(f"prefix_len: {prefix_len}, must be at least 1")
+    _need_numel(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages", (torch.int32,), exact=False)
+    return _cache_attend("qcache_attend_shared", cache, Q, prefix_pages, prefix_len, pages, lens, starts, scale, out,
+                         out_dtype, ws, stream)

@@ -1,0 +1,233 @@
+// Writing the quantized KV cache and reading it back.
+//
+// A row of D values is held by D / 8 neighbouring lanes, 8 values each, so one
+// 16-byte load per lane brings it in, the row's minimum and maximum are DPP
+// reductions inside those lanes, and each lane stores its 8 codes with one
+// store.  No contraction here: the codes come out bit-identical to any other
+// IEEE implementation of the definition.
+#pragma clang fp contract(off)
+
+#include "common.hpp"
+#include "kvcache.hpp"
+
+namespace qg {
+
+constexpr float kKvMax = 65280.0f;   // largest stored magnitude: s*q + o stays below fp16's largest value
+
+// min or max over the LPR (8 or 16) lanes of a row group
+template <int LPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v) {
+  auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : fminf(a, b); };
+  v = op(v, dpp_f32<0xB1>(v));                    // quad_perm [1,0,3,2]
+  v = op(v, dpp_f32<0x4E>(v));                    // quad_perm [2,3,0,1]
+  v = op(v, dpp_f32<0x141>(v));                   // row_half_mirror
+  if constexpr (LPR == 16) v = op(v, dpp_f32<0x140>(v));   // row_mirror
+  return v;
+}
+
+// The next fp16 above / below h (finite, and not the largest in that direction).
+__device__ __forceinline__ uint32_t f16_up(uint32_t h) { return (h & 0x8000u) ? h - 1u : h + 1u; }
+__device__ __forceinline__ uint32_t f16_down(uint32_t h) {
+  return (h & 0x7FFFu) == 0u ? 0x8001u : ((h & 0x8000u) ? h + 1u : h - 1u);
+}
+
+// Constants and codes of a row, x the lane's 8 values of it.  The codes are
+// the fp64 definition's: t = (x - o) / s is formed in fp32 with an error below
+// 255 * 2^-22 < 2^-13, and a lane with a t closer than 2^-12 to a half-way
+// point takes its codes in fp64.
+template <int LPR, int BITS>
+__device__ __forceinline__ void quant_row(float (&x)[8], int lane, uint32_t (&q)[8], uint32_t* meta) {
+  constexpr float L = (float)((1 << BITS) - 1);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bad |= (__float_as_uint(x[i]) & 0x7F800000u) == 0x7F800000u;
+    x[i] = fminf(fmaxf(x[i], -kKvMax), kKvMax);
+  }
+  const uint64_t rowmask = ((1ull << LPR) - 1ull) << (lane & ~(LPR - 1));
+  if (__ballot(bad) & rowmask) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = 0;
+    *meta = 0x7E007E00u;                          // s = o = NaN
+    return;
+  }
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) { mn = fminf(mn, x[i]); mx = fmaxf(mx, x[i]); }
+  mn = row_reduce<LPR, false>(mn);
+  mx = row_reduce<LPR, true>(mx);
+  uint32_t ob = __builtin_bit_cast(uint16_t, (_Float16)mn);
+  if (f16_bits_to_f32(ob) > mn) ob = f16_down(ob);
+  if ((ob & 0x7FFFu) == 0u) ob = 0u;
+  const float o = f16_bits_to_f32(ob);
+  const double v = ((double)mx - (double)o) / (double)L;
+  // two roundings, but the result lies within half a step (and a bit) of v
+  // on either side, so at most one step up reaches the smallest fp16 >= v
+  uint32_t sb = __builtin_bit_cast(uint16_t, (_Float16)(float)v) & 0x7FFFu;   // v >= 0; -0 becomes 0
+  if ((double)f16_bits_to_f32(sb) < v) sb = f16_up(sb);
+  const float s = f16_bits_to_f32(sb);
+  *meta = sb | (ob << 16);
+  const float rs = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
+  bool near = false;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = (x[i] - o) * rs;
+    const float r = __builtin_rintf(t[i]);
+    near |= fabsf(t[i] - r) > 0.5f - 0x1p-12f;
+    q[i] = (uint32_t)(int)fminf(r, L);
+  }
+  if (near && s > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = (uint32_t)(int)fmin(__builtin_rint(((double)x[i] - (double)o) / (double)s), (double)L);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t elem, float (&x)[8]) {
+  if constexpr (F32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
+    const float4 a = f[0], b = f[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + elem);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo_to_f32(v[i]); x[2 * i + 1] = bf16_hi_to_f32(v[i]); }
+  }
+}
+
+// Grid (row groups, head groups): a workgroup takes 256 / LPR tokens and hpw
+// heads of each, K and V, so a token's place is looked up once for 2 hpw rows.
+template <int D, int BITS, bool F32>
+__global__ __launch_bounds__(256) void kv_write_kernel(KvView c, SeqView sv, const void* __restrict__ K, int64_t k_stride,
+                                                       const void* __restrict__ V, int64_t v_stride, int hpw) {
+  constexpr int LPR = D / 8;
+  const int lane = threadIdx.x & 63, sub = threadIdx.x % LPR;
+  const int t = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  if (t >= sv.T) return;                           // whole row groups leave together
+  bool owned;
+  const int64_t slot = slot_of_row<LPR>(c, sv, t, sub, lane, &owned);
+  if (slot < 0) return;
+  const int h0 = blockIdx.y * hpw, h1 = h0 + hpw < c.heads ? h0 + hpw : c.heads;
+  for (int h = h0; h < h1; ++h) {
+    float x[2][8];
+    load8<F32>(K, t * k_stride + h * D + sub * 8, x[0]);
+    load8<F32>(V, t * v_stride + h * D + sub * 8, x[1]);
+    const int64_t row = cache_row(c, slot, h);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t q[8], meta;
+      quant_row<LPR, BITS>(x[kv], lane, q, &meta);
+      if constexpr (BITS == 8) {
+        uint2 w;
+        w.x = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+        w.y = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
+        *reinterpret_cast<uint2*>(c.codes[kv] + row * D + sub * 8) = w;
+      } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w |= q[i] << (4 * i);
+        *reinterpret_cast<uint32_t*>(c.codes[kv] + row * (D / 2) + sub * 4) = w;
+      }
+      if (sub == 0) c.meta[kv][row] = meta;
+    }
+  }
+}
+
+// The same shape as the write; a row without a place is zeros.
+template <int D, int BITS, bool F32>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvView c, SeqView sv, void* __restrict__ K, int64_t k_stride,
+                                                      void* __restrict__ V, int64_t v_stride, int hpw) {
+  constexpr int LPR = D / 8;
+  const int lane = threadIdx.x & 63, sub = threadIdx.x % LPR;
+  const int t = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  if (t >= sv.T) return;
+  bool owned;
+  const int64_t slot = slot_of_row<LPR>(c, sv, t, sub, lane, &owned);
+  if (!owned) return;
+  const int h0 = blockIdx.y * hpw, h1 = h0 + hpw < c.heads ? h0 + hpw : c.heads;
+  for (int h = h0; h < h1; ++h) {
+    const int64_t row = slot < 0 ? 0 : cache_row(c, slot, h);
+    uint32_t w[2][2] = {{0u, 0u}, {0u, 0u}}, meta[2] = {0u, 0u};
+    if (slot >= 0) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if constexpr (BITS == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(c.codes[kv] + row * D + sub * 8);
+          w[kv][0] = v.x; w[kv][1] = v.y;
+        } else {
+          w[kv][0] = *reinterpret_cast<const uint32_t*>(c.codes[kv] + row * (D / 2) + sub * 4);
+        }
+        meta[kv] = c.meta[kv][row];
+      }
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const float s = f16_lo(meta[kv]), o = f16_hi(meta[kv]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t q = BITS == 8 ? (w[kv][i / 4] >> (8 * (i % 4))) & 255u : (w[kv][0] >> (4 * i)) & 15u;
+        x[i] = __builtin_fmaf(s, (float)q, o);
+      }
+      void* out = kv ? V : K;
+      const int64_t at = t * (kv ? v_stride : k_stride) + h * D + sub * 8;
+      if constexpr (F32) {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        f[0] = float4{x[0], x[1], x[2], x[3]};
+        f[1] = float4{x[4], x[5], x[6], x[7]};
+      } else {
+        u32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = cvt_pk_bf16(x[2 * i], x[2 * i + 1]);
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + at) = v;
+      }
+    }
+  }
+}
+
+// Heads per workgroup: as many as leave about 2048 workgroups (8 per CU).
+static int heads_per_wg(int64_t row_groups, int heads) {
+  const int64_t n = row_groups * heads / 2048;
+  return n < 1 ? 1 : (n > heads ? heads : (int)n);
+}
+
+#define KV_DISPATCH(NAME, ...)                                                                        \
+  do {                                                                                                \
+    const int64_t rg = (s.T + 2048 / head_dim - 1) / (2048 / head_dim);                               \
+    const int hpw = heads_per_wg(rg, c.heads);                                                        \
+    const dim3 grid((unsigned)rg, (unsigned)((c.heads + hpw - 1) / hpw));                             \
+    if (head_dim == 128) {                                                                            \
+      if (bits == 8) {                                                                                \
+        if (f32) hipLaunchKernelGGL((NAME<128, 8, true>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);  \
+        else hipLaunchKernelGGL((NAME<128, 8, false>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);     \
+      } else {                                                                                        \
+        if (f32) hipLaunchKernelGGL((NAME<128, 4, true>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);  \
+        else hipLaunchKernelGGL((NAME<128, 4, false>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);     \
+      }                                                                                               \
+    } else {                                                                                          \
+      if (bits == 8) {                                                                                \
+        if (f32) hipLaunchKernelGGL((NAME<64, 8, true>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);   \
+        else hipLaunchKernelGGL((NAME<64, 8, false>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);      \
+      } else {                                                                                        \
+        if (f32) hipLaunchKernelGGL((NAME<64, 4, true>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);   \
+        else hipLaunchKernelGGL((NAME<64, 4, false>), grid, dim3(256), 0, st, __VA_ARGS__, hpw);      \
+      }                                                                                               \
+    }                                                                                                 \
+  } while (0)
+
+hipError_t launch_kv_write(const KvView& c, const SeqView& s, int head_dim, int bits, const void* K, int64_t k_stride,
+                           const void* V, int64_t v_stride, bool f32, hipStream_t st) {
+  KV_DISPATCH(kv_write_kernel, c, s, K, k_stride, V, v_stride);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvView& c, const SeqView& s, int head_dim, int bits, void* K, int64_t k_stride, void* V,
+                          int64_t v_stride, bool f32, hipStream_t st) {
+  KV_DISPATCH(kv_read_kernel, c, s, K, k_stride, V, v_stride);
+  return hipGetLastError();
+}
+#undef KV_DISPATCH
+
+}  // namespace qg

@@ -40,8 +40,9 @@ Modules:
   outlier  outlier channels kept aside in fp16, the rest group RTN
   codebook group codes read through a per-group book of a shared dictionary
   turboquant key-cache quantizer: rotation, Lloyd-Max coordinates, QJL signs
+  kvcache  paged KV cache: rows by RTN at 4 or 8 bits, ragged causal attention
 
 Parity status: every function here is pinned by tests under tests/ marked
 "not gpu" (bounds, brute force, closed forms, special cases, page figures).
 """
-from . import rtn, fmt, binlr, product, sizes, outlier, codebook, turboquant  # noqa: F401
+from . import rtn, fmt, binlr, product, sizes, outlier, codebook, turboquant, kvcache  # noqa: F401
