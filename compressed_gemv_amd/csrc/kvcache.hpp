@@ -38,7 +38,8 @@ struct KvAttend {
   int prefix_len;
 };
 hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws, hipStream_t st);
-size_t kv_attend_ws_bytes(int64_t B, int64_t T, int heads, int group, int head_dim, int64_t prefix_len);
+size_t kv_attend_ws_bytes(int64_t B, int64_t T, int64_t max_pages, int page_shift, int heads, int group, int head_dim,
+                          int64_t prefix_len);
 
 // Largest b in [0, B) with starts[b] <= t, searched by the LPR lanes of a row
 // group together: every step probes LPR evenly spaced entries at once, so B

@@ -157,8 +157,11 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
   if (prefix_len < 0) return Q_EINVAL;
   if (prefix_len > ((int64_t)1 << 30)) return Q_EUNSUPPORTED;
   // rows of one KV head are counted in 32 bits
-  if (s->T * (q_heads / c->heads) > (1 << 30)) return Q_EUNSUPPORTED;
-  *ws_bytes = qg::kv_attend_ws_bytes(s->B, s->T, c->heads, q_heads / c->heads, c->head_dim, prefix_len);
+  const int64_t rows = s->T * (q_heads / c->heads);
+  if (rows > (1 << 30)) return Q_EUNSUPPORTED;
+  // workgroups of a launch: a tile of 16 rows at least for each, and per sequence
+  if ((rows / 16 + s->B + 4096) * c->heads > INT32_MAX) return Q_EUNSUPPORTED;
+  *ws_bytes = qg::kv_attend_ws_bytes(s->B, s->T, s->max_pages, __builtin_ctz((unsigned)c->page_size), c->heads, q_heads / c->heads, c->head_dim, prefix_len);
   return Q_OK;
 }
 

@@ -103,12 +103,14 @@ class Cache:
         return out[0], out[1], owned
 
     def attend(self, Q, pages, lens, starts=None, scale=None, prefix_pages=None, prefix_len=0):
-        """(out fp64 [T][Hq][D], M, owned): M[t][hq][d] = sum_j p_j |v_jd| bounds what roundings of p and v do to out."""
+        """(out fp64 [T][Hq][D], M [2][T][Hq][D], owned): M[0] = sum_j p_j |v_jd| is what relative roundings of p and v
+        act on, M[1] = sum_j p_j (s_j q_jd + |o_j|) what roundings of the two parts of v = s q + o do."""
         T, Hq, D = Q.shape
         G = Hq // self.heads
         scale = D ** -0.5 if scale is None else scale
         kv, vv = self.values(0), self.values(1)
-        out, mag, owned = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.zeros(T, bool)
+        out, mag, owned = np.zeros((T, Hq, D)), np.zeros((2, T, Hq, D)), np.zeros(T, bool)
+        vo = np.abs(unpack_meta(self.meta[1])[1].astype(np.float64))
 
         def slots(table, n):
             return [a for a in (self.place(table[None], None, 0, j) for j in range(n)) if a]
@@ -127,5 +129,7 @@ class Cache:
                 w = np.exp(z - z.max(1, keepdims=True))
                 w /= w.sum(1, keepdims=True)
                 out[t, h * G:(h + 1) * G] = w @ v
-                mag[t, h * G:(h + 1) * G] = w @ np.abs(v)
+                o = vo[p_, h, s_][:, None]
+                mag[0, t, h * G:(h + 1) * G] = w @ np.abs(v)
+                mag[1, t, h * G:(h + 1) * G] = w @ (np.abs(v) + 2 * o)      # s q <= |v| + |o|
         return out, mag, owned

@@ -86,10 +86,14 @@ def attend_bound(batch, Q, scale, mag):
     s*q + o raises to at most 8 A: 128 * 2^-24 * 8 A = 2^-14 A.  A weight exp(z - m) / sum is then off by a
     factor of at most exp(2 d), d = (2^-11 + 2^-14) A.  A weight is rounded to 11 bits and a value to 11 bits:
     2^-11 each.  Sums over the keys in fp32: below 2^-14 for the lengths here (at most 2^10 terms of size mag
-    per partial sum).  All of it relative to mag = sum p |v|."""
+    per partial sum).  All of that relative to mag[0] = sum p |v|.
+
+    A value may also be summed as its two parts, (p s) q and p o, which can cancel down to a v far smaller than
+    either: a weight p s carried in two bf16 parts is off by 2^-8 * 2^-8 of itself at most, and the fp32 sums of
+    the parts by 2^-14 of them, so (2^-16 + 2^-14) mag[1], mag[1] >= sum p (s q + |o|)."""
     d = (2.0 ** -11 + 2.0 ** -14) * logit_size(batch, Q, scale)
     assert d.max() < 0.25
-    return (np.expm1(2 * d)[..., None] + 2.0 ** -10 + 2.0 ** -14) * (mag * 1.01) + 1e-30
+    return (np.expm1(2 * d)[..., None] + 2.0 ** -10 + 2.0 ** -14) * (mag[0] * 1.01) + (2.0 ** -16 + 2.0 ** -14) * mag[1] + 1e-30
 
 
 def check_attend(batch, Q, got32, ref, mag, owned, scale):

@@ -164,7 +164,7 @@ def _attend(gpu, b, rng, group, lead_rows=0, scale=None, shared=False, q_mul=1.0
     got = host(out)
     assert np.all(got[~owned] == 7.0), "a row that no sequence owns was written"
     worst = check_attend(b, q, got, ref, mag, owned, D ** -0.5 if scale is None else scale)
-    none = owned & (mag.max(axis=(1, 2)) == 0)
+    none = owned & (mag[0].max(axis=(1, 2)) == 0)
     assert np.all(got[none] == 0.0)         # rows that see nothing
     o16 = call()
     own = torch.from_numpy(owned).cuda()
