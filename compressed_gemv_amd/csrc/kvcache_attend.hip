@@ -474,6 +474,7 @@ hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, int64_t i
 namespace {
 
 constexpr int kWorkgroups = 1024;   // items aimed at in all: 4 workgroups of 4 waves for each of 256 CUs
+constexpr int kTileWorkgroups = 512;
 constexpr int kJoinGrid = 4096;
 
 // How one call is cut: everything the host decides, from sizes alone.
@@ -487,16 +488,24 @@ struct CallPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tile height and splitting by the rows a KV head has against one run of keys.
+SplitRule rule_for(int64_t rows, int group, int heads, int cap) {
+  const bool tiles = rows > 32;
+  const int wgs = tiles ? kTileWorkgroups : kWorkgroups;
+  return SplitRule{group, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256, tiles ? 64 : 128,
+                   wgs / heads > 1 ? wgs / heads : 1, tiles ? 2 : 1, cap};
+}
+
 CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int heads, int group, int head_dim,
                    int64_t prefix_len) {
   CallPlan p{};
-  const int target = kWorkgroups / heads > 1 ? kWorkgroups / heads : 1;
   const int64_t cap = max_pages << page_shift;
   const int64_t rows = ceil_div(T, B) * group;            // of one sequence, on average
-  p.own = SplitRule{group, rows <= 16 ? 16 : 32, 128, target, 1, (int)cap};
+  p.own = rule_for(rows, group, heads, (int)cap);
   const int64_t tiles = T * group / p.own.rt + B;         // at most, over all sequences
   const int64_t most_chunks = ceil_div(ceil_div(cap, p.own.ku), p.own.min_units);
   p.shared = prefix_len > 0;
+  const int target = p.own.target;
   p.own_items = most_chunks == 1 ? tiles : tiles + target + 8;
   if (tiles * most_chunks < p.own_items) p.own_items = tiles * most_chunks;
   // a launch with `target` tiles or more splits nothing
@@ -505,10 +514,10 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   else if (most_chunks == 1) p.own_slots = 0;
   p.join = p.shared || p.own_slots > 0;
   if (p.shared) {
-    p.pre = SplitRule{group, T * group <= 16 ? 16 : 32, 128, target, 1, 0};
+    p.pre = rule_for(T * group, group, heads, 0);
     const int64_t pt = ceil_div(T * group, p.pre.rt), units = ceil_div(prefix_len, p.pre.ku);
-    int64_t cu = ceil_div(pt * units, target);
-    if (cu < 1) cu = 1;
+    int64_t cu = ceil_div(pt * units, p.pre.target);
+    if (cu < p.pre.min_units) cu = p.pre.min_units;
     if (cu > units) cu = units;
     p.pre_cu = (int)cu;
     p.pre_chunks = (int)ceil_div(units, cu);
@@ -543,8 +552,11 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
   AttendArgs own{a, p.own, Partials{at(p.o_own), at(p.ml_own), (int)p.own_slots}, p.shared, false, 0, 0};
   AttendArgs pre{a, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_items}, true, true, p.pre_cu, p.pre_chunks};
   hipError_t e;
-  if (p.shared && (e = launch_kv_rows(pre, head_dim, bits, p.pre_items, st)) != hipSuccess) return e;
-  if ((e = launch_kv_rows(own, head_dim, bits, p.own_items, st)) != hipSuccess) return e;
+  auto launch = [&](const AttendArgs& x, int64_t items) {
+    return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, items, st) : launch_kv_rows(x, head_dim, bits, items, st);
+  };
+  if (p.shared && (e = launch(pre, p.pre_items)) != hipSuccess) return e;
+  if ((e = launch(own, p.own_items)) != hipSuccess) return e;
   if (!p.join) return hipSuccess;
   const int64_t rows = (int64_t)a.s.T * a.c.heads * a.group;
   const dim3 grid((unsigned)(rows < kJoinGrid ? rows : kJoinGrid));

@@ -110,5 +110,6 @@ __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const 
 }
 
 hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st);
+hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st);
 
 }  // namespace qg
