@@ -492,8 +492,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 SplitRule rule_for(int64_t rows, int group, int heads, int cap) {
   const bool tiles = rows > 32;
   const int wgs = tiles ? kTileWorkgroups : kWorkgroups;
-  return SplitRule{group, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256, tiles ? 64 : 128,
-                   wgs / heads > 1 ? wgs / heads : 1, tiles ? 2 : 1, cap};
+  return SplitRule{group, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256, 128,
+                   wgs / heads > 1 ? wgs / heads : 1, 1, cap};
 }
 
 CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int heads, int group, int head_dim,
