@@ -10,6 +10,7 @@ fallback, and any call fails loudly when the shared library is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -197,6 +198,7 @@ def _need_numel(t: Optional[torch.Tensor], numel: int, what: str, dtypes=None, e
 
 _ACT = (torch.float32, torch.bfloat16, torch.int16, torch.uint16)   # activations (bf16 as 16-bit bits)
 _OUT = (torch.float32, torch.bfloat16)
+_Q16 = (torch.bfloat16,)
 _H16 = (torch.int16, torch.uint16, torch.float16)                    # fp16 bit patterns
 
 
@@ -708,7 +710,8 @@ def make_qcache(n_pages: int, page_size: int, heads: int, head_dim: int, bits: i
     _one_device(*given)
     c = qcache(n_pages, page_size, heads, head_dim, bits, *(t.data_ptr() for t in given))
     c._tensors = given
-    c._device = given[0].device
+    c._device, c._index = given[0].device, given[0].get_device()
+    c._ref = ctypes.byref(c)
     return c
 
 
@@ -721,55 +724,61 @@ def _one_device(first, *rest):
 def _cache_seqs(cache: qcache, T: int, pages, lens, starts) -> qseqs:
     if pages.dim() != 2 or pages.dtype != torch.int32:
         raise ValueError("pages must be int32 [B][max_pages]")
-    B = pages.shape[0]
+    B, width = pages.shape
     _need_numel(lens, B, "lens", (torch.int32,))
     if starts is not None:
         _need_numel(starts, B + 1, "starts", (torch.int32,))
     elif T != B:
         raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} sequences")
-    return qseqs(B, T, pages.shape[1], pages.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr())
+    return qseqs(B, T, width, pages.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr())
 
 
 def _cache_rows(t: torch.Tensor, heads: int, D: int, dtypes, what: str) -> int:
     """Token stride (elements) of rows [T][heads][D]: dense within a token,
     any stride between tokens that keeps 16-byte alignment."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{what}: expected [T][{heads}][{D}], got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{what}: expected [T][{heads}][{D}], got shape {tuple(shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {dtypes}")
-    T = t.shape[0]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < heads * D):
+    token, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != D) or (shape[0] > 1 and token < heads * D):
         raise ValueError(f"{what}: the rows of one token must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if T > 1 else heads * D
+    return token if shape[0] > 1 else heads * D
 
 
-def _cache_call(cache: qcache, stream, fresh, tensors, call, what):
-    """call(stream pointer) on the cache's device; every tensor lives there.
-    fresh: tensors this binding allocated, which a stream other than the
-    current one must be recorded on before they can be reused."""
-    dev = cache._device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        cur = torch.cuda.current_stream()
-        if stream is None or stream == cur:
-            return _check(call(ctypes.c_void_p(cur.cuda_stream)), what)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-    for t in fresh:
-        if t is not None:
-            t.record_stream(stream)
-    with torch.cuda.device(dev):
-        _check(call(ctypes.c_void_p(stream.cuda_stream)), what)
+def _on_device(cache: qcache, dense: bool, *ts):
+    """Every tensor is on the cache's device (and contiguous, where dense)."""
+    for t in ts:
+        if t is None:
+            continue
+        if t.get_device() != cache._index:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA (HIP) tensors")
+            raise ValueError(f"tensors on different devices: {cache._device} and {t.device}")
+        if dense and not t.is_contiguous():
+            raise ValueError("pages, lens, starts and ws must be contiguous")
 
 
-def _need_cuda_rows(*ts):
-    """Row tensors may be strided between tokens, so only the place is checked."""
-    if not all(t.is_cuda for t in ts):
-        raise ValueError("tensors must be CUDA (HIP) tensors")
+def _cache_call(cache: qcache, stream, fresh, what, fn, *args):
+    """fn(cache, *args, stream) on the cache's device.  fresh: tensors this
+    binding allocated, which a stream other than the current one must be
+    recorded on before they can be reused."""
+    idx = cache._index
+    if stream is None and idx == torch.cuda.current_device():
+        status = fn(cache._ref, *args, torch._C._cuda_getCurrentRawStream(idx))
+    else:
+        if stream is None:
+            stream = torch.cuda.current_stream(cache._device)
+        elif stream.device != cache._device:
+            raise ValueError(f"stream on {stream.device}, tensors on {cache._device}")
+        for t in fresh:
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.device(cache._device):
+            status = fn(cache._ref, *args, stream.cuda_stream)
+    if status != Q_OK:
+        raise QError(status, what)
 
 
 def qcache_write(cache: qcache, K: torch.Tensor, V: torch.Tensor, pages, lens, starts=None, stream=None) -> None:
@@ -783,14 +792,12 @@ def qcache_write(cache: qcache, K: torch.Tensor, V: torch.Tensor, pages, lens, s
     if V.shape[0] != T:
         raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
     seqs = _cache_seqs(cache, T, pages, lens, starts)
-    _need_cuda(pages, lens, starts)
-    _need_cuda_rows(K, V)
+    _on_device(cache, True, pages, lens, starts)
+    _on_device(cache, False, K, V)
     if T == 0:
         return
-    lib = load()
-    _cache_call(cache, stream, (), (K, V, pages, lens, starts),
-                lambda st: lib.qcache_write(ctypes.byref(cache), ctypes.byref(seqs), K.data_ptr(), ks, V.data_ptr(), vs,
-                                            _dtype_code(K), st), "qcache_write")
+    _cache_call(cache, stream, (), "qcache_write", load().qcache_write, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
+                _dtype_code(K))
 
 
 def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = None, K: Optional[torch.Tensor] = None,
@@ -817,60 +824,66 @@ def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = N
     if V.shape[0] != T:
         raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
     seqs = _cache_seqs(cache, T, pages, lens, starts)
-    _need_cuda(pages, lens, starts)
-    _need_cuda_rows(K, V)
+    _on_device(cache, True, pages, lens, starts)
+    _on_device(cache, False, K, V)
     if T == 0:
         return K, V
-    lib = load()
-    _cache_call(cache, stream, fresh, (K, V, pages, lens, starts),
-                lambda st: lib.qcache_read(ctypes.byref(cache), ctypes.byref(seqs), K.data_ptr(), ks, V.data_ptr(), vs,
-                                           _dtype_code(K), st), "qcache_read")
+    _cache_call(cache, stream, fresh, "qcache_read", load().qcache_read, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
+                _dtype_code(K))
     return K, V
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_ws(page_size, heads, head_dim, bits, B, T, max_pages, q_heads, prefix_len) -> int:
+    n = ctypes.c_size_t()
+    c, seqs = qcache(1, page_size, heads, head_dim, bits), qseqs(B, T, max_pages)
+    _check(load().qcache_attend_ws(ctypes.byref(c), ctypes.byref(seqs), q_heads, prefix_len, ctypes.byref(n)),
+           "qcache_attend_ws")
+    return n.value
 
 
 def qcache_attend_ws(cache: qcache, B: int, T: int, max_pages: int, q_heads: int, prefix_len: int = 0) -> int:
     """Workspace bytes for B sequences with T rows and page tables of
     max_pages entries (prefix_len: of qcache_attend_shared)."""
-    n = ctypes.c_size_t()
-    seqs = qseqs(B, T, max_pages, None, None, None)
-    _check(load().qcache_attend_ws(ctypes.byref(cache), ctypes.byref(seqs), q_heads, prefix_len, ctypes.byref(n)),
-           "qcache_attend_ws")
-    return n.value
+    return _attend_ws(cache.page_size, cache.heads, cache.head_dim, cache.bits, B, T, max_pages, q_heads, prefix_len)
 
 
-def _cache_attend(what, cache, Q, prefix_pages, prefix_len, pages, lens, starts, scale, out, out_dtype, ws, stream):
-    if Q.dim() != 3 or Q.shape[1] < 1 or Q.shape[1] % cache.heads:
-        raise ValueError(f"Q: expected [T][q_heads][{cache.head_dim}] with q_heads a multiple of {cache.heads}, "
-                         f"got shape {tuple(Q.shape)}")
-    T, q_heads, D = Q.shape
-    qs = _cache_rows(Q, q_heads, cache.head_dim, (torch.bfloat16,), "Q")
+def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_dtype, ws, stream):
+    """prefix: () or (prefix_pages, prefix_len)."""
+    heads, D = cache.heads, cache.head_dim
+    shape = Q.shape
+    if len(shape) != 3 or shape[1] < 1 or shape[1] % heads:
+        raise ValueError(f"Q: expected [T][q_heads][{D}] with q_heads a multiple of {heads}, got shape {tuple(shape)}")
+    T, q_heads, _ = shape
+    q_stride = _cache_rows(Q, q_heads, D, _Q16, "Q")
     seqs = _cache_seqs(cache, T, pages, lens, starts)
-    fresh_out = out is None
-    if fresh_out:
-        out = torch.empty((T, q_heads, D), dtype=out_dtype, device=Q.device)
-    os_ = _cache_rows(out, q_heads, cache.head_dim, _OUT, "out")
+    fresh_out = fresh_ws = None
+    if out is None:
+        out = fresh_out = torch.empty((T, q_heads, D), dtype=out_dtype, device=Q.device)
+    o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
     if out.shape[0] != T:
         raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
-    _need_cuda(pages, lens, starts, prefix_pages, ws)
-    _need_cuda_rows(Q, out)
+    _on_device(cache, True, pages, lens, starts)
+    _on_device(cache, False, Q, out)
     if T == 0:
         return out
-    lib = load()
-    need = ctypes.c_size_t()
-    _check(lib.qcache_attend_ws(ctypes.byref(cache), ctypes.byref(seqs), q_heads, prefix_len, ctypes.byref(need)), what)
-    fresh_ws = ws is None
-    if fresh_ws:
-        ws = torch.empty(need.value, dtype=torch.uint8, device=Q.device)
-    _need_bytes(ws, need.value, "ws")
-    scale = D ** -0.5 if scale is None else float(scale)
-    rest = (Q.data_ptr(), qs, q_heads, scale, out.data_ptr(), os_, _dtype_code(out), ws.data_ptr(), _nbytes(ws))
-    if prefix_pages is None:
-        call = lambda st: lib.qcache_attend(ctypes.byref(cache), ctypes.byref(seqs), *rest, st)   # noqa: E731
+    n_prefix = prefix[1] if prefix else 0
+    need = _attend_ws(cache.page_size, heads, D, cache.bits, seqs.B, T, seqs.max_pages, q_heads, n_prefix)
+    if ws is None:
+        ws = fresh_ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        ws_bytes = need
     else:
-        call = lambda st: lib.qcache_attend_shared(ctypes.byref(cache), ctypes.byref(seqs), prefix_pages.data_ptr(),   # noqa: E731
-                                                   prefix_len, *rest, st)
-    _cache_call(cache, stream, (out if fresh_out else None, ws if fresh_ws else None),
-                (Q, out, ws, pages, lens, starts, prefix_pages), call, what)
+        _need_bytes(ws, need, "ws")
+        _on_device(cache, True, ws)
+        ws_bytes = _nbytes(ws)
+    rest = (Q.data_ptr(), q_stride, q_heads, D ** -0.5 if scale is None else scale, out.data_ptr(), o_stride,
+            Q_F32 if out.dtype == torch.float32 else Q_BF16, ws.data_ptr(), ws_bytes)
+    if prefix:
+        _on_device(cache, True, prefix[0])
+        _cache_call(cache, stream, (fresh_out, fresh_ws), what, load().qcache_attend_shared, seqs, prefix[0].data_ptr(),
+                    n_prefix, *rest)
+    else:
+        _cache_call(cache, stream, (fresh_out, fresh_ws), what, load().qcache_attend, seqs, *rest)
     return out
 
 
@@ -881,7 +894,7 @@ def qcache_attend(cache: qcache, Q: torch.Tensor, pages, lens, starts=None, scal
     (bf16) over the cached tokens of their sequences; pages, lens and starts
     as qcache_write's, whose rows these are.  scale: head_dim^-1/2 by
     default.  Calls that may overlap need a workspace each."""
-    return _cache_attend("qcache_attend", cache, Q, None, 0, pages, lens, starts, scale, out, out_dtype, ws, stream)
+    return _cache_attend("qcache_attend", cache, Q, (), pages, lens, starts, scale, out, out_dtype, ws, stream)
 
 
 def qcache_attend_shared(cache: qcache, Q: torch.Tensor, prefix_pages, prefix_len: int, pages, lens, starts=None,
@@ -895,5 +908,5 @@ def qcache_attend_shared(cache: qcache, Q: torch.Tensor, prefix_pages, prefix_le
     if prefix_len < 1:
         raise ValueError(f"prefix_len: {prefix_len}, must be at least 1")
     _need_numel(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages", (torch.int32,), exact=False)
-    return _cache_attend("qcache_attend_shared", cache, Q, prefix_pages, prefix_len, pages, lens, starts, scale, out,
+    return _cache_attend("qcache_attend_shared", cache, Q, (prefix_pages, prefix_len), pages, lens, starts, scale, out,
                          out_dtype, ws, stream)

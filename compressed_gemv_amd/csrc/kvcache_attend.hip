@@ -62,50 +62,6 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
   const Work w = work_of(x, item, lane);
   if (w.b < 0) return;
 
-  // queries: operand registers, sums, and what each row sees
-  u32x4_t qf[NT][STEPS];
-  float qs[NT];
-  int lim[NT];
-  int limmin = w.k1;
-  const float c0 = a.scale * 1.4426950408889634f, c1 = c0 * kCode;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int row = w.row0 + 16 * n + r;
-    const bool ok = row < w.rows;
-    const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
-    const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D;
-    float sum = 0.f;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int d0 = BITS == 8 ? (D == 128 ? 64 * (s / 2) + 16 * kg + 8 * (s % 2) : 16 * kg + 8 * s)
-                               : 2 * KB * kg + 8 * s;
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (ok) v = *reinterpret_cast<const u32x4_t*>(q + d0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum += bf16_lo_to_f32(v[e]) + bf16_hi_to_f32(v[e]);
-        v[e] = up_pair(v[e]);
-      }
-      if constexpr (BITS == 4) {           // pairs (j, j + 4), as a nibble mask leaves them
-        const u32x4_t t = v;
-        v[0] = __builtin_amdgcn_perm(t[2], t[0], 0x05040100u);
-        v[1] = __builtin_amdgcn_perm(t[2], t[0], 0x07060302u);
-        v[2] = __builtin_amdgcn_perm(t[3], t[1], 0x05040100u);
-        v[3] = __builtin_amdgcn_perm(t[3], t[1], 0x07060302u);
-      }
-      qf[n][s] = v;
-    }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    qs[n] = sum * c0;
-    lim[n] = ok ? row_sees(w, tok) : w.k1;
-    int lo = lim[n];
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) { const int o = __shfl_xor(lo, d); lo = o < lo ? o : lo; }
-    limmin = lo < limmin ? lo : limmin;
-  }
-  limmin = __builtin_amdgcn_readfirstlane(limmin);
-
   f32x4_t acc[NT][TILES];
   float m[NT], l[NT], po[NT];              // maximum, sum of weights, sum of weights times offsets
 #pragma unroll
@@ -178,6 +134,58 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
       w_.vm[hf] = *reinterpret_cast<const u32x4_t*>(a.c.meta[1] + row + 4 * kg);
     }
   };
+
+  // the first keys are on their way while the queries are made ready
+  Raw ra, rb;
+  if (ks < ke) {
+    refill(ks >> shift);
+    load(ks, ra);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  // queries: operand registers, sums, and what each row sees
+  u32x4_t qf[NT][STEPS];
+  float qs[NT];
+  int lim[NT];
+  int limmin = w.k1;
+  const float c0 = a.scale * 1.4426950408889634f, c1 = c0 * kCode;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int row = w.row0 + 16 * n + r;
+    const bool ok = row < w.rows;
+    const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
+    const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D;
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int d0 = BITS == 8 ? (D == 128 ? 64 * (s / 2) + 16 * kg + 8 * (s % 2) : 16 * kg + 8 * s)
+                               : 2 * KB * kg + 8 * s;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (ok) v = *reinterpret_cast<const u32x4_t*>(q + d0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum += bf16_lo_to_f32(v[e]) + bf16_hi_to_f32(v[e]);
+        v[e] = up_pair(v[e]);
+      }
+      if constexpr (BITS == 4) {           // pairs (j, j + 4), as a nibble mask leaves them
+        const u32x4_t t = v;
+        v[0] = __builtin_amdgcn_perm(t[2], t[0], 0x05040100u);
+        v[1] = __builtin_amdgcn_perm(t[2], t[0], 0x07060302u);
+        v[2] = __builtin_amdgcn_perm(t[3], t[1], 0x05040100u);
+        v[3] = __builtin_amdgcn_perm(t[3], t[1], 0x07060302u);
+      }
+      qf[n][s] = v;
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    qs[n] = sum * c0;
+    lim[n] = ok ? row_sees(w, tok) : w.k1;
+    int lo = lim[n];
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) { const int o = __shfl_xor(lo, d); lo = o < lo ? o : lo; }
+    limmin = lo < limmin ? lo : limmin;
+  }
+  limmin = __builtin_amdgcn_readfirstlane(limmin);
 
   auto compute = [&](int key, const Raw& w_) {
     f32x4_t z[NT][2];
@@ -299,9 +307,6 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
   };
 
   if (ks < ke) {
-    refill(ks >> shift);
-    Raw ra, rb;
-    load(ks, ra);
     int key = ks;
     while (true) {
       if (key + 32 < ke) load(key + 32, rb);
@@ -369,21 +374,25 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
 }
 
 // ------------------------------------------------------------------- join
-// One workgroup per (row, query head) at a time: out = sum_c 2^(m_c - M) o_c
-// over sum_c 2^(m_c - M) l_c, c the chunks of the prefix (if any) and of the
-// row's own keys.  D / 4 lanes hold a row, so 256 / (D / 4) chunks are read at
-// once.
-template <int D>
+// out = sum_c 2^(m_c - M) o_c over sum_c 2^(m_c - M) l_c, c the chunks of the
+// prefix (if any) and of the row's own keys.  All latency: D / 4 lanes hold a
+// row, and a lane group takes its chunks in batches of 8 with all their loads
+// in flight at once.  WAVES waves work on one (row, query head): 4 where there
+// are few rows, each with many chunks, 1 where there are many.
+template <int D, int WAVES>
 __global__ __launch_bounds__(256) void kv_join_kernel(AttendArgs own, AttendArgs pre) {
-  constexpr int LPR = D / 4, GRP = 256 / LPR;
-  __shared__ __align__(16) float os[GRP][D];
-  __shared__ float red[2][4];
+  constexpr int LPR = D / 4, GRP = 64 * WAVES / LPR, BATCH = 8;
+  __shared__ __align__(16) float os[WAVES][D];
+  __shared__ float mls[WAVES][2];
   const KvAttend& a = own.a;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int cu = split_units(a.s, own.rule, lane);
   if (!own.shared && cu == kNoSplit) return;
   const int Hq = a.c.heads * a.group;
-  for (int64_t idx = blockIdx.x; idx < (int64_t)a.s.T * Hq; idx += gridDim.x) {   // workgroup-uniform
+  const int grp = (WAVES == 4 ? threadIdx.x : lane) / LPR, sub = lane % LPR;
+  const int64_t step = (int64_t)gridDim.x * (4 / WAVES);
+  for (int64_t idx = (int64_t)blockIdx.x * (4 / WAVES) + (WAVES == 4 ? 0 : wave); idx < (int64_t)a.s.T * Hq; idx += step) {
+    // uniform over the WAVES waves of the row
     const int t = (int)(idx / Hq), hq = (int)(idx % Hq), h = hq / a.group, g = hq - h * a.group;
     int b = t;
     if (a.s.starts) b = find_seq<64>(a.s.starts, a.s.B, t, lane, lane);
@@ -397,56 +406,76 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttendArgs own, AttendArgs
     const int P = t * a.group + g, np = own.shared ? pre.prefix_chunks : 0;
     const int pslot = own.shared ? P / pre.rule.rt * np : 0, prow = own.shared ? P % pre.rule.rt : 0;
     const int n = np + chunks;
-    auto ml_of = [&](int c) -> const float* {
-      return c < np ? part_ml(pre, pslot + c, h, prow) : part_ml(own, slot + c - np, h, row);
-    };
-    float M = -INFINITY;
-    bool nan = false;
-    for (int c = tid; c < n; c += 256) {
-      const float* ml = ml_of(c);
-      M = fmaxf(M, ml[0]);
-      nan |= ml[1] != ml[1];
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-    const bool anynan = __ballot(nan) != 0;
-    if (lane == 0) { red[0][wave] = M; red[1][wave] = anynan ? 1.f : 0.f; }
-    __syncthreads();
-    M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float bad = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-    const int grp = tid / LPR, sub = tid % LPR;
+    float M = -INFINITY, L = 0.f;
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    float L = 0.f;
-#pragma unroll 4
-    for (int c = grp; c < n; c += GRP) {
-      const float* ml = ml_of(c);
-      const float mc = ml[0], lc = ml[1];
-      const float* o = c < np ? part_o<D>(pre, pslot + c, h, prow) : part_o<D>(own, slot + c - np, h, row);
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(o + 4 * sub);
-      const bool some = mc != -INFINITY;
-      const float f = some ? exp2_hw(mc - M) : 0.f;
-      L += some ? lc * f : 0.f;
+    for (int c0 = grp; c0 < n; c0 += GRP * BATCH) {
+      float mc[BATCH], lc[BATCH];
+      f32x4_t o[BATCH];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += some ? v[i] * f : 0.f;
-    }
-    *reinterpret_cast<f32x4_t*>(&os[grp][4 * sub]) = acc;
-    // every lane of a group holds the group's L; the sum over groups through LDS as well
-    __shared__ float Ls[GRP];
-    if (sub == 0) Ls[grp] = L;
-    __syncthreads();
-    if (tid < LPR) {
-      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-      float lt = 0.f;
-      for (int k = 0; k < GRP; ++k) {
-        const f32x4_t u = *reinterpret_cast<const f32x4_t*>(&os[k][4 * tid]);
-        for (int i = 0; i < 4; ++i) v[i] += u[i];
-        lt += Ls[k];
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = c0 + i * GRP;
+        mc[i] = -INFINITY;
+        lc[i] = 0.f;
+        o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (c < n) {
+          const bool p = c < np;
+          const float* ml = p ? part_ml(pre, pslot + c, h, prow) : part_ml(own, slot + c - np, h, row);
+          const float* src = p ? part_o<D>(pre, pslot + c, h, prow) : part_o<D>(own, slot + c - np, h, row);
+          const float2 v = *reinterpret_cast<const float2*>(ml);
+          mc[i] = v.x;
+          lc[i] = v.y;
+          o[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * sub);
+        }
       }
-      const float inv = lt == 0.f ? 0.f : 1.0f / lt;
-      for (int i = 0; i < 4; ++i) v[i] = bad != 0.f ? NAN : v[i] * inv;
-      store_out4(a, (int64_t)t * a.o_stride + (int64_t)hq * D + 4 * tid, v);
+      float mb = M;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) mb = fmaxf(mb, mc[i]);
+      const float f0 = M == -INFINITY ? 0.f : exp2_hw(M - mb);
+      L *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] *= f0;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float f = mc[i] == -INFINITY ? 0.f : exp2_hw(mc[i] - mb);
+        L += lc[i] * f;                    // a NaN sum (a NaN key was seen) stays one
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(o[i][k], f, acc[k]);
+      }
+      M = mb;
     }
-    __syncthreads();
+    // the groups of the wave, then the waves
+    auto join2 = [&](float M2, float L2, const f32x4_t& a2) {
+      const float mm = fmaxf(M, M2);
+      const float f = M == -INFINITY ? 0.f : exp2_hw(M - mm), f2 = M2 == -INFINITY ? 0.f : exp2_hw(M2 - mm);
+      L = L * f + L2 * f2;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f + a2[k] * f2;
+      M = mm;
+    };
+#pragma unroll
+    for (int d = LPR; d < 64; d <<= 1) {
+      f32x4_t a2;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a2[k] = __shfl_xor(acc[k], d);
+      join2(__shfl_xor(M, d), __shfl_xor(L, d), a2);
+    }
+    if constexpr (WAVES > 1) {
+      if (lane < LPR) *reinterpret_cast<f32x4_t*>(&os[wave][4 * sub]) = acc;
+      if (lane == 0) { mls[wave][0] = M; mls[wave][1] = L; }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int w2 = 1; w2 < WAVES; ++w2)
+          join2(mls[w2][0], mls[w2][1], *reinterpret_cast<const f32x4_t*>(&os[w2][4 * sub]));
+      }
+      __syncthreads();
+    }
+    if (lane < LPR && (WAVES == 1 || wave == 0)) {
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] *= inv;
+      store_out4(a, (int64_t)t * a.o_stride + (int64_t)hq * D + 4 * sub, acc);
+    }
   }
 }
 
@@ -475,7 +504,8 @@ namespace {
 
 constexpr int kWorkgroups = 1024;   // items aimed at in all: 4 workgroups of 4 waves for each of 256 CUs
 constexpr int kTileWorkgroups = 512;
-constexpr int kJoinGrid = 4096;
+constexpr int kJoinGrid = 4096;      // workgroups of the join at most; each takes rows in turn
+constexpr int kJoinFew = 1024;       // rows up to which a whole workgroup joins one row
 
 // How one call is cut: everything the host decides, from sizes alone.
 struct CallPlan {
@@ -559,9 +589,16 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
   if ((e = launch(own, p.own_items)) != hipSuccess) return e;
   if (!p.join) return hipSuccess;
   const int64_t rows = (int64_t)a.s.T * a.c.heads * a.group;
-  const dim3 grid((unsigned)(rows < kJoinGrid ? rows : kJoinGrid));
-  if (head_dim == 128) hipLaunchKernelGGL((kv_join_kernel<128>), grid, dim3(256), 0, st, own, pre);
-  else hipLaunchKernelGGL((kv_join_kernel<64>), grid, dim3(256), 0, st, own, pre);
+  const bool few = rows <= kJoinFew;
+  const int64_t wgs = few ? rows : ceil_div(rows, 4);
+  const dim3 grid((unsigned)(wgs < kJoinGrid ? wgs : kJoinGrid));
+  if (head_dim == 128) {
+    if (few) hipLaunchKernelGGL((kv_join_kernel<128, 4>), grid, dim3(256), 0, st, own, pre);
+    else hipLaunchKernelGGL((kv_join_kernel<128, 1>), grid, dim3(256), 0, st, own, pre);
+  } else {
+    if (few) hipLaunchKernelGGL((kv_join_kernel<64, 4>), grid, dim3(256), 0, st, own, pre);
+    else hipLaunchKernelGGL((kv_join_kernel<64, 1>), grid, dim3(256), 0, st, own, pre);
+  }
   return hipGetLastError();
 }
 

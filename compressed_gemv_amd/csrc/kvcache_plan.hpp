@@ -61,13 +61,24 @@ __device__ __forceinline__ int split_units(const SeqView& s, const SplitRule& p,
     w += (float)rt * (float)((r.need + p.ku - 1) / p.ku);
     tiles += rt;
   }
-  float tf = (float)tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) { w += __shfl_xor(w, d); tf += __shfl_xor(tf, d); }
+  w = wave_sum(w);
+  const float tf = wave_sum((float)tiles);
   if (tf >= (float)p.target) return kNoSplit;
   const float c = w / (float)p.target;
   const int cu = c < 1e9f ? (int)c + 1 : kNoSplit;
   return cu < p.min_units ? p.min_units : cu;
+}
+
+// Inclusive sum over the lanes of a wave: DPP shifts inside the rows of 16,
+// then lane 15 of a row added to the next one, lane 31 to the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return v;
 }
 
 // One item of the launch, wave-uniform; b < 0: there is none.
@@ -82,12 +93,7 @@ __device__ __forceinline__ Item find_item(const SeqView& s, const SplitRule& p, 
   for (int b0 = 0; b0 < s.B; b0 += 64) {
     const SeqRows r = seq_rows(s, b0 + lane, p.cap);
     const int ch = chunks_of(p, r, cu), n = tiles_of(p, r) * ch;
-    int inc = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(inc, d);
-      if (lane >= d) inc += v;
-    }
+    const int inc = wave_scan(n);
     const uint64_t m = __ballot(carry + inc > item);
     if (m) {
       const int l = __ffsll((unsigned long long)m) - 1;
@@ -114,9 +120,7 @@ __device__ __forceinline__ int items_before(const SeqView& s, const SplitRule& p
     const SeqRows r = seq_rows(s, b0 + lane, p.cap);
     if (b0 + lane < b) sum += tiles_of(p, r) * chunks_of(p, r, cu);
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  return sum;
+  return __builtin_amdgcn_readlane(wave_scan(sum), 63);
 }
 
 // Partial results of one part of the keys: item slots of RT rows, per row the

@@ -7,8 +7,6 @@
 // multiples of 2^-24 below fp16's normal range, so small rows stay exact), keys
 // row by row, values transposed.  fp16 and not bf16 for values and weights: the
 // roundings of both then stay an eighth of the output's own.
-#include <type_traits>
-
 #include "common.hpp"
 #include "kvcache_attend.hpp"
 
@@ -93,7 +91,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
     int ex = (int)(big >> 7) - 127;
     ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
     const float down = ldexpf(a.scale < 0.f ? -1.f : 1.f, -ex);
-    cq = ldexpf(c0, ex);
+    cq = fmaxf(ldexpf(c0, ex), 1e-37f);    // positive also for a scale of 0: -inf times it stays -inf
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       u32x4_t v;
@@ -249,23 +247,33 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
     }
   };
 
-  // Two instances of the step, so that the one without masks holds no select.
   const uint8_t* kread = ksh + col * KP + hh * 16;
   const uint8_t* vread = vsh + col * VP + hh * 16;
-  auto compute = [&](auto with_mask, int key0, int buf, uint32_t holes) {
-    constexpr bool masked = decltype(with_mask)::value;
+  auto compute = [&](int key0, int buf, uint32_t holes) {
+    const bool masked = key0 + KT > limmin || holes;
     const uint8_t* kp = kread + buf * KBUF;
     const uint8_t* vp = vread + buf * VBUF;
+    f16x8_t kf[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f16x8_t*>(kp + s * 32);
 #pragma unroll
     for (int kb = 0; kb < KT / 32; ++kb) {
       f32x16_t z;
 #pragma unroll
       for (int i = 0; i < 16; ++i) z[i] = 0.f;
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8_t*>(kp + kb * 32 * KP + s * 32), qf[s], z, 0,
-                                                   0, 0);
-      if constexpr (masked) {
+      for (int s = 0; s < STEPS; ++s) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[s], qf[s], z, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      // operands of the products to come, read while the softmax runs
+      f16x8_t vf[DT];
+#pragma unroll
+      for (int t = 0; t < DT; ++t) vf[t] = *reinterpret_cast<const f16x8_t*>(vp + t * 32 * VP + 4 * kb * 16);
+      if (kb + 1 < KT / 32) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f16x8_t*>(kp + (kb + 1) * 32 * KP + s * 32);
+      }
+      if (masked) {
+        asm volatile("");                  // a branch: the selects must not run in every step
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int k = 32 * kb + 8 * (i / 4) + 4 * hh + i % 4;
@@ -276,7 +284,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
       float mx = z[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) mx = fmaxf(mx, z[i]);
-      mx = mx == -INFINITY ? mx : mx * cq;   // a scale of 0 must not turn -inf into NaN
+      mx *= cq;
       if (__ballot(mx > m + 8.0f)) {       // the maximum may lag by 8, as in the kernel for few rows
         float v = fmaxf(mx, __shfl_xor(mx, 32));
         v = fmaxf(v, m);
@@ -293,19 +301,19 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], cq, -base));
-        if constexpr (masked) pv[i] = z[i] == -INFINITY ? 0.f : pv[i];
         l += pv[i];
       }
       u32x4_t p[2];
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e / 4][e % 4] = cvt_pk_f16(pv[2 * e], pv[2 * e + 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int t = 0; t < DT; ++t)
-          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const f16x8_t*>(vp + t * 32 * VP + (4 * kb + 2 * s) * 16),
-              __builtin_bit_cast(f16x8_t, p[s]), acc[t], 0, 0, 0);
+        for (int t = 0; t < DT; ++t) {
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[t], __builtin_bit_cast(f16x8_t, p[s]), acc[t], 0, 0, 0);
+          if (s == 0) vf[t] = *reinterpret_cast<const f16x8_t*>(vp + t * 32 * VP + (4 * kb + 2) * 16);
+        }
     }
   };
 
@@ -327,8 +335,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
 #pragma unroll
         for (int i = 0; i < NW; ++i) holes |= gone[buf][i];
         holes = __builtin_amdgcn_readfirstlane(holes);
-        if (key + KT > limmin || holes) compute(std::true_type{}, key, buf, holes);
-        else compute(std::false_type{}, key, buf, 0u);
+        compute(key, buf, holes);
       }
       if (more) decode(key + KT, r, buf ^ 1);
       __syncthreads();

@@ -133,7 +133,7 @@ def test_workspace_query(lib):
 # ---------------------------------------------------------------- binding
 def _bare():
     c = _cache()
-    c._tensors, c._device = (), torch.device("cuda", 0)
+    c._tensors, c._device, c._index = (), torch.device("cuda", 0), 0
     return c
 
 
@@ -159,7 +159,7 @@ def test_binding_checks(lib):
     refuses("K", cg.qcache_write, c, K[:, :1], K, pages, lens)
     refuses("V", cg.qcache_write, c, K, K.float(), pages, lens)
     refuses("V", cg.qcache_write, c, K, K[:2], pages, lens)
-    refuses("contiguous", cg.qcache_write, c, K.transpose(1, 2).reshape(3, 64, 2).transpose(1, 2), K, pages, lens)
+    refuses("contiguous", cg.qcache_write, c, K.transpose(1, 2).contiguous().transpose(1, 2), K, pages, lens)
     refuses("dtype", cg.qcache_write, c, K.half(), K.half(), pages, lens)
     refuses("rows", cg.qcache_read, c, pages, lens, starts)
     refuses("both", cg.qcache_read, c, pages, lens, K=K)
