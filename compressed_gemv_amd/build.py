@@ -34,6 +34,13 @@ CXXFLAGS = [
 ]
 
 
+# Flags of one file.  The cache's attention kernels use the results of most of
+# their products in vector code at once: with products that write to ordinary
+# registers those results need no move out of the accumulation registers.
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+FILE_FLAGS = {"kvcache_tile.hip": VGPR_FORM, "kvcache_attend.hip": VGPR_FORM}
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -48,7 +55,7 @@ def build(verbose: bool = False, extra_flags=(), out: str = LIB, objdir: str = N
 
     def compile_one(src):
         obj = os.path.join(objdir, src.replace(".hip", ".o"))
-        cmd = [cc, *CXXFLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [cc, *CXXFLAGS, *FILE_FLAGS.get(src, []), *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

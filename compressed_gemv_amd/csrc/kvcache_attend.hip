@@ -23,6 +23,9 @@ constexpr float kCode = 0x1p69f;                   // product of a scaled operan
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// fp16 times fp32 in one instruction (v_fma_mix_f32; a plain product would convert first)
+__device__ __forceinline__ float mix_mul(float h, float x) { return __builtin_fmaf(h, x, 0.f); }
+
 // bf16 pair times 2^64
 __device__ __forceinline__ uint32_t up_pair(uint32_t w) {
   const float lo = bf16_lo_to_f32(w) * kUp, hi = bf16_hi_to_f32(w) * kUp;
@@ -216,7 +219,9 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
     // logits; where some row of the tile does not see all of the step, what it does not see is -inf
     float t[NT][8];
     const bool masked = key + 32 > limmin || w_.bad;
-    bool vis[NT][8];
+    auto seen = [&](int n, int j) {
+      return key + 16 * (j / 4) + 4 * kg + j % 4 < lim[n] && !((w_.bad >> (j / 4)) & 1);
+    };
     bool grow = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -224,14 +229,12 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t km = w_.km[j / 4][j % 4];
-        t[n][j] = __builtin_fmaf(z[n][j / 4][j % 4], f16_lo(km) * c1, f16_hi(km) * qs[n]);
+        t[n][j] = __builtin_fmaf(z[n][j / 4][j % 4], mix_mul(f16_lo(km), c1), mix_mul(f16_hi(km), qs[n]));
       }
       if (masked) {
+        asm volatile("");                  // a branch: the selects must not run in every step
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          vis[n][j] = key + 16 * (j / 4) + 4 * kg + j % 4 < lim[n] && !((w_.bad >> (j / 4)) & 1);
-          t[n][j] = vis[n][j] ? t[n][j] : -INFINITY;
-        }
+        for (int j = 0; j < 8; ++j) t[n][j] = seen(n, j) ? t[n][j] : -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) mx = fmaxf(mx, t[n][j]);
@@ -261,19 +264,21 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float base = m[n] == -INFINITY ? 0.f : m[n] - 64.0f;
-      float p[8], wv[8];
+      uint32_t vm[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vm[j] = w_.vm[j / 4][j % 4];
+      if (masked) {                        // constants of slots that are not seen may be anything
+        asm volatile("");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vm[j] = seen(n, j) ? vm[j] : 0u;
+      }
+      float wv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t vm = w_.vm[j / 4][j % 4];
-        p[j] = exp2_hw(t[n][j] - base);    // 2^64 times the weight
-        wv[j] = p[j] * f16_lo(vm);
-        float pv = p[j] * f16_hi(vm);
-        if (masked) {                      // constants of slots that are not seen may be anything
-          wv[j] = vis[n][j] ? wv[j] : 0.f;
-          pv = vis[n][j] ? pv : 0.f;
-        }
-        l[n] += p[j];
-        po[n] += pv;
+        const float p = exp2_hw(t[n][j] - base);   // 2^64 times the weight
+        wv[j] = mix_mul(f16_lo(vm[j]), p);
+        po[n] = __builtin_fmaf(f16_hi(vm[j]), p, po[n]);
+        l[n] += p;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -7,6 +7,8 @@
 // multiples of 2^-24 below fp16's normal range, so small rows stay exact), keys
 // row by row, values transposed.  fp16 and not bf16 for values and weights: the
 // roundings of both then stay an eighth of the output's own.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kvcache_attend.hpp"
 
@@ -28,34 +30,52 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
 }
 
+// The order of a turn's instructions: after each product the vector work of one
+// logit (a fused multiply-add, an exponential, a sum, half a conversion) and a
+// read from LDS; the products then run without a pause and the vector unit
+// fills their time.
+#define KV_SCHED                                          \
+  _Pragma("unroll") for (int i_ = 0; i_ < 16; ++i_) {     \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    \
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    \
+    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);    \
+  }
+
 constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 1024, -1024
 
 }  // namespace
 
-// A workgroup: NW waves of 32 rows; 16 NW keys a step, two LDS buffers, one
-// barrier a step.  The first half of the waves decode the keys of the next
-// step, the others its values.  S^T = K Q^T on 32x32x16 products puts a row's
-// logits of 16 keys into one lane; the weights go back in as the other operand
-// of O^T = V^T P^T without leaving the lane, because V's columns are stored in
-// the order in which the lanes hold them.  LDS rows are padded by 16 bytes: 16
-// neighbouring rows then cover all banks, and every address of the inner loop
-// is one register plus a constant.  Coordinate DPT g + q of V lies in row
-// 16 q + g, so that the lanes that write it (q fixed) write neighbouring rows.
+// A workgroup: NW waves of 64 rows (two blocks of 32), one wave per SIMD with
+// all its registers; 32 NW keys a step, two LDS buffers, one barrier a step.
+// S^T = K Q^T on 32x32x16 products puts a row's logits of 16 keys into one
+// lane; the weights go back in as the other operand of O^T = V^T P^T without
+// leaving the lane, because V's columns are stored in the order in which the
+// lanes hold them.  64 rows per wave halve the LDS reads per product, which
+// otherwise cost as much time as the products; the two blocks take turns, the
+// products of one running while the vector unit does the softmax of the other:
+//   turn 1 of 32 keys:  products  O_A += V P_A (the keys before), S_A (these)
+//                       vector    softmax of S_B (the keys before)
+//   turn 2:             products  O_B += V P_B (the keys before), S_B (these)
+//                       vector    softmax of S_A (these)
+// LDS rows are padded by 16 bytes: 16 neighbouring rows then cover all banks,
+// and every address of the inner loop is one register plus a constant.
+// Coordinate DPT g + q of V lies in row 16 q + g, so that the lanes that write
+// it (q fixed) write neighbouring rows.
 template <int D, int BITS, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
-  constexpr int KT = 16 * NW;              // keys per step
+__global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
+  constexpr int KT = 32 * NW;              // keys per step
+  constexpr int KBS = KT / 32;
   constexpr int ROWB = D * BITS / 8;
   constexpr int STEPS = D / 16, DT = D / 32;
   constexpr int KP = D * 2 + 16, VP = KT * 2 + 16;   // pitch of a key's and of a coordinate's LDS row
   constexpr int KBUF = KT * KP, VBUF = D * VP;
-  constexpr int KL = ROWB / 2 / 16;        // 16-byte loads per K thread (half a row)
-  constexpr int VB = ROWB / 16;            // bytes of a value row per V thread
+  constexpr int KL = ROWB / 2 / 16;        // 16-byte loads of a thread's half key row
+  constexpr int VB = ROWB / 16;            // bytes of a value row per thread
   constexpr int VW = VB < 4 ? 1 : VB / 4;
-  constexpr int DPT = D / 16;              // coordinates per V thread
-  constexpr int CW = 4 * KL > 8 * VW ? 4 * KL : 8 * VW;
+  constexpr int DPT = D / 16;              // coordinates per thread of 8 values
   __shared__ __align__(16) uint8_t ksh[2 * KBUF];
   __shared__ __align__(16) uint8_t vsh[2 * VBUF];
-  __shared__ uint32_t gone[2][NW];         // per 16 keys: 1 << (their place) where they are not in the cache
+  __shared__ uint32_t gone[2][KT / 16];    // per 16 keys: 1 << (their place) where they are not in the cache
   const KvAttend& a = x.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
@@ -65,13 +85,15 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
 
   // queries: rows scaled by a power of two to a largest value in [1, 2) (exact
   // up to 2^-25 of it), what each row sees, and the factor back
-  f16x8_t qf[STEPS];
+  f16x8_t qf[2][STEPS];
+  float cq[2];
+  int lim[2], limmin = w.k1;
   const float c0 = fabsf(a.scale) * 1.4426950408889634f;
-  const int trow = wave * 32 + col, row = w.row0 + trow;
-  const bool ok = row < w.rows;
-  const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
-  float cq;
-  {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int row = w.row0 + wave * 64 + n * 32 + col;
+    const bool ok = row < w.rows;
+    const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
     const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D;
     u32x4_t raw[STEPS];
     uint32_t big = 0;
@@ -91,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
     int ex = (int)(big >> 7) - 127;
     ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
     const float down = ldexpf(a.scale < 0.f ? -1.f : 1.f, -ex);
-    cq = fmaxf(ldexpf(c0, ex), 1e-37f);    // positive also for a scale of 0: -inf times it stays -inf
+    cq[n] = fmaxf(ldexpf(c0, ex), 1e-37f); // positive also for a scale of 0: -inf times it stays -inf
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       u32x4_t v;
@@ -104,271 +126,302 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_tile_kernel(AttendArgs x) {
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = cvt_pk_f16(bf16_lo_to_f32(raw[s][e]) * down, bf16_hi_to_f32(raw[s][e]) * down);
-      qf[s] = __builtin_bit_cast(f16x8_t, v);
+      qf[n][s] = __builtin_bit_cast(f16x8_t, v);
     }
-  }
-  const int lim = ok ? row_sees(w, tok) : w.k1;
-  int limmin = lim, limmax = ok ? lim : 0; // over the wave's rows
+    lim[n] = ok ? row_sees(w, tok) : w.k1;
+    int lo = lim[n];                       // the least of the wave's rows
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int u = __shfl_xor(limmin, d), v = __shfl_xor(limmax, d);
-    limmin = u < limmin ? u : limmin;
-    limmax = v > limmax ? v : limmax;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_xor(lo, d);
+      lo = u < lo ? u : lo;
+    }
+    limmin = lo < limmin ? lo : limmin;
   }
   limmin = __builtin_amdgcn_readfirstlane(limmin);
-  limmax = __builtin_amdgcn_readfirstlane(limmax);
 
-  f32x16_t acc[DT];
-  float m = -INFINITY, l = 0.f;
+  f32x16_t acc[2][DT], z[2];
+  float m[2], l[2];
+  u32x4_t p[2][2];
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
+  for (int n = 0; n < 2; ++n) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[n][t][i] = 0.f;
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+    p[n][0] = p[n][1] = u32x4_t{0u, 0u, 0u, 0u};
+  }
 
-  // ---- what this thread decodes: half a key row, or 8 values of DPT coordinates
-  const bool is_k = wave < NW / 2;
-  const int dt = tid & (32 * NW - 1);
-  const int kkey = dt >> 1, khalf = dt & 1;
-  const int vchunk = dt >> 4;              // 8 keys
+  // ---- what this thread decodes: half a key row, and DPT coordinates of 8 values
+  const int kkey = tid >> 1, khalf = tid & 1;
+  const int vchunk = tid >> 4, vg = tid & 15;
   const int vkey = 16 * (vchunk >> 1) + 4 * (vchunk & 1);   // keys vkey .. + 3 and vkey + 8 .. + 3
-  const int mykey = is_k ? kkey : vkey;
-  const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
-  // byte offsets inside a page: this head's rows, this thread's part of a row
-  const uint32_t page_rows = (uint32_t)heads << shift;
-  const uint32_t head_row = (uint32_t)h << shift;
-  const uint32_t my_off = is_k ? khalf * (ROWB / 2) : (dt & 15) * VB;
-  auto page_of = [&](int key0) -> int {    // page of this thread's keys of the step at key0
-    const int key = key0 + (is_k ? kkey : vkey & ~15);
+  const int shift = a.c.page_shift;
+  const uint32_t pmask = (1u << shift) - 1u;
+  const uint32_t page_rows = (uint32_t)heads << shift, head_row = (uint32_t)h << shift;
+  auto page_of = [&](int key) -> int {
     if (key >= w.k1 || (key >> shift) >= w.max_pages) return -1;
     const int id = w.pages[key >> shift];
     return id < a.c.n_pages ? id : -1;
   };
   struct Codes {
-    uint32_t c[CW];
-    uint32_t meta[8];                      // K: own key's constants of K and V; V: those of the 8 keys
-    int page;
+    u32x4_t k[KL];
+    uint32_t v[8][VW];
+    uint32_t km, kvm;                      // the key's constants of K and of V
+    u32x4_t vm[2];
+    int kpage, vpage;
   };
-  auto load = [&](int key0, int page, Codes& r) {
-    r.page = page;
-    const uint32_t in_page = head_row + ((uint32_t)(key0 + mykey) & (uint32_t)pmask);
-    const uint64_t prow = (uint64_t)(uint32_t)(page < 0 ? 0 : page) * page_rows + in_page;
-    if (is_k) {
-      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(a.c.codes[0] + prow * ROWB + my_off);
+  int kpage = page_of(w.k0 + kkey), vpage = page_of(w.k0 + (vkey & ~15));   // of the step to be loaded next
+  auto load = [&](int key0, Codes& r) {
+    r.kpage = kpage;
+    r.vpage = vpage;
+    const uint64_t krow = (uint64_t)(uint32_t)(kpage < 0 ? 0 : kpage) * page_rows + (head_row + ((uint32_t)(key0 + kkey) & pmask));
+    const uint64_t vrow = (uint64_t)(uint32_t)(vpage < 0 ? 0 : vpage) * page_rows + (head_row + ((uint32_t)(key0 + vkey) & pmask));
+    const u32x4_t* kp = reinterpret_cast<const u32x4_t*>(a.c.codes[0] + krow * ROWB + khalf * (ROWB / 2));
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const u32x4_t v = p[i];
+    for (int i = 0; i < KL; ++i) r.k[i] = kp[i];
+    r.km = a.c.meta[0][krow];
+    r.kvm = a.c.meta[1][krow];
+    const uint8_t* vp = a.c.codes[1] + vrow * ROWB + vg * VB;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r.c[4 * i + e] = v[e];
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* pj = vp + ((j & 3) + 8 * (j >> 2)) * ROWB;
+      if constexpr (VB == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(pj);
+        r.v[j][0] = v.x;
+        r.v[j][1 % VW] = v.y;
+      } else if constexpr (VB == 4) {
+        r.v[j][0] = *reinterpret_cast<const uint32_t*>(pj);
+      } else {
+        r.v[j][0] = *reinterpret_cast<const uint16_t*>(pj);
       }
-      r.meta[0] = a.c.meta[0][prow];
-      r.meta[1] = a.c.meta[1][prow];
-    } else {
-      const uint8_t* p = a.c.codes[1] + prow * ROWB + my_off;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* pj = p + ((j & 3) + 8 * (j >> 2)) * ROWB;
-        if constexpr (VB == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(pj);
-          r.c[2 * j] = v.x;
-          r.c[(2 * j + 1) % CW] = v.y;
-        } else if constexpr (VB == 4) {
-          r.c[j] = *reinterpret_cast<const uint32_t*>(pj);
-        } else {
-          r.c[j] = *reinterpret_cast<const uint16_t*>(pj);
-        }
-      }
-      const uint32_t* mp = a.c.meta[1] + prow;
-      const u32x4_t m0 = *reinterpret_cast<const u32x4_t*>(mp), m1 = *reinterpret_cast<const u32x4_t*>(mp + 8);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) { r.meta[e] = m0[e]; r.meta[4 + e] = m1[e]; }
     }
+    const uint32_t* mp = a.c.meta[1] + vrow;
+    r.vm[0] = *reinterpret_cast<const u32x4_t*>(mp);
+    r.vm[1] = *reinterpret_cast<const u32x4_t*>(mp + 8);
+    kpage = page_of(key0 + KT + kkey);
+    vpage = page_of(key0 + KT + (vkey & ~15));
   };
   // A value row that is NaN is decoded as zeros and makes its key NaN instead,
   // so it reaches exactly the rows whose mask lets them see it; constants of
   // keys that no row sees become zero.
   auto nan_meta = [](uint32_t mt) { return (mt & 0x7C00u) == 0x7C00u; };
-  auto decode = [&](int key0, const Codes& r, int buf) {
-    if (is_k) {
-      uint32_t mt = r.page < 0 || key0 + kkey >= w.k1 ? 0u : (nan_meta(r.meta[1]) ? 0x7E007E00u : r.meta[0]);
-      const uint32_t s2 = __builtin_amdgcn_perm(mt, mt, 0x01000100u), o2 = __builtin_amdgcn_perm(mt, mt, 0x03020302u);
+  auto decode_k = [&](int key0, const Codes& r, int buf) {
+    const uint32_t mt = r.kpage < 0 || key0 + kkey >= w.k1 ? 0u : (nan_meta(r.kvm) ? 0x7E007E00u : r.km);
+    const uint32_t s2 = __builtin_amdgcn_perm(mt, mt, 0x01000100u), o2 = __builtin_amdgcn_perm(mt, mt, 0x03020302u);
+    uint8_t* out = ksh + buf * KBUF + kkey * KP + khalf * D;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        u32x4_t v;
-        if constexpr (BITS == 8) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            v[2 * e] = __builtin_amdgcn_perm(k1024, r.c[2 * i + e], 0x05010500u);
-            v[2 * e + 1] = __builtin_amdgcn_perm(k1024, r.c[2 * i + e], 0x05030502u);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = ((r.c[i] >> (4 * e)) & 0x000F000Fu) | k1024;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = pk_fma(pk_add(v[e], kM1024), s2, o2);
-        *reinterpret_cast<u32x4_t*>(ksh + buf * KBUF + kkey * KP + khalf * D + i * 16) = v;
-      }
-      if (khalf == 0 && (kkey & 15) == 0) gone[buf][kkey >> 4] = r.page < 0 ? 1u << (kkey >> 4) : 0u;
-    } else {
-      uint32_t s2[4], o2[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        uint32_t mt[2];
+    for (int i = 0; i < D / 16; ++i) {
+      u32x4_t v;
+      if constexpr (BITS == 8) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = 2 * p + e;
-          const uint32_t t = r.meta[j];
-          mt[e] = r.page < 0 || key0 + vkey + (j & 3) + 8 * (j >> 2) >= w.k1 || nan_meta(t) ? 0u : t;
+          const uint32_t c = r.k[(2 * i + e) / 4][(2 * i + e) % 4];
+          v[2 * e] = __builtin_amdgcn_perm(k1024, c, 0x05010500u);
+          v[2 * e + 1] = __builtin_amdgcn_perm(k1024, c, 0x05030502u);
         }
-        s2[p] = __builtin_amdgcn_perm(mt[1], mt[0], 0x05040100u);
-        o2[p] = __builtin_amdgcn_perm(mt[1], mt[0], 0x07060302u);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = ((r.k[i / 4][i % 4] >> (4 * e)) & 0x000F000Fu) | k1024;
       }
-      uint32_t half[4] = {0u, 0u, 0u, 0u};
-      uint8_t* vout = vsh + buf * VBUF + (dt & 15) * VP + vchunk * 16;
 #pragma unroll
-      for (int d = 0; d < DPT; ++d) {
-        u32x4_t v;
+      for (int e = 0; e < 4; ++e) v[e] = pk_fma(pk_add(v[e], kM1024), s2, o2);
+      *reinterpret_cast<u32x4_t*>(out + i * 16) = v;
+    }
+    if (khalf == 0 && (kkey & 15) == 0) gone[buf][kkey >> 4] = r.kpage < 0 ? 1u << (kkey >> 4) : 0u;
+  };
+  auto decode_v = [&](int key0, const Codes& r, int buf) {
+    uint32_t s2[4], o2[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t u;
-          if constexpr (BITS == 8) {       // two coordinates of both keys, then one with the exponent of 1024
-            if (d % 2 == 0)
-              half[p] = __builtin_amdgcn_perm(r.c[(2 * p + 1) * VW + d / 4], r.c[2 * p * VW + d / 4],
-                                              d % 4 == 0 ? 0x05010400u : 0x07030602u);
-            u = __builtin_amdgcn_perm(k1024, half[p], d % 2 == 0 ? 0x05010500u : 0x05030502u);
-          } else {
-            if (d % 4 == 0) half[p] = __builtin_amdgcn_perm(r.c[2 * p + 1], r.c[2 * p], d == 0 ? 0x05040100u : 0x07060302u);
-            u = ((half[p] >> (4 * (d % 4))) & 0x000F000Fu) | k1024;
-          }
-          v[p] = pk_fma(pk_add(u, kM1024), s2[p], o2[p]);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t mt[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * q + e;
+        const uint32_t t = r.vm[j / 4][j % 4];
+        mt[e] = r.vpage < 0 || key0 + vkey + (j & 3) + 8 * (j >> 2) >= w.k1 || nan_meta(t) ? 0u : t;
+      }
+      s2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x05040100u);
+      o2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x07060302u);
+    }
+    uint32_t half[4] = {0u, 0u, 0u, 0u};
+    uint8_t* out = vsh + buf * VBUF + vg * VP + vchunk * 16;
+#pragma unroll
+    for (int d = 0; d < DPT; ++d) {
+      u32x4_t v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u;
+        if constexpr (BITS == 8) {         // two coordinates of both keys, then one with the exponent of 1024
+          if (d % 2 == 0)
+            half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][d / 4], r.v[2 * q][d / 4], d % 4 == 0 ? 0x05010400u : 0x07030602u);
+          u = __builtin_amdgcn_perm(k1024, half[q], d % 2 == 0 ? 0x05010500u : 0x05030502u);
+        } else {
+          if (d % 4 == 0) half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][0], r.v[2 * q][0], d == 0 ? 0x05040100u : 0x07060302u);
+          u = ((half[q] >> (4 * (d % 4))) & 0x000F000Fu) | k1024;
         }
-        *reinterpret_cast<u32x4_t*>(vout + 16 * d * VP) = v;
+        v[q] = pk_fma(pk_add(u, kM1024), s2[q], o2[q]);
       }
+      *reinterpret_cast<u32x4_t*>(out + 16 * d * VP) = v;
     }
   };
 
   const uint8_t* kread = ksh + col * KP + hh * 16;
   const uint8_t* vread = vsh + col * VP + hh * 16;
-  auto compute = [&](int key0, int buf, uint32_t holes) {
-    const bool masked = key0 + KT > limmin || holes;
-    const uint8_t* kp = kread + buf * KBUF;
-    const uint8_t* vp = vread + buf * VBUF;
-    f16x8_t kf[STEPS];
+  f16x8_t kf[STEPS], vf[2][DT];
+  auto read_k = [&](int buf, int kb) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f16x8_t*>(kp + s * 32);
+    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f16x8_t*>(kread + buf * KBUF + kb * 32 * KP + s * 32);
+  };
+  auto read_v = [&](int buf, int kb) {
 #pragma unroll
-    for (int kb = 0; kb < KT / 32; ++kb) {
-      f32x16_t z;
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[s], qf[s], z, 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      // operands of the products to come, read while the softmax runs
-      f16x8_t vf[DT];
-#pragma unroll
-      for (int t = 0; t < DT; ++t) vf[t] = *reinterpret_cast<const f16x8_t*>(vp + t * 32 * VP + 4 * kb * 16);
-      if (kb + 1 < KT / 32) {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f16x8_t*>(kp + (kb + 1) * 32 * KP + s * 32);
-      }
-      if (masked) {
-        asm volatile("");                  // a branch: the selects must not run in every step
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = 32 * kb + 8 * (i / 4) + 4 * hh + i % 4;
-          const bool vis = key0 + k < lim && !((holes >> (2 * kb + i / 8)) & 1u);
-          z[i] = vis ? z[i] : -INFINITY;
-        }
-      }
-      float mx = z[0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) mx = fmaxf(mx, z[i]);
-      mx *= cq;
-      if (__ballot(mx > m + 8.0f)) {       // the maximum may lag by 8, as in the kernel for few rows
-        float v = fmaxf(mx, __shfl_xor(mx, 32));
-        v = fmaxf(v, m);
-        const float f = v == m ? 1.0f : __builtin_amdgcn_exp2f(m - v);
-        m = v;
-        l *= f;
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[t][i] *= f;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      float pv[16];
+      for (int t = 0; t < DT; ++t)
+        vf[s][t] = *reinterpret_cast<const f16x8_t*>(vread + buf * VBUF + t * 32 * VP + (4 * kb + 2 * s) * 16);
+  };
+  // masks and the maximum of one block's logits (keys key .. key + 31)
+  auto bounds = [&](auto blk, int key, uint32_t holes) {
+    constexpr int n = decltype(blk)::value;
+    if (key + 32 > limmin || holes) {
+      asm volatile("");                    // a branch: the selects must not run in every step
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], cq, -base));
-        l += pv[i];
+        const bool vis = key + 8 * (i / 4) + 4 * hh + i % 4 < lim[n] && !((holes >> (i / 8)) & 1u);
+        z[n][i] = vis ? z[n][i] : -INFINITY;
       }
-      u32x4_t p[2];
+    }
+    float mx = z[n][0];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e / 4][e % 4] = cvt_pk_f16(pv[2 * e], pv[2 * e + 1]);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, z[n][i]);
+    mx *= cq[n];
+    if (__ballot(mx > m[n] + 8.0f)) {      // the maximum may lag by 8, as in the kernel for few rows
+      float v = fmaxf(mx, __shfl_xor(mx, 32));
+      v = fmaxf(v, m[n]);
+      const float f = v == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - v);
+      m[n] = v;
+      l[n] *= f;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[t], __builtin_bit_cast(f16x8_t, p[s]), acc[t], 0, 0, 0);
-          if (s == 0) vf[t] = *reinterpret_cast<const f16x8_t*>(vp + t * 32 * VP + (4 * kb + 2) * 16);
-        }
+        for (int i = 0; i < 16; ++i) acc[n][t][i] *= f;
     }
   };
+  // One turn: the softmax of block S against the products of the other block.
+  // READS: the operands for what follows, fetched as the products release them.
+  auto turn = [&](auto soft, auto&& after_pv, auto&& after_s) {
+    constexpr int n = decltype(soft)::value, o = 1 - n;
+    const float base = m[n] == -INFINITY ? 0.f : m[n];
+    float pv[16];
+    f32x16_t zn;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zn[i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+        acc[o][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], __builtin_bit_cast(f16x8_t, p[o][s]), acc[o][t], 0, 0, 0);
+    after_pv();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) zn = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[s], qf[o][s], zn, 0, 0, 0);
+    after_s();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq[n], -base));
+      l[n] += pv[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[n][e / 4][e % 4] = cvt_pk_f16(pv[2 * e], pv[2 * e + 1]);
+    z[o] = zn;
+    // the weights are made here, not where they are used one turn later
+    asm volatile("" : "+v"(p[n][0]), "+v"(p[n][1]), "+v"(l[n]));
+    KV_SCHED
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using A = std::integral_constant<int, 0>;
+  using B = std::integral_constant<int, 1>;
+  auto none = [] {};
 
   if (w.k0 < w.k1) {                       // workgroup-uniform
     Codes r;
-    load(w.k0, page_of(w.k0), r);
-    int next = page_of(w.k0 + KT);
-    decode(w.k0, r, 0);
+    load(w.k0, r);
+    decode_k(w.k0, r, 0);
+    decode_v(w.k0, r, 0);
+    if (w.k0 + KT < w.k1) load(w.k0 + KT, r);
     __syncthreads();
-    int buf = 0;
-    for (int key = w.k0; key < w.k1; key += KT) {
-      const bool more = key + KT < w.k1;
-      if (more) {
-        load(key + KT, next, r);
-        next = page_of(key + 2 * KT);
-      }
-      if (key < limmax) {
-        uint32_t holes = 0;
+    // before the first keys: weights of zero, logits that add nothing
 #pragma unroll
-        for (int i = 0; i < NW; ++i) holes |= gone[buf][i];
-        holes = __builtin_amdgcn_readfirstlane(holes);
-        compute(key, buf, holes);
+    for (int i = 0; i < 16; ++i) z[0][i] = z[1][i] = -INFINITY;
+    read_k(0, 0);
+    read_v(0, 0);
+    int buf = 0, prev_holes = 0;
+    for (int key = w.k0; key < w.k1; key += KT, buf ^= 1) {
+      uint32_t holes = 0;
+#pragma unroll
+      for (int i = 0; i < KT / 16; ++i) holes |= gone[buf][i];
+      holes = __builtin_amdgcn_readfirstlane(holes);
+      const bool more = key + KT < w.k1;
+#pragma unroll
+      for (int kb = 0; kb < KBS; ++kb) {
+        const int k = key + 32 * kb;
+        bounds(B{}, k - 32, kb == 0 ? (uint32_t)prev_holes : (holes >> (2 * kb - 2)) & 3u);
+        turn(B{}, none, none);             // softmax B (before); O_A, S_A
+        bounds(A{}, k, (holes >> (2 * kb)) & 3u);
+        turn(A{}, [&] { read_v(buf, kb); }, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); });
+        if (kb == KBS - 2 && more) decode_k(key + KT, r, buf ^ 1);
+        if (kb == KBS - 1 && more) {
+          decode_v(key + KT, r, buf ^ 1);
+          if (key + 2 * KT < w.k1) load(key + 2 * KT, r);
+        }
       }
-      if (more) decode(key + KT, r, buf ^ 1);
+      prev_holes = (int)((holes >> (2 * KBS - 2)) & 3u);
       __syncthreads();
-      buf ^= 1;
+      if (more) read_k(buf ^ 1, 0);
     }
+    // what is left: the last keys' products and block B's softmax
+    const int last = w.k0 + (w.k1 - w.k0 + KT - 1) / KT * KT - 32;
+    bounds(B{}, last, (uint32_t)prev_holes);
+    turn(B{}, none, none);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+        acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], __builtin_bit_cast(f16x8_t, p[1][s]), acc[1][t], 0, 0, 0);
   }
 
   // Register i of tile t is LDS row 32 t + 8 (i / 4) + 4 hh + i % 4 of V: with
   // i = 4 e + j, coordinate DPT (8 (e % 2) + 4 hh + j) + 2 t + e / 2.  For one
   // (e % 2, j) a lane holds DPT neighbouring coordinates.
-  l += __shfl_xor(l, 32);
-  if (!ok) return;
-  const float inv = w.direct ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;
-  const int64_t at = (int64_t)(w.t0 + tok) * a.o_stride + (int64_t)(h * a.group + g) * D;
-  float* po = w.direct ? nullptr : part_o<D>(x, w.slot, h, trow);
 #pragma unroll
-  for (int e0 = 0; e0 < 2; ++e0)
+  for (int n = 0; n < 2; ++n) {
+    l[n] += __shfl_xor(l[n], 32);
+    const int trow = wave * 64 + n * 32 + col, row = w.row0 + trow;
+    if (row >= w.rows) continue;
+    const int tok = row / a.group, g = row - tok * a.group;
+    const float inv = w.direct ? (l[n] == 0.f ? 0.f : 1.0f / l[n]) : 1.0f;
+    const int64_t at = (int64_t)(w.t0 + tok) * a.o_stride + (int64_t)(h * a.group + g) * D;
+    float* po = w.direct ? nullptr : part_o<D>(x, w.slot, h, trow);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d0 = DPT * (8 * e0 + 4 * hh + j);
+    for (int e0 = 0; e0 < 2; ++e0)
 #pragma unroll
-      for (int q = 0; q < DPT; q += 4) {
-        f32x4_t v;
+      for (int j = 0; j < 4; ++j) {
+        const int d0 = DPT * (8 * e0 + 4 * hh + j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = acc[(q + i) / 2][4 * (e0 + 2 * ((q + i) % 2)) + j] * inv;
-        if (w.direct) store_out4(a, at + d0 + q, v);
-        else *reinterpret_cast<f32x4_t*>(po + d0 + q) = v;
+        for (int q = 0; q < DPT; q += 4) {
+          f32x4_t v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = acc[n][(q + i) / 2][4 * (e0 + 2 * ((q + i) % 2)) + j] * inv;
+          if (w.direct) store_out4(a, at + d0 + q, v);
+          else *reinterpret_cast<f32x4_t*>(po + d0 + q) = v;
+        }
       }
+    if (!w.direct && hh == 0) {
+      float* ml = part_ml(x, w.slot, h, trow);
+      ml[0] = m[n];
+      ml[1] = l[n];
     }
-  if (!w.direct && hh == 0) {
-    float* ml = part_ml(x, w.slot, h, trow);
-    ml[0] = m;
-    ml[1] = l;
   }
 }
 
@@ -377,8 +430,8 @@ hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, int64_t 
 #define TILE(D, B, N) hipLaunchKernelGGL((kv_tile_kernel<D, B, N>), grid, dim3(64 * N), 0, st, x)
 #define TILE_N(D, B)                     \
   do {                                   \
-    if (x.rule.rt == 128) TILE(D, B, 4); \
-    else TILE(D, B, 8);                  \
+    if (x.rule.rt == 128) TILE(D, B, 2); \
+    else TILE(D, B, 4);                  \
   } while (0)
   if (head_dim == 128) {
     if (bits == 8) TILE_N(128, 8);
