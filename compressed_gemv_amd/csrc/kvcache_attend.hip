@@ -39,15 +39,15 @@ __device__ __forceinline__ V ld_nt(const uint8_t* base, uint32_t off) {
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// One workgroup: one item of 16 NT rows.  Its four waves take a quarter of the
-// chunk's keys each, 32 keys a step.  Lane l, r = l % 16, kg = l / 16:
+// A workgroup goes through the tiles (16 NT rows) of its piece; its four waves
+// take a quarter of a tile's keys each, 32 keys a step.  Lane l, r = l % 16, kg = l / 16:
 //   K operand: key r, a quarter kg of the coordinates, straight from memory
 //   logits:    query r, keys 4 kg .. 4 kg + 3 of both halves of the step
 //   V operand: coordinates r D/16 .. of exactly those eight keys (the order of
 //              the contraction is free), so the weights never leave their lane
 // The row constants of a lane's eight keys come with four 16-byte loads.
 template <int D, int BITS, int NT>
-__global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
+__global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(AttendArgs x) {
   constexpr int RT = 16 * NT;
   constexpr int ROWB = D * BITS / 8;       // bytes of a cache row
   constexpr int KB = ROWB / 4;             // bytes of a K row per lane
@@ -61,10 +61,10 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
   const KvAttend& a = x.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
-  const int heads = a.c.heads, h = blockIdx.x % heads, item = blockIdx.x / heads;
-  const Work w = work_of(x, item, lane);
-  if (w.b < 0) return;
-
+  const int heads = a.c.heads, h = blockIdx.x % heads;
+  Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
+  Work w;
+  while (next_work(x, pieces, w, lane)) {
   f32x4_t acc[NT][TILES];
   float m[NT], l[NT], po[NT];              // maximum, sum of weights, sum of weights times offsets
 #pragma unroll
@@ -376,117 +376,186 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(AttendArgs x) {
       }
     }
   }
+  __syncthreads();                         // LDS is free for the next tile
+  }
 }
 
 // ------------------------------------------------------------------- join
-// out = sum_c 2^(m_c - M) o_c over sum_c 2^(m_c - M) l_c, c the chunks of the
-// prefix (if any) and of the row's own keys.  All latency: D / 4 lanes hold a
-// row, and a lane group takes its chunks in batches of 8 with all their loads
-// in flight at once.  WAVES waves work on one (row, query head): 4 where there
-// are few rows, each with many chunks, 1 where there are many.
-template <int D, int WAVES>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttendArgs own, AttendArgs pre) {
-  constexpr int LPR = D / 4, GRP = 64 * WAVES / LPR, BATCH = 8;
-  __shared__ __align__(16) float os[WAVES][D];
-  __shared__ float mls[WAVES][2];
-  const KvAttend& a = own.a;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cu = split_units(a.s, own.rule, lane);
-  if (!own.shared && cu == kNoSplit) return;
-  const int Hq = a.c.heads * a.group;
-  const int grp = (WAVES == 4 ? threadIdx.x : lane) / LPR, sub = lane % LPR;
-  const int64_t step = (int64_t)gridDim.x * (4 / WAVES);
-  for (int64_t idx = (int64_t)blockIdx.x * (4 / WAVES) + (WAVES == 4 ? 0 : wave); idx < (int64_t)a.s.T * Hq; idx += step) {
-    // uniform over the WAVES waves of the row
-    const int t = (int)(idx / Hq), hq = (int)(idx % Hq), h = hq / a.group, g = hq - h * a.group;
-    int b = t;
-    if (a.s.starts) b = find_seq<64>(a.s.starts, a.s.B, t, lane, lane);
-    const SeqRows r = seq_rows(a.s, b, own.rule.cap);
-    if (t < r.t0 || t >= r.t0 + r.count) continue;
-    const int chunks = chunks_of(own.rule, r, cu);
-    if (!own.shared && chunks == 1) continue;
-    const int R = (t - r.t0) * a.group + g;
-    const int slot = items_before(a.s, own.rule, cu, b, lane) + R / own.rule.rt * chunks, row = R % own.rule.rt;
-    if (slot + chunks > own.part.slots) continue;
-    const int P = t * a.group + g, np = own.shared ? pre.prefix_chunks : 0;
-    const int pslot = own.shared ? P / pre.rule.rt * np : 0, prow = own.shared ? P % pre.rule.rt : 0;
-    const int n = np + chunks;
-    float M = -INFINITY, L = 0.f;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = grp; c0 < n; c0 += GRP * BATCH) {
-      float mc[BATCH], lc[BATCH];
-      f32x4_t o[BATCH];
+// out = sum_c 2^(m_c - M) o_c over sum_c 2^(m_c - M) l_c, c the parts of a row.
+// All latency: D / 4 lanes hold a row, and a lane group takes its parts in
+// batches of 8 with all their loads in flight at once.
+struct RowSum {
+  float M, L;
+  f32x4_t acc;
+};
+
+__device__ __forceinline__ void join2(RowSum& a, float M2, float L2, const f32x4_t& a2) {
+  const float mm = fmaxf(a.M, M2);
+  const float f = a.M == -INFINITY ? 0.f : exp2_hw(a.M - mm), f2 = M2 == -INFINITY ? 0.f : exp2_hw(M2 - mm);
+  a.L = a.L * f + L2 * f2;
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int c = c0 + i * GRP;
-        mc[i] = -INFINITY;
-        lc[i] = 0.f;
-        o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if (c < n) {
-          const bool p = c < np;
-          const float* ml = p ? part_ml(pre, pslot + c, h, prow) : part_ml(own, slot + c - np, h, row);
-          const float* src = p ? part_o<D>(pre, pslot + c, h, prow) : part_o<D>(own, slot + c - np, h, row);
-          const float2 v = *reinterpret_cast<const float2*>(ml);
-          mc[i] = v.x;
-          lc[i] = v.y;
-          o[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * sub);
-        }
+  for (int k = 0; k < 4; ++k) a.acc[k] = a.acc[k] * f + a2[k] * f2;
+  a.M = mm;
+}
+
+// Parts first, first + step, ... below n of one row; at(c): the partials and slot of part c, and the row in it.
+template <int D, typename AT>
+__device__ __forceinline__ RowSum sum_parts(AT at, int first, int step, int n, int h, int sub) {
+  constexpr int BATCH = 8;
+  RowSum s{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  for (int c0 = first; c0 < n; c0 += step * BATCH) {
+    float mc[BATCH], lc[BATCH];
+    f32x4_t o[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int c = c0 + i * step;
+      mc[i] = -INFINITY;
+      lc[i] = 0.f;
+      o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (c < n) {
+        const AttendArgs* x;
+        int slot, row;
+        at(c, x, slot, row);
+        const float2 v = *reinterpret_cast<const float2*>(part_ml(*x, slot, h, row));
+        mc[i] = v.x;
+        lc[i] = v.y;
+        o[i] = *reinterpret_cast<const f32x4_t*>(part_o<D>(*x, slot, h, row) + 4 * sub);
       }
-      float mb = M;
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) mb = fmaxf(mb, mc[i]);
-      const float f0 = M == -INFINITY ? 0.f : exp2_hw(M - mb);
-      L *= f0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] *= f0;
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const float f = mc[i] == -INFINITY ? 0.f : exp2_hw(mc[i] - mb);
-        L += lc[i] * f;                    // a NaN sum (a NaN key was seen) stays one
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(o[i][k], f, acc[k]);
-      }
-      M = mb;
     }
-    // the groups of the wave, then the waves
-    auto join2 = [&](float M2, float L2, const f32x4_t& a2) {
-      const float mm = fmaxf(M, M2);
-      const float f = M == -INFINITY ? 0.f : exp2_hw(M - mm), f2 = M2 == -INFINITY ? 0.f : exp2_hw(M2 - mm);
-      L = L * f + L2 * f2;
+    float mb = s.M;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f + a2[k] * f2;
-      M = mm;
-    };
+    for (int i = 0; i < BATCH; ++i) mb = fmaxf(mb, mc[i]);
+    const float f0 = s.M == -INFINITY ? 0.f : exp2_hw(s.M - mb);
+    s.L *= f0;
 #pragma unroll
-    for (int d = LPR; d < 64; d <<= 1) {
-      f32x4_t a2;
+    for (int k = 0; k < 4; ++k) s.acc[k] *= f0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a2[k] = __shfl_xor(acc[k], d);
-      join2(__shfl_xor(M, d), __shfl_xor(L, d), a2);
+    for (int i = 0; i < BATCH; ++i) {
+      const float f = mc[i] == -INFINITY ? 0.f : exp2_hw(mc[i] - mb);
+      s.L += lc[i] * f;                    // a NaN sum (a NaN key was seen) stays one
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s.acc[k] = __builtin_fmaf(o[i][k], f, s.acc[k]);
     }
-    if constexpr (WAVES > 1) {
-      if (lane < LPR) *reinterpret_cast<f32x4_t*>(&os[wave][4 * sub]) = acc;
-      if (lane == 0) { mls[wave][0] = M; mls[wave][1] = L; }
+    s.M = mb;
+  }
+  return s;
+}
+
+// Joins the lane groups of a wave; every lane then holds the wave's sum.
+template <int D>
+__device__ __forceinline__ void join_groups(RowSum& s) {
+#pragma unroll
+  for (int d = D / 4; d < 64; d <<= 1) {
+    f32x4_t a2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a2[k] = __shfl_xor(s.acc[k], d);
+    join2(s, __shfl_xor(s.M, d), __shfl_xor(s.L, d), a2);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const KvAttend& a, const SeqRows& r, int R, int h, int sub, const RowSum& s) {
+  const int tok = R / a.group, g = R - tok * a.group;
+  const float inv = s.L == 0.f ? 0.f : 1.0f / s.L;
+  f32x4_t v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = s.acc[k] * inv;
+  store_out4(a, (int64_t)(r.t0 + tok) * a.o_stride + (int64_t)(h * a.group + g) * D + 4 * sub, v);
+}
+
+// The tiles that cuts go through: one workgroup per cut and KV head, the cuts
+// of one tile share its rows.  With few parts a wave joins a row; with many
+// (few rows then, one long sequence) all four waves do.
+template <int D>
+__global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
+  constexpr int LPR = D / 4, GRP = 64 / LPR;
+  __shared__ __align__(16) float os[4][D];
+  __shared__ float mls[4][2];
+  const KvAttend& a = x.a;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPR;
+  const int h = blockIdx.x % a.c.heads, i = blockIdx.x / a.c.heads + 1;
+  const Line line = line_of(x.s, x.rule, lane);
+  if (i >= line.N) return;
+  const int64_t cut = line.cut(i);
+  const TileAt t = tile_at(x.s, x.rule, cut, lane);
+  if (t.b < 0 || t.lo == cut) return;
+  const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
+  const int slot0 = (int)slot_of(line, t, i0, false);
+  if (2 * (i0 + parts) > x.part.slots) return;
+  const int row0 = t.tile * x.rule.rt, rows = t.r.count * a.group - row0, n = rows < x.rule.rt ? rows : x.rule.rt;
+  const int k = i - i0 - 1, sharers = parts - 1;
+  if (parts >= 16) {
+    for (int row = k; row < n; row += sharers) {           // workgroup-uniform
+      auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
+        px = &x;
+        slot = c == 0 ? slot0 : 2 * (i0 + c);
+        r = row;
+      };
+      RowSum s = sum_parts<D>(at, wave * GRP + lane / LPR, 4 * GRP, parts, h, sub);
+      join_groups<D>(s);
+      if (lane < LPR) *reinterpret_cast<f32x4_t*>(&os[wave][4 * sub]) = s.acc;
+      if (lane == 0) { mls[wave][0] = s.M; mls[wave][1] = s.L; }
       __syncthreads();
-      if (wave == 0) {
+      if (wave == 0 && lane < LPR) {
 #pragma unroll
-        for (int w2 = 1; w2 < WAVES; ++w2)
-          join2(mls[w2][0], mls[w2][1], *reinterpret_cast<const f32x4_t*>(&os[w2][4 * sub]));
+        for (int w = 1; w < 4; ++w) join2(s, mls[w][0], mls[w][1], *reinterpret_cast<const f32x4_t*>(&os[w][4 * sub]));
+        store_row<D>(a, t.r, row0 + row, h, sub, s);
       }
       __syncthreads();
     }
-    if (lane < LPR && (WAVES == 1 || wave == 0)) {
-      const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] *= inv;
-      store_out4(a, (int64_t)t * a.o_stride + (int64_t)hq * D + 4 * sub, acc);
+  } else {
+    for (int row = 4 * k + wave; row < n; row += 4 * sharers) {
+      auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
+        px = &x;
+        slot = c == 0 ? slot0 : 2 * (i0 + c);
+        r = row;
+      };
+      RowSum s = sum_parts<D>(at, lane / LPR, GRP, parts, h, sub);
+      join_groups<D>(s);
+      if (lane < LPR) store_row<D>(a, t.r, row0 + row, h, sub, s);
     }
   }
 }
 
+// Every row's own parts and its prefix's: workgroups of `rpw` rows of a tile, a wave per row.
+template <int D>
+__global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, AttendArgs pre, int rpw) {
+  constexpr int LPR = D / 4, GRP = 64 / LPR;
+  const KvAttend& a = own.a;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPR;
+  const int per_tile = own.rule.rt / rpw;
+  const int h = blockIdx.x % a.c.heads, u = blockIdx.x / a.c.heads;
+  const TileAt t = tile_at<true>(own.s, own.rule, u / per_tile, lane);
+  if (t.b < 0) return;
+  const int row0 = t.tile * own.rule.rt, rows = t.r.count * a.group;
+  const int first = row0 + u % per_tile * rpw;
+  if (first >= rows) return;
+  const Line line = line_of(own.s, own.rule, lane), pline = line_of(pre.s, pre.rule, lane);
+  const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
+  const int slot0 = (int)(i0 + t.index);
+  if (slot0 + parts > own.part.slots) return;
+  const int A = weights_of(pre.rule, seq_rows(pre.s, 0, pre.rule.cap)).A;   // of every tile of the prefix
+  const int last = first + rpw < rows ? first + rpw : rows;
+  for (int R = first + wave; R < last; R += 4) {
+    const int64_t P = (int64_t)t.r.t0 * a.group + R;
+    const int pt = (int)(P / pre.rule.rt), prow = (int)(P % pre.rule.rt);
+    const int p0 = pline.piece((int64_t)A * pt), np = pline.piece((int64_t)A * (pt + 1) - 1) - p0 + 1;
+    if (p0 + pt + np > pre.part.slots) continue;
+    auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
+      const bool p = c < np;
+      px = p ? &pre : &own;
+      slot = p ? p0 + pt + c : slot0 + c - np;
+      r = p ? prow : R - row0;
+    };
+    RowSum s = sum_parts<D>(at, lane / LPR, GRP, np + parts, h, sub);
+    join_groups<D>(s);
+    if (lane < LPR) store_row<D>(a, t.r, R, h, sub, s);
+  }
+}
+
 // ------------------------------------------------------------------ launch
-hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st) {
-  const dim3 grid((unsigned)(items * x.a.c.heads));
+hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
+  const dim3 grid((unsigned)(x.rule.wgs * x.a.c.heads));
 #define ROWS(D, B, N) hipLaunchKernelGGL((kv_rows_kernel<D, B, N>), grid, dim3(256), 0, st, x)
 #define ROWS_N(D, B)                   \
   do {                                 \
@@ -507,56 +576,53 @@ hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, int64_t i
 
 namespace {
 
-constexpr int kWorkgroups = 1024;   // items aimed at in all: 4 workgroups of 4 waves for each of 256 CUs
-constexpr int kTileWorkgroups = 512;
-constexpr int kJoinGrid = 4096;      // workgroups of the join at most; each takes rows in turn
-constexpr int kJoinFew = 1024;       // rows up to which a whole workgroup joins one row
+// Workgroups in all: as many as are resident at once on 256 CUs, two of the
+// kernel for few rows, one of the other.
+constexpr int kRowWorkgroups = 512;
+constexpr int kTileWorkgroups = 256;
 
-// How one call is cut: everything the host decides, from sizes alone.
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Everything the host decides about one call, from sizes alone.
 struct CallPlan {
   SplitRule own, pre;
-  int pre_cu, pre_chunks;
-  int64_t own_items, own_slots, pre_items;   // per KV head
+  int64_t own_slots, pre_slots;      // per KV head
   bool shared, join;
   size_t o_own, ml_own, o_pre, ml_pre, bytes;
 };
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Tile height and splitting by the rows a KV head has against one run of keys.
-SplitRule rule_for(int64_t rows, int group, int heads, int cap) {
-  const bool tiles = rows > 32;
-  const int wgs = tiles ? kTileWorkgroups : kWorkgroups;
-  return SplitRule{group, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256, 128,
-                   wgs / heads > 1 ? wgs / heads : 1, 1, cap};
+// Tile height and workgroups by the rows a KV head has against one run of
+// keys, at most `tiles` tiles of at most cap keys.
+SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap) {
+  SplitRule r{};
+  r.group = group;
+  r.rt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  r.ku = 128;
+  r.cap = cap;
+  r.sloped = r.rt > 32;
+  r.grain = r.sloped && cap > r.ku ? 1 : kSub;
+  const int64_t most = (total_rows / r.rt + seqs) * ceil_div(cap > 0 ? cap : 1, r.ku);   // steps of keys, at most
+  int64_t n = (r.rt > 32 ? kTileWorkgroups : kRowWorkgroups) / heads;
+  if (n > most) n = most;
+  r.wgs = (int)(n < 1 ? 1 : n);
+  return r;
 }
 
 CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int heads, int group, int head_dim,
                    int64_t prefix_len) {
   CallPlan p{};
   const int64_t cap = max_pages << page_shift;
-  const int64_t rows = ceil_div(T, B) * group;            // of one sequence, on average
-  p.own = rule_for(rows, group, heads, (int)cap);
-  const int64_t tiles = T * group / p.own.rt + B;         // at most, over all sequences
-  const int64_t most_chunks = ceil_div(ceil_div(cap, p.own.ku), p.own.min_units);
+  p.own = rule_for(ceil_div(T, B) * group, T * group, B, group, heads, (int)cap);
+  const int64_t tiles = T * group / p.own.rt + B;           // at most, over all sequences
   p.shared = prefix_len > 0;
-  const int target = p.own.target;
-  p.own_items = most_chunks == 1 ? tiles : tiles + target + 8;
-  if (tiles * most_chunks < p.own_items) p.own_items = tiles * most_chunks;
-  // a launch with `target` tiles or more splits nothing
-  p.own_slots = p.own_items < 2 * target + 8 ? p.own_items : 2 * target + 8;
-  if (p.shared) p.own_slots = p.own_items;
-  else if (most_chunks == 1) p.own_slots = 0;
-  p.join = p.shared || p.own_slots > 0;
+  p.own_slots = p.shared ? p.own.wgs + tiles : 2 * p.own.wgs;
+  p.join = p.shared || (cap > p.own.ku && p.own.wgs > 1);   // a tile of one step is never cut
+  if (!p.join) p.own_slots = 0;
   if (p.shared) {
-    p.pre = rule_for(T * group, group, heads, 0);
-    const int64_t pt = ceil_div(T * group, p.pre.rt), units = ceil_div(prefix_len, p.pre.ku);
-    int64_t cu = ceil_div(pt * units, p.pre.target);
-    if (cu < p.pre.min_units) cu = p.pre.min_units;
-    if (cu > units) cu = units;
-    p.pre_cu = (int)cu;
-    p.pre_chunks = (int)ceil_div(units, cu);
-    p.pre_items = pt * p.pre_chunks;
+    p.pre = rule_for(T * group, T * group, 1, group, heads, (int)prefix_len);
+    p.pre.sloped = false;                                   // every row sees all of it
+    p.pre.grain = kSub;
+    p.pre_slots = p.pre.wgs + ceil_div(T * group, p.pre.rt);
   }
   size_t at = 0;
   auto take = [&](int64_t floats) {
@@ -566,8 +632,8 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   };
   p.o_own = take(p.own_slots * heads * p.own.rt * head_dim);
   p.ml_own = take(p.own_slots * heads * p.own.rt * 2);
-  p.o_pre = take(p.pre_items * heads * p.pre.rt * head_dim);
-  p.ml_pre = take(p.pre_items * heads * p.pre.rt * 2);
+  p.o_pre = take(p.pre_slots * heads * p.pre.rt * head_dim);
+  p.ml_pre = take(p.pre_slots * heads * p.pre.rt * 2);
   p.bytes = at > 16 ? at : 16;
   return p;
 }
@@ -584,25 +650,27 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
       plan_call(a.s.B, a.s.T, a.s.max_pages, a.c.page_shift, a.c.heads, a.group, head_dim, a.prefix_len);
   char* base = static_cast<char*>(ws);
   auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
-  AttendArgs own{a, p.own, Partials{at(p.o_own), at(p.ml_own), (int)p.own_slots}, p.shared, false, 0, 0};
-  AttendArgs pre{a, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_items}, true, true, p.pre_cu, p.pre_chunks};
+  const int pre_pages = (a.prefix_len + (1 << a.c.page_shift) - 1) >> a.c.page_shift;
+  const SeqView prefix{a.prefix_pages, nullptr, nullptr, 1, a.s.T, pre_pages};
+  const AttendArgs own{a, a.s, p.own, Partials{at(p.o_own), at(p.ml_own), (int)p.own_slots}, p.shared};
+  const AttendArgs pre{a, prefix, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_slots}, true};
   hipError_t e;
-  auto launch = [&](const AttendArgs& x, int64_t items) {
-    return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, items, st) : launch_kv_rows(x, head_dim, bits, items, st);
+  auto launch = [&](const AttendArgs& x) {
+    return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, st) : launch_kv_rows(x, head_dim, bits, st);
   };
-  if (p.shared && (e = launch(pre, p.pre_items)) != hipSuccess) return e;
-  if ((e = launch(own, p.own_items)) != hipSuccess) return e;
+  if (p.shared && (e = launch(pre)) != hipSuccess) return e;
+  if ((e = launch(own)) != hipSuccess) return e;
   if (!p.join) return hipSuccess;
-  const int64_t rows = (int64_t)a.s.T * a.c.heads * a.group;
-  const bool few = rows <= kJoinFew;
-  const int64_t wgs = few ? rows : ceil_div(rows, 4);
-  const dim3 grid((unsigned)(wgs < kJoinGrid ? wgs : kJoinGrid));
-  if (head_dim == 128) {
-    if (few) hipLaunchKernelGGL((kv_join_kernel<128, 4>), grid, dim3(256), 0, st, own, pre);
-    else hipLaunchKernelGGL((kv_join_kernel<128, 1>), grid, dim3(256), 0, st, own, pre);
+  if (p.shared) {
+    const int rpw = own.rule.rt <= 32 ? 4 : 16;
+    const int64_t tiles = p.own_slots - p.own.wgs;
+    const dim3 grid((unsigned)(tiles * (own.rule.rt / rpw) * a.c.heads));
+    if (head_dim == 128) hipLaunchKernelGGL((kv_join_prefix_kernel<128>), grid, dim3(256), 0, st, own, pre, rpw);
+    else hipLaunchKernelGGL((kv_join_prefix_kernel<64>), grid, dim3(256), 0, st, own, pre, rpw);
   } else {
-    if (few) hipLaunchKernelGGL((kv_join_kernel<64, 4>), grid, dim3(256), 0, st, own, pre);
-    else hipLaunchKernelGGL((kv_join_kernel<64, 1>), grid, dim3(256), 0, st, own, pre);
+    const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads));
+    if (head_dim == 128) hipLaunchKernelGGL((kv_join_cuts_kernel<128>), grid, dim3(256), 0, st, own);
+    else hipLaunchKernelGGL((kv_join_cuts_kernel<64>), grid, dim3(256), 0, st, own);
   }
   return hipGetLastError();
 }

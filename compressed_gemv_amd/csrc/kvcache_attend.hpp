@@ -8,78 +8,80 @@ namespace qg {
 
 struct AttendArgs {
   KvAttend a;
+  SeqView s;                   // a.s, or the prefix as one sequence that owns all rows
   SplitRule rule;
   Partials part;
-  bool shared;                // a prefix part exists: results always go through the partials
-  // prefix launch: all T rows against the prefix's keys in host-known chunks
-  bool prefix;
-  int prefix_cu, prefix_chunks;
+  bool keep;                   // every result goes through the partials (a shared prefix joins in)
 };
 
-// Wave-uniform description of what one workgroup does.
+// Wave-uniform description of one tile's part in one piece.
 struct Work {
-  int b;                      // < 0: nothing
-  int slot;                   // partial slot of this item
-  int row0, rows;             // first row (token * group + g) of the tile and rows of the sequence in all
+  int slot;                    // partial slot
+  int row0, rows;              // first row (token * group + g) of the tile and rows of the sequence in all
   int t0, vis0;
-  int k0, k1;                 // keys of the chunk that some row of the tile may see
-  int need;                   // keys the sequence's last row sees
+  int k0, k1;                  // keys of this part that some row of the tile may see
+  int need;                    // keys the sequence's last row sees
   bool causal, direct;
   const int32_t* pages;
   int max_pages;
 };
 
-__device__ __forceinline__ Work work_of(const AttendArgs& x, int item, int lane) {
-  const KvAttend& a = x.a;
-  Work w{};
-  w.b = -1;
-  int tile, chunk, cu;
-  if (x.prefix) {
-    tile = item / x.prefix_chunks;
-    chunk = item % x.prefix_chunks;
-    cu = x.prefix_cu;
-    w.b = 0;
-    w.t0 = 0;
-    w.rows = a.s.T * a.group;
-    w.vis0 = w.need = a.prefix_len;
-    w.causal = false;
-    w.direct = false;
-    w.pages = a.prefix_pages;
-    w.max_pages = (a.prefix_len + (1 << a.c.page_shift) - 1) >> a.c.page_shift;
-  } else {
-    cu = split_units(a.s, x.rule, lane);
-    const Item it = find_item(a.s, x.rule, cu, item, lane);
-    if (it.b < 0) return w;
-    tile = it.tile;
-    chunk = it.chunk;
-    w.b = it.b;
-    w.t0 = it.r.t0;
-    w.rows = it.r.count * a.group;
-    w.vis0 = it.r.vis0;
-    w.need = it.r.need;
-    w.causal = true;
-    w.direct = it.chunks == 1 && !x.shared;
-    w.pages = a.s.pages + (int64_t)it.b * a.s.max_pages;
-    w.max_pages = a.s.max_pages;
+// Steps through the tiles of a workgroup's piece.
+struct Pieces {
+  Line line;
+  int piece;
+  int64_t x, end;              // weights still to do
+};
+
+__device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int lane) {
+  Pieces p;
+  p.line = line_of(x.s, x.rule, lane);
+  p.piece = piece;
+  p.x = p.end = 0;
+  if (piece < p.line.N) {
+    p.x = p.line.cut(piece);
+    p.end = p.line.cut(piece + 1);
   }
-  w.slot = item;
-  if (!w.direct && item >= x.part.slots) {
-    w.b = -1;
-    return w;
+  return p;
+}
+
+__device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& w, int lane) {
+  while (p.x < p.end) {
+    const TileAt t = tile_at(x.s, x.rule, p.x, lane);
+    if (t.b < 0) return false;
+    const int64_t from = p.x;
+    const bool whole = t.lo >= from && t.hi <= p.end;
+    const int64_t slot = slot_of(p.line, t, p.piece, x.keep);
+    w.t0 = t.r.t0;
+    w.rows = t.r.count * x.a.group;
+    w.vis0 = t.r.vis0;
+    w.need = t.r.need;
+    w.causal = x.s.lens != nullptr;
+    w.direct = whole && !x.keep;
+    w.pages = x.s.pages + (int64_t)t.b * x.s.max_pages;
+    w.max_pages = x.s.max_pages;
+    w.slot = (int)slot;
+    w.row0 = t.tile * x.rule.rt;
+    // the last row of the tile sees the most
+    int last = w.row0 + x.rule.rt - 1;
+    if (last >= w.rows) last = w.rows - 1;
+    int vis = w.need;
+    if (w.causal) {
+      const int v = w.vis0 + last / x.a.group;
+      vis = v < 0 ? 0 : (v < w.need ? v : w.need);
+    }
+    // the cuts, from weights to whole steps of the tile's keys
+    const int units = (vis + x.rule.ku - 1) / x.rule.ku;
+    const double per = (double)units / (double)(t.hi - t.lo);
+    const int u0 = from <= t.lo ? 0 : __builtin_amdgcn_readfirstlane((int)((double)(from - t.lo) * per));
+    const int u1 = p.end >= t.hi ? units : __builtin_amdgcn_readfirstlane((int)((double)(p.end - t.lo) * per));
+    w.k0 = u0 * x.rule.ku;
+    w.k1 = u1 * x.rule.ku < vis ? u1 * x.rule.ku : vis;
+    if (w.k0 > w.k1) w.k0 = w.k1;
+    p.x = t.hi;
+    if (w.direct || slot < x.part.slots) return true;
   }
-  w.row0 = tile * x.rule.rt;
-  // the last row of the tile sees the most
-  int last = w.row0 + x.rule.rt - 1;
-  if (last >= w.rows) last = w.rows - 1;
-  int vis = w.need;
-  if (w.causal) {
-    const int v = w.vis0 + last / a.group;
-    vis = v < 0 ? 0 : (v < w.need ? v : w.need);
-  }
-  const int64_t len = (int64_t)cu * x.rule.ku, k0 = chunk * len, k1 = k0 + len;
-  w.k0 = k0 < vis ? (int)k0 : vis;
-  w.k1 = k1 < vis ? (int)k1 : vis;
-  return w;
+  return false;
 }
 
 // Keys that row R (an index of the sequence's rows) sees.
@@ -109,7 +111,7 @@ __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const 
   }
 }
 
-hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st);
-hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st);
+hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
+hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
 
 }  // namespace qg

@@ -3,11 +3,14 @@
 // the sequences as they grow).
 //
 // A KV head's rows of one sequence are its tokens times `group` query heads,
-// row = token * group + g; they are cut into tiles of RT rows, and the keys a
-// tile sees into chunks of `cu` units of KU keys.  An item is one (sequence,
-// row tile, chunk).  cu is the least that leaves about `target` items per KV
-// head, one number for the whole batch, so items cost about the same however
-// unequal the sequences are; with `target` row tiles or more nothing is split.
+// row = token * group + g; they are cut into tiles of RT rows.  Tile t of a
+// sequence weighs A + S t, about the keys it sees in steps of KU / 16 (later
+// tokens see more, so S > 0 where a tile holds a good part of a step).  All
+// tiles of the batch form one line of U weights per KV head, which is cut into
+// N equal pieces, one per workgroup, wherever the cuts fall: no workgroup has
+// more to do than another, however unequal the sequences are.  A tile that a
+// cut goes through leaves partial results, which the join adds up.  All of it
+// in integers, so every wave of every kernel finds the same cuts.
 #pragma once
 
 #include "common.hpp"
@@ -15,120 +18,187 @@
 
 namespace qg {
 
-constexpr int kNoSplit = 1 << 30;
+constexpr int kSub = 16;       // weight of KU keys
+
+struct SplitRule {
+  int group, rt, ku;           // query heads per KV head, rows per tile, keys per step
+  int wgs;                     // workgroups per KV head in the grid
+  int cap;                     // positions the page table holds
+  bool sloped;                 // weigh a sequence's tiles by what each sees
+  int grain;                   // cuts lie at multiples of this weight; kSub where all tiles weigh
+                               // whole steps, so that a tile of one step is never cut
+};
 
 struct SeqRows {
-  int t0, count;              // rows of Q that the sequence owns
-  int vis0;                   // keys that row t0 sees (may be <= 0); each later row sees one more
-  int need;                   // keys that its last row sees, 0 .. cap
+  int t0, count;               // rows of Q that the sequence owns
+  int vis0;                    // keys that row t0 sees (may be <= 0); each later row sees one more
+  int need;                    // keys that its last row sees, 0 .. cap
 };
 
 __device__ __forceinline__ SeqRows seq_rows(const SeqView& s, int b, int cap) {
   SeqRows r{0, 0, 0, 0};
   if (b >= s.B) return r;
+  if (!s.lens) return SeqRows{0, s.T, cap, cap};        // a shared prefix: every row sees all of it
   int64_t s0 = b, s1 = b + 1;
   if (s.starts) { s0 = s.starts[b]; s1 = s.starts[b + 1]; }
   const int64_t end = s1 < s.T ? s1 : s.T, t0 = s0 < 0 ? 0 : s0;
   if (end <= t0) return r;
   r.t0 = (int)t0;
   r.count = (int)(end - t0);
-  const int64_t len = s.lens[b];
-  int64_t v0 = len - (s1 - t0) + 1, v1 = len - (s1 - end);
-  v0 = v0 < -(int64_t)kNoSplit ? -(int64_t)kNoSplit : (v0 > cap ? cap : v0);
-  v1 = v1 < 0 ? 0 : (v1 > cap ? cap : v1);
-  r.vis0 = (int)v0;
-  r.need = (int)v1;
+  const int64_t len = s.lens[b], low = -((int64_t)1 << 30);
+  const int64_t v0 = len - (s1 - t0) + 1, v1 = len - (s1 - end);
+  r.vis0 = (int)(v0 < low ? low : (v0 > cap ? cap : v0));
+  r.need = (int)(v1 < 0 ? 0 : (v1 > cap ? cap : v1));
   return r;
 }
 
-struct SplitRule { int group, rt, ku, target, min_units, cap; };
+// Weights of a sequence: W(t) = A t + S t (t - 1) / 2 before tile t.
+struct Weights {
+  int tiles;
+  int A, S;
+  __device__ __forceinline__ int64_t before(int64_t t) const { return A * t + S * (t * (t - 1) / 2); }
+};
 
-__device__ __forceinline__ int tiles_of(const SplitRule& p, const SeqRows& r) {
-  return (int)(((int64_t)r.count * p.group + p.rt - 1) / p.rt);
-}
-__device__ __forceinline__ int chunks_of(const SplitRule& p, const SeqRows& r, int cu) {
-  const int units = (r.need + p.ku - 1) / p.ku;
-  return units <= cu ? 1 : (units + cu - 1) / cu;
-}
-
-// The batch's chunk length in units.  Wave-uniform; all lanes take part.
-__device__ __forceinline__ int split_units(const SeqView& s, const SplitRule& p, int lane) {
-  float w = 0.f;
-  int64_t tiles = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 64) {
-    const SeqRows r = seq_rows(s, b0 + lane, p.cap);
-    const int rt = tiles_of(p, r);
-    w += (float)rt * (float)((r.need + p.ku - 1) / p.ku);
-    tiles += rt;
+__device__ __forceinline__ Weights weights_of(const SplitRule& p, const SeqRows& r) {
+  Weights w;
+  w.tiles = (int)(((int64_t)r.count * p.group + p.rt - 1) / p.rt);
+  const int step = p.ku / kSub;
+  const int full = (r.need + p.ku - 1) / p.ku * kSub;     // of a tile that sees all
+  w.A = full < kSub ? kSub : full;
+  w.S = 0;
+  if (p.sloped && w.tiles > 1) {
+    const int s = p.rt / p.group / step;
+    const int64_t first = w.A - (int64_t)s * (w.tiles - 1);
+    if (first >= kSub) { w.S = s; w.A = (int)first; }
+    else { w.S = (w.A - kSub) / (w.tiles - 1); w.A -= w.S * (w.tiles - 1); }
   }
-  w = wave_sum(w);
-  const float tf = wave_sum((float)tiles);
-  if (tf >= (float)p.target) return kNoSplit;
-  const float c = w / (float)p.target;
-  const int cu = c < 1e9f ? (int)c + 1 : kNoSplit;
-  return cu < p.min_units ? p.min_units : cu;
+  return w;
 }
 
-// Inclusive sum over the lanes of a wave: DPP shifts inside the rows of 16,
+// Inclusive sums over the lanes of a wave: DPP shifts inside the rows of 16,
 // then lane 15 of a row added to the next one, lane 31 to the upper half.
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t dpp_i64(int64_t v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xF, false);
+  return ((int64_t)hi << 32) | (uint32_t)lo;
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  v += dpp_i64<0x111, 0xF>(v);     // row_shr:1
+  v += dpp_i64<0x112, 0xF>(v);
+  v += dpp_i64<0x114, 0xF>(v);
+  v += dpp_i64<0x118, 0xF>(v);
+  v += dpp_i64<0x142, 0xA>(v);     // row_bcast:15
+  v += dpp_i64<0x143, 0xC>(v);     // row_bcast:31
   return v;
 }
+__device__ __forceinline__ int64_t lane_i64(int64_t v, int l) {
+  return ((int64_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+}
 
-// One item of the launch, wave-uniform; b < 0: there is none.
-struct Item {
-  int b, tile, chunk, chunks;
+// fp64 results live in vector registers; equal in all lanes, they go back to scalar ones.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// The cut line.  Quotients go through fp64: with all products below 2^52 the
+// rounded quotient never reaches the next integer.
+struct Line {
+  int64_t U;                   // in grains
+  int N, grain;
+  __device__ __forceinline__ int64_t cut(int i) const {
+    return uniform((int64_t)((double)i * (double)U / (double)N)) * grain;
+  }
+  // the piece that weight x lies in
+  __device__ __forceinline__ int piece(int64_t x) const {
+    const int64_t y = grain == 1 ? x : x / kSub;
+    return __builtin_amdgcn_readfirstlane((int)(((double)(y + 1) * (double)N - 1.0) / (double)U));
+  }
+};
+
+__device__ __forceinline__ Line line_of(const SeqView& s, const SplitRule& p, int lane) {
+  int64_t u = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    const Weights w = weights_of(p, seq_rows(s, b0 + lane, p.cap));
+    u += w.before(w.tiles);
+  }
+  Line l;
+  u = lane_i64(wave_scan(u), 63);
+  l.grain = p.grain;
+  l.U = p.grain == 1 ? u : u / kSub;
+  const int64_t n = u / kSub;                              // a piece is a step of keys at least
+  l.N = n < p.wgs ? (int)n : p.wgs;
+  if (l.N < 1) l.N = 1;
+  return l;
+}
+
+// The tile that weight x of the line lies in, or (BY_INDEX) tile number x of
+// it; b < 0: none.
+struct TileAt {
+  int b, tile;
+  int64_t index;               // of the tile in the whole line
+  int64_t lo, hi;              // its weights
   SeqRows r;
 };
 
-__device__ __forceinline__ Item find_item(const SeqView& s, const SplitRule& p, int cu, int item, int lane) {
-  Item it{-1, 0, 0, 1, {0, 0, 0, 0}};
-  int carry = 0;
+template <bool BY_INDEX = false>
+__device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, int64_t x, int lane) {
+  TileAt a{};
+  a.b = -1;
+  int64_t carry = 0, tiles = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
     const SeqRows r = seq_rows(s, b0 + lane, p.cap);
-    const int ch = chunks_of(p, r, cu), n = tiles_of(p, r) * ch;
-    const int inc = wave_scan(n);
-    const uint64_t m = __ballot(carry + inc > item);
+    const Weights w = weights_of(p, r);
+    const int64_t u = w.before(w.tiles), inc = wave_scan(u), tinc = wave_scan((int64_t)w.tiles);
+    const uint64_t m = __ballot(BY_INDEX ? tiles + tinc > x : carry + inc > x);
     if (m) {
       const int l = __ffsll((unsigned long long)m) - 1;
-      const int k = item - carry - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(n, l));
-      it.chunks = __builtin_amdgcn_readlane(ch, l);
-      it.b = b0 + l;
-      it.tile = k / it.chunks;
-      it.chunk = k % it.chunks;
-      it.r.t0 = __builtin_amdgcn_readlane(r.t0, l);
-      it.r.count = __builtin_amdgcn_readlane(r.count, l);
-      it.r.vis0 = __builtin_amdgcn_readlane(r.vis0, l);
-      it.r.need = __builtin_amdgcn_readlane(r.need, l);
-      return it;
+      Weights v;
+      v.tiles = __builtin_amdgcn_readlane(w.tiles, l);
+      v.A = __builtin_amdgcn_readlane(w.A, l);
+      v.S = __builtin_amdgcn_readlane(w.S, l);
+      const int64_t base = carry + lane_i64(inc, l) - lane_i64(u, l), first = tiles + lane_i64(tinc, l) - v.tiles;
+      int lo = 0;
+      if (BY_INDEX) {
+        lo = (int)(x - first);
+      } else {
+        int n = v.tiles;                                   // last tile that begins at or before x
+        while (n > 1) {
+          const int half = n >> 1;
+          if (base + v.before(lo + half) <= x) { lo += half; n -= half; }
+          else n = half;
+        }
+      }
+      a.b = b0 + l;
+      a.tile = lo;
+      a.index = first + lo;
+      a.lo = base + v.before(lo);
+      a.hi = base + v.before(lo + 1);
+      a.r.t0 = __builtin_amdgcn_readlane(r.t0, l);
+      a.r.count = __builtin_amdgcn_readlane(r.count, l);
+      a.r.vis0 = __builtin_amdgcn_readlane(r.vis0, l);
+      a.r.need = __builtin_amdgcn_readlane(r.need, l);
+      return a;
     }
-    carry += __builtin_amdgcn_readlane(inc, 63);
+    carry += lane_i64(inc, 63);
+    tiles += lane_i64(tinc, 63);
   }
-  return it;
+  return a;
 }
 
-// Items of the sequences before b.
-__device__ __forceinline__ int items_before(const SeqView& s, const SplitRule& p, int cu, int b, int lane) {
-  int sum = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) {
-    const SeqRows r = seq_rows(s, b0 + lane, p.cap);
-    if (b0 + lane < b) sum += tiles_of(p, r) * chunks_of(p, r, cu);
-  }
-  return __builtin_amdgcn_readlane(wave_scan(sum), 63);
-}
-
-// Partial results of one part of the keys: item slots of RT rows, per row the
-// unnormalised sum of D values, its maximum (log2 domain) and its sum of weights.
+// Partial results: slots of RT rows, per row the unnormalised sum of D values,
+// its maximum (log2 domain) and its sum of weights.  A piece has at most two
+// tiles that a cut goes through, its first and its last; where everything is
+// kept (a shared prefix joins in), piece + tile index numbers the parts.
 struct Partials {
-  float* o;                   // [slot][rt][D]
-  float* ml;                  // [slot][rt][2]
-  int slots;                  // per KV head; starts that overlap could ask for more, which are left out
+  float* o;                    // [slot][head][rt][D]
+  float* ml;                   // [slot][head][rt][2]
+  int slots;                   // starts that overlap could ask for more, which are left out
 };
+
+__device__ __forceinline__ int64_t slot_of(const Line& line, const TileAt& t, int piece, bool keep_all) {
+  return keep_all ? piece + t.index : 2 * (int64_t)piece + (t.lo > line.cut(piece) ? 1 : 0);
+}
 
 }  // namespace qg

@@ -79,10 +79,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   const KvAttend& a = x.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int heads = a.c.heads, h = blockIdx.x % heads, item = blockIdx.x / heads;
-  const Work w = work_of(x, item, lane);
-  if (w.b < 0) return;
-
+  const int heads = a.c.heads, h = blockIdx.x % heads;
+  Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
+  Work w;
+  while (next_work(x, pieces, w, lane)) {
   // queries: rows scaled by a power of two to a largest value in [1, 2) (exact
   // up to 2^-25 of it), what each row sees, and the factor back
   f16x8_t qf[2][STEPS];
@@ -423,10 +423,12 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       ml[1] = l[n];
     }
   }
+  __syncthreads();                         // LDS is free for the next tile
+  }
 }
 
-hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, int64_t items, hipStream_t st) {
-  const dim3 grid((unsigned)(items * x.a.c.heads));
+hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
+  const dim3 grid((unsigned)(x.rule.wgs * x.a.c.heads));
 #define TILE(D, B, N) hipLaunchKernelGGL((kv_tile_kernel<D, B, N>), grid, dim3(64 * N), 0, st, x)
 #define TILE_N(D, B)                     \
   do {                                   \
