@@ -483,7 +483,8 @@ __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
   const int slot0 = (int)slot_of(line, t, i0, false);
   if (2 * (i0 + parts) > x.part.slots) return;
   const int row0 = t.tile * x.rule.rt, rows = t.r.count * a.group - row0, n = rows < x.rule.rt ? rows : x.rule.rt;
-  const int k = i - i0 - 1, sharers = parts - 1;
+  // the tile's rows go round the workgroups of its cuts, gridDim.y of them each
+  const int k = (i - i0 - 1) * gridDim.y + blockIdx.y, sharers = (parts - 1) * gridDim.y;
   if (parts >= 16) {
     for (int row = k; row < n; row += sharers) {           // workgroup-uniform
       auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
@@ -530,16 +531,16 @@ __global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, Att
   const int row0 = t.tile * own.rule.rt, rows = t.r.count * a.group;
   const int first = row0 + u % per_tile * rpw;
   if (first >= rows) return;
-  const Line line = line_of(own.s, own.rule, lane), pline = line_of(pre.s, pre.rule, lane);
+  const Line line = line_of(own.s, own.rule, lane), pline = pre.line;
   const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
   const int slot0 = (int)(i0 + t.index);
   if (slot0 + parts > own.part.slots) return;
-  const int A = weights_of(pre.rule, seq_rows(pre.s, 0, pre.rule.cap)).A;   // of every tile of the prefix
+  const int64_t A = (int64_t)(pre.a.prefix_len + pre.rule.ku - 1) / pre.rule.ku * kSub;   // weight of a tile of the prefix
   const int last = first + rpw < rows ? first + rpw : rows;
   for (int R = first + wave; R < last; R += 4) {
     const int64_t P = (int64_t)t.r.t0 * a.group + R;
     const int pt = (int)(P / pre.rule.rt), prow = (int)(P % pre.rule.rt);
-    const int p0 = pline.piece((int64_t)A * pt), np = pline.piece((int64_t)A * (pt + 1) - 1) - p0 + 1;
+    const int p0 = pline.piece(A * pt), np = pline.piece(A * (pt + 1) - 1) - p0 + 1;
     if (p0 + pt + np > pre.part.slots) continue;
     auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
       const bool p = c < np;
@@ -581,6 +582,11 @@ namespace {
 constexpr int kRowWorkgroups = 512;
 constexpr int kTileWorkgroups = 256;
 
+// Keys are decoded beforehand where at least this many rows of a sequence meet
+// them (4 tiles) and the images, sized for full page tables, fit this many bytes.
+constexpr int64_t kImageRows = 1024;
+constexpr int64_t kImageBytes = (int64_t)1 << 30;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Everything the host decides about one call, from sizes alone.
@@ -588,7 +594,9 @@ struct CallPlan {
   SplitRule own, pre;
   int64_t own_slots, pre_slots;      // per KV head
   bool shared, join;
-  size_t o_own, ml_own, o_pre, ml_pre, bytes;
+  int64_t images;                    // steps of keys to decode beforehand
+  Line pre_line;
+  size_t o_own, ml_own, o_pre, ml_pre, image, bytes;
 };
 
 // Tile height and workgroups by the rows a KV head has against one run of
@@ -623,6 +631,12 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
     p.pre.sloped = false;                                   // every row sees all of it
     p.pre.grain = kSub;
     p.pre_slots = p.pre.wgs + ceil_div(T * group, p.pre.rt);
+    p.pre_line = Line{ceil_div(T * group, p.pre.rt) * ceil_div(prefix_len, p.pre.ku), p.pre.wgs, kSub};
+    if (p.pre_line.U < p.pre_line.N) p.pre_line.N = (int)p.pre_line.U;
+  }
+  if (p.own.rt == 256 && ceil_div(T, B) * group >= kImageRows) {
+    p.images = B * ceil_div(cap, 128);
+    if (p.images * heads * kv_image_bytes(head_dim) > kImageBytes) p.images = 0;
   }
   size_t at = 0;
   auto take = [&](int64_t floats) {
@@ -634,6 +648,7 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   p.ml_own = take(p.own_slots * heads * p.own.rt * 2);
   p.o_pre = take(p.pre_slots * heads * p.pre.rt * head_dim);
   p.ml_pre = take(p.pre_slots * heads * p.pre.rt * 2);
+  p.image = take(p.images * heads * kv_image_bytes(head_dim) / 4);
   p.bytes = at > 16 ? at : 16;
   return p;
 }
@@ -652,23 +667,25 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
   auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   const int pre_pages = (a.prefix_len + (1 << a.c.page_shift) - 1) >> a.c.page_shift;
   const SeqView prefix{a.prefix_pages, nullptr, nullptr, 1, a.s.T, pre_pages};
-  const AttendArgs own{a, a.s, p.own, Partials{at(p.o_own), at(p.ml_own), (int)p.own_slots}, p.shared};
-  const AttendArgs pre{a, prefix, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_slots}, true};
+  const AttendArgs own{a, a.s, p.own, Partials{at(p.o_own), at(p.ml_own), (int)p.own_slots}, p.shared, Line{},
+                       p.images ? reinterpret_cast<uint8_t*>(base + p.image) : nullptr, p.images};
+  const AttendArgs pre{a, prefix, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_slots}, true, p.pre_line, nullptr, 0};
   hipError_t e;
   auto launch = [&](const AttendArgs& x) {
     return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, st) : launch_kv_rows(x, head_dim, bits, st);
   };
   if (p.shared && (e = launch(pre)) != hipSuccess) return e;
+  if (own.image && (e = launch_kv_images(own, head_dim, bits, st)) != hipSuccess) return e;
   if ((e = launch(own)) != hipSuccess) return e;
   if (!p.join) return hipSuccess;
   if (p.shared) {
-    const int rpw = own.rule.rt <= 32 ? 4 : 16;
+    const int rpw = own.rule.rt <= 32 ? 8 : 16;
     const int64_t tiles = p.own_slots - p.own.wgs;
     const dim3 grid((unsigned)(tiles * (own.rule.rt / rpw) * a.c.heads));
     if (head_dim == 128) hipLaunchKernelGGL((kv_join_prefix_kernel<128>), grid, dim3(256), 0, st, own, pre, rpw);
     else hipLaunchKernelGGL((kv_join_prefix_kernel<64>), grid, dim3(256), 0, st, own, pre, rpw);
   } else {
-    const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads));
+    const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads), (unsigned)ceil_div(own.rule.rt, 32));
     if (head_dim == 128) hipLaunchKernelGGL((kv_join_cuts_kernel<128>), grid, dim3(256), 0, st, own);
     else hipLaunchKernelGGL((kv_join_cuts_kernel<64>), grid, dim3(256), 0, st, own);
   }

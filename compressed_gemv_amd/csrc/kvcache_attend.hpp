@@ -12,6 +12,10 @@ struct AttendArgs {
   SplitRule rule;
   Partials part;
   bool keep;                   // every result goes through the partials (a shared prefix joins in)
+  Line line;                   // of a shared prefix, known on the host
+  // decoded keys and values, one image for each step of keys and KV head, or null
+  uint8_t* image;
+  int64_t images;              // steps of keys there is room for
 };
 
 // Wave-uniform description of one tile's part in one piece.
@@ -24,6 +28,7 @@ struct Work {
   bool causal, direct;
   const int32_t* pages;
   int max_pages;
+  int64_t steps;               // images: of the sequences before this one
 };
 
 // Steps through the tiles of a workgroup's piece.
@@ -35,7 +40,7 @@ struct Pieces {
 
 __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int lane) {
   Pieces p;
-  p.line = line_of(x.s, x.rule, lane);
+  p.line = x.s.lens ? line_of(x.s, x.rule, lane) : x.line;
   p.piece = piece;
   p.x = p.end = 0;
   if (piece < p.line.N) {
@@ -45,10 +50,12 @@ __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int 
   return p;
 }
 
+template <bool STEPS = false>
 __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& w, int lane) {
   while (p.x < p.end) {
-    const TileAt t = tile_at(x.s, x.rule, p.x, lane);
+    const TileAt t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane);
     if (t.b < 0) return false;
+    w.steps = t.steps;
     const int64_t from = p.x;
     const bool whole = t.lo >= from && t.hi <= p.end;
     const int64_t slot = slot_of(p.line, t, p.piece, x.keep);
@@ -113,5 +120,10 @@ __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const 
 
 hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
 hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
+hipError_t launch_kv_images(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
+// Bytes of one image (128 keys of one KV head): the LDS rows of the keys, those
+// of the values' coordinates, and 1 KB whose first word has a bit for every 16
+// keys whose page is not in the cache.
+constexpr int64_t kv_image_bytes(int head_dim) { return 128 * (2 * head_dim + 16) + head_dim * (2 * 128 + 16) + 1024; }
 
 }  // namespace qg

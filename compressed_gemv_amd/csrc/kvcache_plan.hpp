@@ -52,6 +52,8 @@ __device__ __forceinline__ SeqRows seq_rows(const SeqView& s, int b, int cap) {
   return r;
 }
 
+__device__ __forceinline__ int steps_of(const SplitRule& p, const SeqRows& r) { return (r.need + p.ku - 1) / p.ku; }
+
 // Weights of a sequence: W(t) = A t + S t (t - 1) / 2 before tile t.
 struct Weights {
   int tiles;
@@ -139,17 +141,20 @@ struct TileAt {
   int b, tile;
   int64_t index;               // of the tile in the whole line
   int64_t lo, hi;              // its weights
+  int64_t steps;               // steps of keys of the sequences before b
   SeqRows r;
 };
 
-template <bool BY_INDEX = false>
+template <bool BY_INDEX = false, bool STEPS = false>
 __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, int64_t x, int lane) {
   TileAt a{};
   a.b = -1;
-  int64_t carry = 0, tiles = 0;
+  int64_t carry = 0, tiles = 0, steps = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
     const SeqRows r = seq_rows(s, b0 + lane, p.cap);
     const Weights w = weights_of(p, r);
+    const int k = steps_of(p, r);
+    const int64_t kinc = STEPS ? wave_scan((int64_t)k) : 0;
     const int64_t u = w.before(w.tiles), inc = wave_scan(u), tinc = wave_scan((int64_t)w.tiles);
     const uint64_t m = __ballot(BY_INDEX ? tiles + tinc > x : carry + inc > x);
     if (m) {
@@ -172,6 +177,7 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
       }
       a.b = b0 + l;
       a.tile = lo;
+      a.steps = STEPS ? steps + lane_i64(kinc, l) - __builtin_amdgcn_readlane(k, l) : 0;
       a.index = first + lo;
       a.lo = base + v.before(lo);
       a.hi = base + v.before(lo + 1);
@@ -183,8 +189,31 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
     }
     carry += lane_i64(inc, 63);
     tiles += lane_i64(tinc, 63);
+    if (STEPS) steps += lane_i64(kinc, 63);
   }
   return a;
+}
+
+// Step x of all the sequences' steps of keys; b < 0: none.
+struct StepAt {
+  int b, step, need;
+};
+
+__device__ __forceinline__ StepAt step_at(const SeqView& s, const SplitRule& p, int64_t x, int lane) {
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    const SeqRows r = seq_rows(s, b0 + lane, p.cap);
+    const int k = steps_of(p, r);
+    const int64_t inc = wave_scan((int64_t)k);
+    const uint64_t m = __ballot(carry + inc > x);
+    if (m) {
+      const int l = __ffsll((unsigned long long)m) - 1;
+      return StepAt{b0 + l, (int)(x - carry - lane_i64(inc, l)) + __builtin_amdgcn_readlane(k, l),
+                    __builtin_amdgcn_readlane(r.need, l)};
+    }
+    carry += lane_i64(inc, 63);
+  }
+  return StepAt{-1, 0, 0};
 }
 
 // Partial results: slots of RT rows, per row the unnormalised sum of D values,

@@ -45,6 +45,144 @@ constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 10
 
 }  // namespace
 
+// Decoding of KT = NT / 2 keys by NT threads: half a key row and D / 16
+// coordinates of 8 values each.  ks, vs: LDS or an image in memory.
+template <int D, int BITS, int NT>
+struct Decoder {
+  static constexpr int KT = NT / 2;
+  static constexpr int ROWB = D * BITS / 8;
+  static constexpr int KP = D * 2 + 16, VP = KT * 2 + 16;   // pitch of a key's and of a coordinate's row
+  static constexpr int KBUF = KT * KP, VBUF = D * VP;
+  static constexpr int KL = ROWB / 2 / 16;        // 16-byte loads of a thread's half key row
+  static constexpr int VB = ROWB / 16;            // bytes of a value row per thread
+  static constexpr int VW = VB < 4 ? 1 : VB / 4;
+  static constexpr int DPT = D / 16;              // coordinates per thread of 8 values
+  struct Codes {
+    u32x4_t k[KL];
+    uint32_t v[8][VW];
+    uint32_t km, kvm;                      // the key's constants of K and of V
+    u32x4_t vm[2];
+    int kpage, vpage;
+  };
+  const KvView& c;
+  const int32_t* pages;
+  int max_pages, k1;                       // keys behind k1 are nobody's
+  int kkey, khalf, vchunk, vg, vkey;       // values vkey .. + 3 and vkey + 8 .. + 3
+  uint32_t pmask, page_rows, head_row;
+  int kpage, vpage;                        // of the step to be loaded next
+
+  __device__ __forceinline__ Decoder(const KvView& c_, int h, int tid) : c(c_) {
+    kkey = tid >> 1;
+    khalf = tid & 1;
+    vchunk = tid >> 4;
+    vg = tid & 15;
+    vkey = 16 * (vchunk >> 1) + 4 * (vchunk & 1);
+    pmask = (1u << c.page_shift) - 1u;
+    page_rows = (uint32_t)c.heads << c.page_shift;
+    head_row = (uint32_t)h << c.page_shift;
+  }
+  __device__ __forceinline__ int page_of(int key) const {
+    if (key >= k1 || (key >> c.page_shift) >= max_pages) return -1;
+    const int id = pages[key >> c.page_shift];
+    return id < c.n_pages ? id : -1;
+  }
+  __device__ __forceinline__ void find_pages(int key0) {
+    kpage = page_of(key0 + kkey);
+    vpage = page_of(key0 + (vkey & ~15));
+  }
+  __device__ __forceinline__ void load(int key0, Codes& r) {
+    r.kpage = kpage;
+    r.vpage = vpage;
+    const uint64_t krow = (uint64_t)(uint32_t)(kpage < 0 ? 0 : kpage) * page_rows + (head_row + ((uint32_t)(key0 + kkey) & pmask));
+    const uint64_t vrow = (uint64_t)(uint32_t)(vpage < 0 ? 0 : vpage) * page_rows + (head_row + ((uint32_t)(key0 + vkey) & pmask));
+    const u32x4_t* kp = reinterpret_cast<const u32x4_t*>(c.codes[0] + krow * ROWB + khalf * (ROWB / 2));
+#pragma unroll
+    for (int i = 0; i < KL; ++i) r.k[i] = kp[i];
+    r.km = c.meta[0][krow];
+    r.kvm = c.meta[1][krow];
+    const uint8_t* vp = c.codes[1] + vrow * ROWB + vg * VB;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* pj = vp + ((j & 3) + 8 * (j >> 2)) * ROWB;
+      if constexpr (VB == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(pj);
+        r.v[j][0] = v.x;
+        r.v[j][1 % VW] = v.y;
+      } else if constexpr (VB == 4) {
+        r.v[j][0] = *reinterpret_cast<const uint32_t*>(pj);
+      } else {
+        r.v[j][0] = *reinterpret_cast<const uint16_t*>(pj);
+      }
+    }
+    const uint32_t* mp = c.meta[1] + vrow;
+    r.vm[0] = *reinterpret_cast<const u32x4_t*>(mp);
+    r.vm[1] = *reinterpret_cast<const u32x4_t*>(mp + 8);
+  }
+  // A value row that is NaN is decoded as zeros and makes its key NaN instead,
+  // so it reaches exactly the rows whose mask lets them see it; constants of
+  // keys that no row sees become zero.
+  static __device__ __forceinline__ bool nan_meta(uint32_t mt) { return (mt & 0x7C00u) == 0x7C00u; }
+  __device__ __forceinline__ void keys(int key0, const Codes& r, uint8_t* ks, uint32_t* gone) const {
+    const uint32_t mt = r.kpage < 0 || key0 + kkey >= k1 ? 0u : (nan_meta(r.kvm) ? 0x7E007E00u : r.km);
+    const uint32_t s2 = __builtin_amdgcn_perm(mt, mt, 0x01000100u), o2 = __builtin_amdgcn_perm(mt, mt, 0x03020302u);
+    uint8_t* out = ks + kkey * KP + khalf * D;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      u32x4_t v;
+      if constexpr (BITS == 8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t c = r.k[(2 * i + e) / 4][(2 * i + e) % 4];
+          v[2 * e] = __builtin_amdgcn_perm(k1024, c, 0x05010500u);
+          v[2 * e + 1] = __builtin_amdgcn_perm(k1024, c, 0x05030502u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = ((r.k[i / 4][i % 4] >> (4 * e)) & 0x000F000Fu) | k1024;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = pk_fma(pk_add(v[e], kM1024), s2, o2);
+      *reinterpret_cast<u32x4_t*>(out + i * 16) = v;
+    }
+    if (khalf == 0 && (kkey & 15) == 0) gone[kkey >> 4] = r.kpage < 0 ? 1u << (kkey >> 4) : 0u;
+  }
+  __device__ __forceinline__ void values(int key0, const Codes& r, uint8_t* vs) const {
+    uint32_t s2[4], o2[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t mt[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * q + e;
+        const uint32_t t = r.vm[j / 4][j % 4];
+        mt[e] = r.vpage < 0 || key0 + vkey + (j & 3) + 8 * (j >> 2) >= k1 || nan_meta(t) ? 0u : t;
+      }
+      s2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x05040100u);
+      o2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x07060302u);
+    }
+    uint32_t half[4] = {0u, 0u, 0u, 0u};
+    uint8_t* out = vs + vg * VP + vchunk * 16;
+#pragma unroll
+    for (int d = 0; d < DPT; ++d) {
+      u32x4_t v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u;
+        if constexpr (BITS == 8) {         // two coordinates of both keys, then one with the exponent of 1024
+          if (d % 2 == 0)
+            half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][d / 4], r.v[2 * q][d / 4], d % 4 == 0 ? 0x05010400u : 0x07030602u);
+          u = __builtin_amdgcn_perm(k1024, half[q], d % 2 == 0 ? 0x05010500u : 0x05030502u);
+        } else {
+          if (d % 4 == 0) half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][0], r.v[2 * q][0], d == 0 ? 0x05040100u : 0x07060302u);
+          u = ((half[q] >> (4 * (d % 4))) & 0x000F000Fu) | k1024;
+        }
+        v[q] = pk_fma(pk_add(u, kM1024), s2[q], o2[q]);
+      }
+      *reinterpret_cast<u32x4_t*>(out + 16 * d * VP) = v;
+    }
+  }
+};
+
 // A workgroup: NW waves of 64 rows (two blocks of 32), one wave per SIMD with
 // all its registers; 32 NW keys a step, two LDS buffers, one barrier a step.
 // S^T = K Q^T on 32x32x16 products puts a row's logits of 16 keys into one
@@ -61,28 +199,24 @@ constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 10
 // and every address of the inner loop is one register plus a constant.
 // Coordinate DPT g + q of V lies in row 16 q + g, so that the lanes that write
 // it (q fixed) write neighbouring rows.
-template <int D, int BITS, int NW>
+template <int D, int BITS, int NW, bool IMAGE>
 __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   constexpr int KT = 32 * NW;              // keys per step
   constexpr int KBS = KT / 32;
-  constexpr int ROWB = D * BITS / 8;
-  constexpr int STEPS = D / 16, DT = D / 32;
-  constexpr int KP = D * 2 + 16, VP = KT * 2 + 16;   // pitch of a key's and of a coordinate's LDS row
-  constexpr int KBUF = KT * KP, VBUF = D * VP;
-  constexpr int KL = ROWB / 2 / 16;        // 16-byte loads of a thread's half key row
-  constexpr int VB = ROWB / 16;            // bytes of a value row per thread
-  constexpr int VW = VB < 4 ? 1 : VB / 4;
-  constexpr int DPT = D / 16;              // coordinates per thread of 8 values
+  constexpr int STEPS = D / 16, DT = D / 32, DPT = D / 16;
+  using Dec = Decoder<D, BITS, 64 * NW>;
+  constexpr int KP = Dec::KP, VP = Dec::VP, KBUF = Dec::KBUF, VBUF = Dec::VBUF;
   __shared__ __align__(16) uint8_t ksh[2 * KBUF];
   __shared__ __align__(16) uint8_t vsh[2 * VBUF];
-  __shared__ uint32_t gone[2][KT / 16];    // per 16 keys: 1 << (their place) where they are not in the cache
+  // per 16 keys: 1 << (their place) where they are not in the cache (an image brings 1 KB)
+  __shared__ __align__(16) uint32_t gone[2][IMAGE ? 256 : KT / 16];
   const KvAttend& a = x.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
   const int heads = a.c.heads, h = blockIdx.x % heads;
   Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
   Work w;
-  while (next_work(x, pieces, w, lane)) {
+  while (next_work<IMAGE>(x, pieces, w, lane)) {
   // queries: rows scaled by a power of two to a largest value in [1, 2) (exact
   // up to 2^-25 of it), what each row sees, and the factor back
   f16x8_t qf[2][STEPS];
@@ -153,120 +287,24 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     p[n][0] = p[n][1] = u32x4_t{0u, 0u, 0u, 0u};
   }
 
-  // ---- what this thread decodes: half a key row, and DPT coordinates of 8 values
-  const int kkey = tid >> 1, khalf = tid & 1;
-  const int vchunk = tid >> 4, vg = tid & 15;
-  const int vkey = 16 * (vchunk >> 1) + 4 * (vchunk & 1);   // keys vkey .. + 3 and vkey + 8 .. + 3
-  const int shift = a.c.page_shift;
-  const uint32_t pmask = (1u << shift) - 1u;
-  const uint32_t page_rows = (uint32_t)heads << shift, head_row = (uint32_t)h << shift;
-  auto page_of = [&](int key) -> int {
-    if (key >= w.k1 || (key >> shift) >= w.max_pages) return -1;
-    const int id = w.pages[key >> shift];
-    return id < a.c.n_pages ? id : -1;
-  };
-  struct Codes {
-    u32x4_t k[KL];
-    uint32_t v[8][VW];
-    uint32_t km, kvm;                      // the key's constants of K and of V
-    u32x4_t vm[2];
-    int kpage, vpage;
-  };
-  int kpage = page_of(w.k0 + kkey), vpage = page_of(w.k0 + (vkey & ~15));   // of the step to be loaded next
-  auto load = [&](int key0, Codes& r) {
-    r.kpage = kpage;
-    r.vpage = vpage;
-    const uint64_t krow = (uint64_t)(uint32_t)(kpage < 0 ? 0 : kpage) * page_rows + (head_row + ((uint32_t)(key0 + kkey) & pmask));
-    const uint64_t vrow = (uint64_t)(uint32_t)(vpage < 0 ? 0 : vpage) * page_rows + (head_row + ((uint32_t)(key0 + vkey) & pmask));
-    const u32x4_t* kp = reinterpret_cast<const u32x4_t*>(a.c.codes[0] + krow * ROWB + khalf * (ROWB / 2));
-#pragma unroll
-    for (int i = 0; i < KL; ++i) r.k[i] = kp[i];
-    r.km = a.c.meta[0][krow];
-    r.kvm = a.c.meta[1][krow];
-    const uint8_t* vp = a.c.codes[1] + vrow * ROWB + vg * VB;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint8_t* pj = vp + ((j & 3) + 8 * (j >> 2)) * ROWB;
-      if constexpr (VB == 8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(pj);
-        r.v[j][0] = v.x;
-        r.v[j][1 % VW] = v.y;
-      } else if constexpr (VB == 4) {
-        r.v[j][0] = *reinterpret_cast<const uint32_t*>(pj);
-      } else {
-        r.v[j][0] = *reinterpret_cast<const uint16_t*>(pj);
-      }
-    }
-    const uint32_t* mp = a.c.meta[1] + vrow;
-    r.vm[0] = *reinterpret_cast<const u32x4_t*>(mp);
-    r.vm[1] = *reinterpret_cast<const u32x4_t*>(mp + 8);
-    kpage = page_of(key0 + KT + kkey);
-    vpage = page_of(key0 + KT + (vkey & ~15));
-  };
-  // A value row that is NaN is decoded as zeros and makes its key NaN instead,
-  // so it reaches exactly the rows whose mask lets them see it; constants of
-  // keys that no row sees become zero.
-  auto nan_meta = [](uint32_t mt) { return (mt & 0x7C00u) == 0x7C00u; };
-  auto decode_k = [&](int key0, const Codes& r, int buf) {
-    const uint32_t mt = r.kpage < 0 || key0 + kkey >= w.k1 ? 0u : (nan_meta(r.kvm) ? 0x7E007E00u : r.km);
-    const uint32_t s2 = __builtin_amdgcn_perm(mt, mt, 0x01000100u), o2 = __builtin_amdgcn_perm(mt, mt, 0x03020302u);
-    uint8_t* out = ksh + buf * KBUF + kkey * KP + khalf * D;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      u32x4_t v;
-      if constexpr (BITS == 8) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t c = r.k[(2 * i + e) / 4][(2 * i + e) % 4];
-          v[2 * e] = __builtin_amdgcn_perm(k1024, c, 0x05010500u);
-          v[2 * e + 1] = __builtin_amdgcn_perm(k1024, c, 0x05030502u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ((r.k[i / 4][i % 4] >> (4 * e)) & 0x000F000Fu) | k1024;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = pk_fma(pk_add(v[e], kM1024), s2, o2);
-      *reinterpret_cast<u32x4_t*>(out + i * 16) = v;
-    }
-    if (khalf == 0 && (kkey & 15) == 0) gone[buf][kkey >> 4] = r.kpage < 0 ? 1u << (kkey >> 4) : 0u;
-  };
-  auto decode_v = [&](int key0, const Codes& r, int buf) {
-    uint32_t s2[4], o2[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t mt[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int j = 2 * q + e;
-        const uint32_t t = r.vm[j / 4][j % 4];
-        mt[e] = r.vpage < 0 || key0 + vkey + (j & 3) + 8 * (j >> 2) >= w.k1 || nan_meta(t) ? 0u : t;
-      }
-      s2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x05040100u);
-      o2[q] = __builtin_amdgcn_perm(mt[1], mt[0], 0x07060302u);
-    }
-    uint32_t half[4] = {0u, 0u, 0u, 0u};
-    uint8_t* out = vsh + buf * VBUF + vg * VP + vchunk * 16;
-#pragma unroll
-    for (int d = 0; d < DPT; ++d) {
-      u32x4_t v;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t u;
-        if constexpr (BITS == 8) {         // two coordinates of both keys, then one with the exponent of 1024
-          if (d % 2 == 0)
-            half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][d / 4], r.v[2 * q][d / 4], d % 4 == 0 ? 0x05010400u : 0x07030602u);
-          u = __builtin_amdgcn_perm(k1024, half[q], d % 2 == 0 ? 0x05010500u : 0x05030502u);
-        } else {
-          if (d % 4 == 0) half[q] = __builtin_amdgcn_perm(r.v[2 * q + 1][0], r.v[2 * q][0], d == 0 ? 0x05040100u : 0x07060302u);
-          u = ((half[q] >> (4 * (d % 4))) & 0x000F000Fu) | k1024;
-        }
-        v[q] = pk_fma(pk_add(u, kM1024), s2[q], o2[q]);
-      }
-      *reinterpret_cast<u32x4_t*>(out + 16 * d * VP) = v;
-    }
-  };
+  Dec dec(a.c, h, tid);
+  dec.pages = w.pages;
+  dec.max_pages = w.max_pages;
+  dec.k1 = w.k1;
 
+  // An image is copied to LDS as it lies, 1 KB a wave and instruction, without
+  // passing through registers; __syncthreads waits for it.
+  auto fetch = [&](int key0, int buf) {
+    const int64_t step = w.steps + key0 / KT;
+    const uint8_t* src = x.image + (step * heads + h) * kv_image_bytes(D) + lane * 16;
+    auto put = [&](const uint8_t* from, uint8_t* to) {
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    };
+    for (int i = wave; i < KBUF / 1024; i += NW) put(src + i * 1024, ksh + buf * KBUF + i * 1024);
+    for (int i = wave; i < VBUF / 1024; i += NW) put(src + KBUF + i * 1024, vsh + buf * VBUF + i * 1024);
+    if (wave == 0) put(src + KBUF + VBUF, reinterpret_cast<uint8_t*>(gone[buf]));
+  };
   const uint8_t* kread = ksh + col * KP + hh * 16;
   const uint8_t* vread = vsh + col * VP + hh * 16;
   f16x8_t kf[STEPS], vf[2][DT];
@@ -345,11 +383,20 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   auto none = [] {};
 
   if (w.k0 < w.k1) {                       // workgroup-uniform
-    Codes r;
-    load(w.k0, r);
-    decode_k(w.k0, r, 0);
-    decode_v(w.k0, r, 0);
-    if (w.k0 + KT < w.k1) load(w.k0 + KT, r);
+    typename Dec::Codes r;
+    if constexpr (IMAGE) {
+      fetch(w.k0, 0);
+    } else {
+      dec.find_pages(w.k0);
+      dec.load(w.k0, r);
+      dec.find_pages(w.k0 + KT);
+      dec.keys(w.k0, r, ksh, gone[0]);
+      dec.values(w.k0, r, vsh);
+      if (w.k0 + KT < w.k1) {
+        dec.load(w.k0 + KT, r);
+        dec.find_pages(w.k0 + 2 * KT);
+      }
+    }
     __syncthreads();
     // before the first keys: weights of zero, logits that add nothing
 #pragma unroll
@@ -363,6 +410,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       for (int i = 0; i < KT / 16; ++i) holes |= gone[buf][i];
       holes = __builtin_amdgcn_readfirstlane(holes);
       const bool more = key + KT < w.k1;
+      if constexpr (IMAGE) {
+        if (more) fetch(key + KT, buf ^ 1);
+      }
 #pragma unroll
       for (int kb = 0; kb < KBS; ++kb) {
         const int k = key + 32 * kb;
@@ -370,10 +420,15 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
         turn(B{}, none, none);             // softmax B (before); O_A, S_A
         bounds(A{}, k, (holes >> (2 * kb)) & 3u);
         turn(A{}, [&] { read_v(buf, kb); }, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); });
-        if (kb == KBS - 2 && more) decode_k(key + KT, r, buf ^ 1);
-        if (kb == KBS - 1 && more) {
-          decode_v(key + KT, r, buf ^ 1);
-          if (key + 2 * KT < w.k1) load(key + 2 * KT, r);
+        if constexpr (!IMAGE) {
+          if (kb == KBS - 2 && more) dec.keys(key + KT, r, ksh + (buf ^ 1) * KBUF, gone[buf ^ 1]);
+          if (kb == KBS - 1 && more) {
+            dec.values(key + KT, r, vsh + (buf ^ 1) * VBUF);
+            if (key + 2 * KT < w.k1) {
+              dec.load(key + 2 * KT, r);
+              dec.find_pages(key + 3 * KT);
+            }
+          }
         }
       }
       prev_holes = (int)((holes >> (2 * KBS - 2)) & 3u);
@@ -427,13 +482,54 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   }
 }
 
+// Images of the decoded keys and values, one workgroup for 128 keys of one KV
+// head at a time: where many row tiles meet the same keys, each key is decoded
+// once and not once for every tile, and the tile kernel's vector unit, which
+// shares its issue slots with the products, is left to the softmax.
+template <int D, int BITS>
+__global__ __launch_bounds__(256) void kv_image_kernel(AttendArgs x) {
+  using Dec = Decoder<D, BITS, 256>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int heads = x.a.c.heads;
+  for (int64_t i = blockIdx.x; i < x.images * heads; i += gridDim.x) {
+    const int h = (int)(i % heads);
+    const StepAt at = step_at(x.s, x.rule, i / heads, lane);
+    if (at.b < 0) return;
+    Dec dec(x.a.c, h, tid);
+    dec.pages = x.s.pages + (int64_t)at.b * x.s.max_pages;
+    dec.max_pages = x.s.max_pages;
+    dec.k1 = at.need;
+    typename Dec::Codes r;
+    const int key0 = at.step * 128;
+    dec.find_pages(key0);
+    dec.load(key0, r);
+    uint8_t* out = x.image + i * kv_image_bytes(D);
+    dec.keys(key0, r, out, reinterpret_cast<uint32_t*>(out + Dec::KBUF + Dec::VBUF));
+    dec.values(key0, r, out + Dec::KBUF);
+  }
+}
+
+hipError_t launch_kv_images(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
+  const int64_t n = x.images * x.a.c.heads;
+  const dim3 grid((unsigned)(n < 8192 ? n : 8192));
+  if (head_dim == 128) {
+    if (bits == 8) hipLaunchKernelGGL((kv_image_kernel<128, 8>), grid, dim3(256), 0, st, x);
+    else hipLaunchKernelGGL((kv_image_kernel<128, 4>), grid, dim3(256), 0, st, x);
+  } else {
+    if (bits == 8) hipLaunchKernelGGL((kv_image_kernel<64, 8>), grid, dim3(256), 0, st, x);
+    else hipLaunchKernelGGL((kv_image_kernel<64, 4>), grid, dim3(256), 0, st, x);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
   const dim3 grid((unsigned)(x.rule.wgs * x.a.c.heads));
-#define TILE(D, B, N) hipLaunchKernelGGL((kv_tile_kernel<D, B, N>), grid, dim3(64 * N), 0, st, x)
-#define TILE_N(D, B)                     \
-  do {                                   \
-    if (x.rule.rt == 128) TILE(D, B, 2); \
-    else TILE(D, B, 4);                  \
+#define TILE(D, B, N, I) hipLaunchKernelGGL((kv_tile_kernel<D, B, N, I>), grid, dim3(64 * N), 0, st, x)
+#define TILE_N(D, B)                             \
+  do {                                           \
+    if (x.rule.rt == 128) TILE(D, B, 2, false);  \
+    else if (!x.image) TILE(D, B, 4, false);     \
+    else TILE(D, B, 4, true);                    \
   } while (0)
   if (head_dim == 128) {
     if (bits == 8) TILE_N(128, 8);
