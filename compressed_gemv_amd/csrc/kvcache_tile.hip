@@ -272,6 +272,12 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     limmin = lo < limmin ? lo : limmin;
   }
   limmin = __builtin_amdgcn_readfirstlane(limmin);
+  // The queries never change and only products read them: accumulation
+  // registers hold them, the vector unit's stay free.
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) asm volatile("" : "+a"(qf[n][s]));
 
   f32x16_t acc[2][DT], z[2];
   float m[2], l[2];
