@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
   _Pragma("unroll") for (int i_ = 0; i_ < 16; ++i_) {     \
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    \
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    \
-    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);    \
+    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    \
   }
 
 constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 1024, -1024
@@ -325,7 +325,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       for (int t = 0; t < DT; ++t)
         vf[s][t] = *reinterpret_cast<const f16x8_t*>(vread + buf * VBUF + t * 32 * VP + (4 * kb + 2 * s) * 16);
   };
-  // masks and the maximum of one block's logits (keys key .. key + 31)
+  float mx[2];                             // of a block's logits, its lane's
+  auto max_of = [&](const f32x16_t& v) {
+    float r = v[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) r = fmaxf(r, v[i]);
+    return r;
+  };
+  // masks, and the running maximum moved where it has to be (keys key .. key + 31)
   auto bounds = [&](auto blk, int key, uint32_t holes) {
     constexpr int n = decltype(blk)::value;
     if (key + 32 > limmin || holes) {
@@ -335,13 +342,11 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
         const bool vis = key + 8 * (i / 4) + 4 * hh + i % 4 < lim[n] && !((holes >> (i / 8)) & 1u);
         z[n][i] = vis ? z[n][i] : -INFINITY;
       }
+      mx[n] = max_of(z[n]);
     }
-    float mx = z[n][0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, z[n][i]);
-    mx *= cq[n];
-    if (__ballot(mx > m[n] + 8.0f)) {      // the maximum may lag by 8, as in the kernel for few rows
-      float v = fmaxf(mx, __shfl_xor(mx, 32));
+    if (__ballot(mx[n] * cq[n] > m[n] + 8.0f)) {   // the maximum may lag by 8, as in the kernel for few rows
+      float v = mx[n] * cq[n];
+      v = fmaxf(v, __shfl_xor(v, 32));
       v = fmaxf(v, m[n]);
       const float f = v == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - v);
       m[n] = v;
@@ -352,9 +357,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
         for (int i = 0; i < 16; ++i) acc[n][t][i] *= f;
     }
   };
-  // One turn: the softmax of block S against the products of the other block.
-  // READS: the operands for what follows, fetched as the products release them.
-  auto turn = [&](auto soft, auto&& after_pv, auto&& after_s) {
+  // One turn: the softmax of block n against the products of the other block,
+  // logits first, so that their maximum is there when the turn ends.
+  auto turn = [&](auto soft, auto&& after_s, auto&& after_pv) {
     constexpr int n = decltype(soft)::value, o = 1 - n;
     const float base = m[n] == -INFINITY ? 0.f : m[n];
     float pv[16];
@@ -363,14 +368,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     for (int i = 0; i < 16; ++i) zn[i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
+    for (int s = 0; s < STEPS; ++s) zn = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[s], qf[o][s], zn, 0, 0, 0);
+    after_s();
+#pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < DT; ++t)
         acc[o][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], __builtin_bit_cast(f16x8_t, p[o][s]), acc[o][t], 0, 0, 0);
     after_pv();
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) zn = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[s], qf[o][s], zn, 0, 0, 0);
-    after_s();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq[n], -base));
@@ -379,8 +384,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[n][e / 4][e % 4] = cvt_pk_f16(pv[2 * e], pv[2 * e + 1]);
     z[o] = zn;
-    // the weights are made here, not where they are used one turn later
-    asm volatile("" : "+v"(p[n][0]), "+v"(p[n][1]), "+v"(l[n]));
+    mx[o] = max_of(zn);
+    // the weights and the maximum are made here, not where they are used
+    asm volatile("" : "+v"(p[n][0]), "+v"(p[n][1]), "+v"(l[n]), "+v"(mx[o]));
     KV_SCHED
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -407,6 +413,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     // before the first keys: weights of zero, logits that add nothing
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[0][i] = z[1][i] = -INFINITY;
+    mx[0] = mx[1] = -INFINITY;
     read_k(0, 0);
     read_v(0, 0);
     int buf = 0, prev_holes = 0;
@@ -425,7 +432,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
         bounds(B{}, k - 32, kb == 0 ? (uint32_t)prev_holes : (holes >> (2 * kb - 2)) & 3u);
         turn(B{}, none, none);             // softmax B (before); O_A, S_A
         bounds(A{}, k, (holes >> (2 * kb)) & 3u);
-        turn(A{}, [&] { read_v(buf, kb); }, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); });
+        turn(A{}, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); }, [&] { read_v(buf, kb); });
         if constexpr (!IMAGE) {
           if (kb == KBS - 2 && more) dec.keys(key + KT, r, ksh + (buf ^ 1) * KBUF, gone[buf ^ 1]);
           if (kb == KBS - 1 && more) {
