@@ -813,8 +813,7 @@ def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = N
             if starts is not None:
                 raise ValueError("rows: missing, and no outputs given")
             rows = pages.shape[0]
-        K = torch.empty((rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device)
-        V = torch.empty((rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device)
+        K, V = torch.empty((2, rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device).unbind(0)
         fresh = (K, V)
     elif K is None or V is None:
         raise ValueError("K and V: both outputs or neither")

@@ -31,69 +31,103 @@ __device__ __forceinline__ uint32_t f16_down(uint32_t h) {
   return (h & 0x7FFFu) == 0u ? 0x8001u : ((h & 0x8000u) ? h + 1u : h - 1u);
 }
 
-// Constants and codes of a row, x the lane's 8 values of it.  The codes are
-// the fp64 definition's: t = (x - o) / s is formed in fp32 with an error below
-// 255 * 2^-22 < 2^-13, and a lane with a t closer than 2^-12 to a half-way
-// point takes its codes in fp64.
-template <int LPR, int BITS>
-__device__ __forceinline__ void quant_row(float (&x)[8], int lane, uint32_t (&q)[8], uint32_t* meta) {
+// 8 values of a lane as they come from memory.
+template <bool F32>
+struct Raw8 {
+  u32x4_t w[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load8(const void* p, int64_t elem) {
+  Raw8<F32> r;
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + elem * (F32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.w[i] = q[i];
+  return r;
+}
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// Constants and packed codes of a row, r the lane's 8 values of it.  The codes
+// are the fp64 definition's: t = (x - o) / s is formed in fp32 with an error
+// below 255 * 2^-22 < 2^-13, and a lane with a t closer than 2^-12 to a
+// half-way point takes its codes in fp64.  Bound by the vector unit until it
+// was cut to about 15 instructions a value: the checks for values that are not
+// finite or too large look at packed bits and leave the clamp to a branch, the
+// codes go from fp32 to bytes in one instruction each (4 bits: two codes make
+// one byte in fp32 first), and (max - o) / L is a product with 1 / L whose
+// rounding is put right by comparing s L with max - o, both exact in fp64.
+template <int LPR, int BITS, bool F32>
+__device__ __forceinline__ void quant_row(const Raw8<F32>& r, int lane, uint32_t (&q)[BITS / 4], uint32_t* meta) {
   constexpr float L = (float)((1 << BITS) - 1);
-  bool bad = false;
+  float x[8];
+  uint32_t big;                                   // largest magnitude, as bits; bf16: in the upper half
+  if constexpr (F32) {
+    big = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bad |= (__float_as_uint(x[i]) & 0x7F800000u) == 0x7F800000u;
-    x[i] = fminf(fmaxf(x[i], -kKvMax), kKvMax);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = r.w[i / 4][i % 4], m = u & 0x7FFFFFFFu;
+      x[i] = __uint_as_float(u);
+      big = m > big ? m : big;
+    }
+  } else {
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, r.w[0][i] & 0x7FFF7FFFu));
+      x[2 * i] = bf16_lo_to_f32(r.w[0][i]);
+      x[2 * i + 1] = bf16_hi_to_f32(r.w[0][i]);
+    }
+    big = (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
   }
-  const uint64_t rowmask = ((1ull << LPR) - 1ull) << (lane & ~(LPR - 1));
-  if (__ballot(bad) & rowmask) {
+  if (__ballot(big > 0x477F0000u)) {              // 65280: in some row of the wave
+    const uint64_t rowmask = ((1ull << LPR) - 1ull) << (lane & ~(LPR - 1));
+    if (__ballot(big >= 0x7F800000u) & rowmask) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = 0;
-    *meta = 0x7E007E00u;                          // s = o = NaN
-    return;
+      for (int i = 0; i < BITS / 4; ++i) q[i] = 0;
+      *meta = 0x7E007E00u;                        // s = o = NaN
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kKvMax), kKvMax);
   }
-  float mn = x[0], mx = x[0];
+  float mn = fminf(x[0], x[1]), mx = fmaxf(x[0], x[1]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) { mn = fminf(mn, x[i]); mx = fmaxf(mx, x[i]); }
+  for (int i = 2; i < 8; ++i) { mn = fminf(mn, x[i]); mx = fmaxf(mx, x[i]); }
   mn = row_reduce<LPR, false>(mn);
   mx = row_reduce<LPR, true>(mx);
   uint32_t ob = __builtin_bit_cast(uint16_t, (_Float16)mn);
   if (f16_bits_to_f32(ob) > mn) ob = f16_down(ob);
   if ((ob & 0x7FFFu) == 0u) ob = 0u;
   const float o = f16_bits_to_f32(ob);
-  const double v = ((double)mx - (double)o) / (double)L;
-  // two roundings, but the result lies within half a step (and a bit) of v
-  // on either side, so at most one step up reaches the smallest fp16 >= v
-  uint32_t sb = __builtin_bit_cast(uint16_t, (_Float16)(float)v) & 0x7FFFu;   // v >= 0; -0 becomes 0
-  if ((double)f16_bits_to_f32(sb) < v) sb = f16_up(sb);
+  const double d = (double)mx - (double)o;        // >= 0
+  // three roundings, but the result lies within half a step (and a bit) of
+  // d / L on either side, so at most one step up reaches the smallest fp16 >= d / L
+  uint32_t sb = __builtin_bit_cast(uint16_t, (_Float16)(float)(d * (1.0 / L))) & 0x7FFFu;   // -0 becomes 0
+  if ((double)(f16_bits_to_f32(sb) * L) < d) sb = f16_up(sb);
   const float s = f16_bits_to_f32(sb);
   *meta = sb | (ob << 16);
   const float rs = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
-  bool near = false;
-  float t[8];
+  float n[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    t[i] = (x[i] - o) * rs;
-    const float r = __builtin_rintf(t[i]);
-    near |= fabsf(t[i] - r) > 0.5f - 0x1p-12f;
-    q[i] = (uint32_t)(int)fminf(r, L);
+    const float t = (x[i] - o) * rs;              // 0 .. L
+    n[i] = __builtin_rintf(t);
+    far = fmaxf(far, fabsf(t - n[i]));
   }
-  if (near && s > 0.0f) {
+  if (far > 0.5f - 0x1p-12f && s > 0.0f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      q[i] = (uint32_t)(int)fmin(__builtin_rint(((double)x[i] - (double)o) / (double)s), (double)L);
+      n[i] = fminf((float)__builtin_rint(((double)x[i] - (double)o) / (double)s), L);
   }
-}
-
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t elem, float (&x)[8]) {
-  if constexpr (F32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + elem);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo_to_f32(v[i]); x[2 * i + 1] = bf16_hi_to_f32(v[i]); }
+  for (int i = 0; i < BITS / 4; ++i) q[i] = 0;
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i / 4] = __builtin_amdgcn_cvt_pk_u8_f32(n[i], i % 4, q[i / 4]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[0] = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_fmaf(n[2 * i + 1], 16.f, n[2 * i]), i, q[0]);
   }
 }
 
@@ -111,25 +145,14 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvView c, SeqView sv, con
   if (slot < 0) return;
   const int h0 = blockIdx.y * hpw, h1 = h0 + hpw < c.heads ? h0 + hpw : c.heads;
   for (int h = h0; h < h1; ++h) {
-    float x[2][8];
-    load8<F32>(K, t * k_stride + h * D + sub * 8, x[0]);
-    load8<F32>(V, t * v_stride + h * D + sub * 8, x[1]);
+    const Raw8<F32> x[2] = {load8<F32>(K, t * k_stride + h * D + sub * 8), load8<F32>(V, t * v_stride + h * D + sub * 8)};
     const int64_t row = cache_row(c, slot, h);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      uint32_t q[8], meta;
-      quant_row<LPR, BITS>(x[kv], lane, q, &meta);
-      if constexpr (BITS == 8) {
-        uint2 w;
-        w.x = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
-        w.y = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
-        *reinterpret_cast<uint2*>(c.codes[kv] + row * D + sub * 8) = w;
-      } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w |= q[i] << (4 * i);
-        *reinterpret_cast<uint32_t*>(c.codes[kv] + row * (D / 2) + sub * 4) = w;
-      }
+      uint32_t q[BITS / 4], meta;
+      quant_row<LPR, BITS, F32>(x[kv], lane, q, &meta);
+      if constexpr (BITS == 8) *reinterpret_cast<uint2*>(c.codes[kv] + row * D + sub * 8) = uint2{q[0], q[1]};
+      else *reinterpret_cast<uint32_t*>(c.codes[kv] + row * (D / 2) + sub * 4) = q[0];
       if (sub == 0) c.meta[kv][row] = meta;
     }
   }

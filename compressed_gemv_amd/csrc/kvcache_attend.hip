@@ -383,7 +383,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
 // ------------------------------------------------------------------- join
 // out = sum_c 2^(m_c - M) o_c over sum_c 2^(m_c - M) l_c, c the parts of a row.
 // All latency: D / 4 lanes hold a row, and a lane group takes its parts in
-// batches of 8 with all their loads in flight at once.
+// batches of 8 (or 4) with all their loads in flight at once.
 struct RowSum {
   float M, L;
   f32x4_t acc;
@@ -399,9 +399,8 @@ __device__ __forceinline__ void join2(RowSum& a, float M2, float L2, const f32x4
 }
 
 // Parts first, first + step, ... below n of one row; at(c): the partials and slot of part c, and the row in it.
-template <int D, typename AT>
+template <int D, int BATCH, typename AT>
 __device__ __forceinline__ RowSum sum_parts(AT at, int first, int step, int n, int h, int sub) {
-  constexpr int BATCH = 8;
   RowSum s{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
   for (int c0 = first; c0 < n; c0 += step * BATCH) {
     float mc[BATCH], lc[BATCH];
@@ -464,8 +463,8 @@ __device__ __forceinline__ void store_row(const KvAttend& a, const SeqRows& r, i
 }
 
 // The tiles that cuts go through: one workgroup per cut and KV head, the cuts
-// of one tile share its rows.  With few parts a wave joins a row; with many
-// (few rows then, one long sequence) all four waves do.
+// of one tile share its rows.  With few parts a lane group joins a row; with
+// many (few rows then, one long sequence) all four waves do.
 template <int D>
 __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
   constexpr int LPR = D / 4, GRP = 64 / LPR;
@@ -492,7 +491,7 @@ __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
         slot = c == 0 ? slot0 : 2 * (i0 + c);
         r = row;
       };
-      RowSum s = sum_parts<D>(at, wave * GRP + lane / LPR, 4 * GRP, parts, h, sub);
+      RowSum s = sum_parts<D, 8>(at, wave * GRP + lane / LPR, 4 * GRP, parts, h, sub);
       join_groups<D>(s);
       if (lane < LPR) *reinterpret_cast<f32x4_t*>(&os[wave][4 * sub]) = s.acc;
       if (lane == 0) { mls[wave][0] = s.M; mls[wave][1] = s.L; }
@@ -504,16 +503,15 @@ __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
       }
       __syncthreads();
     }
-  } else {
-    for (int row = 4 * k + wave; row < n; row += 4 * sharers) {
+  } else {                                 // a lane group for each row
+    for (int row = (4 * k + wave) * GRP + lane / LPR; row < n; row += 4 * sharers * GRP) {
       auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
         px = &x;
         slot = c == 0 ? slot0 : 2 * (i0 + c);
         r = row;
       };
-      RowSum s = sum_parts<D>(at, lane / LPR, GRP, parts, h, sub);
-      join_groups<D>(s);
-      if (lane < LPR) store_row<D>(a, t.r, row0 + row, h, sub, s);
+      const RowSum s = sum_parts<D, 4>(at, 0, 1, parts, h, sub);
+      store_row<D>(a, t.r, row0 + row, h, sub, s);
     }
   }
 }
@@ -548,7 +546,7 @@ __global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, Att
       slot = p ? p0 + pt + c : slot0 + c - np;
       r = p ? prow : R - row0;
     };
-    RowSum s = sum_parts<D>(at, lane / LPR, GRP, np + parts, h, sub);
+    RowSum s = sum_parts<D, 8>(at, lane / LPR, GRP, np + parts, h, sub);
     join_groups<D>(s);
     if (lane < LPR) store_row<D>(a, t.r, R, h, sub, s);
   }
@@ -581,6 +579,9 @@ namespace {
 // kernel for few rows, one of the other.
 constexpr int kRowWorkgroups = 512;
 constexpr int kTileWorkgroups = 256;
+// Page tables of up to so many positions leave their tiles whole: a second
+// launch to join parts would cost more than the keys.
+constexpr int kWholeKeys = 768;
 
 // Keys are decoded beforehand where at least this many rows of a sequence meet
 // them (4 tiles) and the images, sized for full page tables, fit this many bytes.
@@ -601,7 +602,7 @@ struct CallPlan {
 
 // Tile height and workgroups by the rows a KV head has against one run of
 // keys, at most `tiles` tiles of at most cap keys.
-SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap) {
+SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
   SplitRule r{};
   r.group = group;
   r.rt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
@@ -609,7 +610,8 @@ SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, in
   r.cap = cap;
   r.sloped = r.rt > 32;
   r.grain = r.sloped && cap > r.ku ? 1 : kSub;
-  const int64_t most = (total_rows / r.rt + seqs) * ceil_div(cap > 0 ? cap : 1, r.ku);   // steps of keys, at most
+  r.whole = r.rt <= 32 && cap <= kWholeKeys && !must_cut;
+  const int64_t most = (total_rows / r.rt + seqs) * (r.whole ? 1 : ceil_div(cap > 0 ? cap : 1, r.ku));   // steps of keys, at most
   int64_t n = (r.rt > 32 ? kTileWorkgroups : kRowWorkgroups) / heads;
   if (n > most) n = most;
   r.wgs = (int)(n < 1 ? 1 : n);
@@ -620,14 +622,14 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
                    int64_t prefix_len) {
   CallPlan p{};
   const int64_t cap = max_pages << page_shift;
-  p.own = rule_for(ceil_div(T, B) * group, T * group, B, group, heads, (int)cap);
+  p.own = rule_for(ceil_div(T, B) * group, T * group, B, group, heads, (int)cap, false);
   const int64_t tiles = T * group / p.own.rt + B;           // at most, over all sequences
   p.shared = prefix_len > 0;
   p.own_slots = p.shared ? p.own.wgs + tiles : 2 * p.own.wgs;
-  p.join = p.shared || (cap > p.own.ku && p.own.wgs > 1);   // a tile of one step is never cut
+  p.join = p.shared || (cap > p.own.ku && !p.own.whole && p.own.wgs > 1);   // a tile of one step is never cut
   if (!p.join) p.own_slots = 0;
   if (p.shared) {
-    p.pre = rule_for(T * group, T * group, 1, group, heads, (int)prefix_len);
+    p.pre = rule_for(T * group, T * group, 1, group, heads, (int)prefix_len, true);
     p.pre.sloped = false;                                   // every row sees all of it
     p.pre.grain = kSub;
     p.pre_slots = p.pre.wgs + ceil_div(T * group, p.pre.rt);
@@ -685,7 +687,7 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
     if (head_dim == 128) hipLaunchKernelGGL((kv_join_prefix_kernel<128>), grid, dim3(256), 0, st, own, pre, rpw);
     else hipLaunchKernelGGL((kv_join_prefix_kernel<64>), grid, dim3(256), 0, st, own, pre, rpw);
   } else {
-    const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads), (unsigned)ceil_div(own.rule.rt, 32));
+    const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads), (unsigned)ceil_div(own.rule.rt, 64));
     if (head_dim == 128) hipLaunchKernelGGL((kv_join_cuts_kernel<128>), grid, dim3(256), 0, st, own);
     else hipLaunchKernelGGL((kv_join_cuts_kernel<64>), grid, dim3(256), 0, st, own);
   }

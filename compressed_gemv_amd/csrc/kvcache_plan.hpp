@@ -24,6 +24,7 @@ struct SplitRule {
   int group, rt, ku;           // query heads per KV head, rows per tile, keys per step
   int wgs;                     // workgroups per KV head in the grid
   int cap;                     // positions the page table holds
+  bool whole;                  // tiles are never cut: each weighs one step
   bool sloped;                 // weigh a sequence's tiles by what each sees
   int grain;                   // cuts lie at multiples of this weight; kSub where all tiles weigh
                                // whole steps, so that a tile of one step is never cut
@@ -66,7 +67,7 @@ __device__ __forceinline__ Weights weights_of(const SplitRule& p, const SeqRows&
   w.tiles = (int)(((int64_t)r.count * p.group + p.rt - 1) / p.rt);
   const int step = p.ku / kSub;
   const int full = (r.need + p.ku - 1) / p.ku * kSub;     // of a tile that sees all
-  w.A = full < kSub ? kSub : full;
+  w.A = full < kSub || p.whole ? kSub : full;
   w.S = 0;
   if (p.sloped && w.tiles > 1) {
     const int s = p.rt / p.group / step;

@@ -491,7 +491,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       ml[1] = l[n];
     }
   }
-  __syncthreads();                         // LDS is free for the next tile
+  // the last step's barrier has freed the LDS for the next tile
   }
 }
 
