@@ -159,8 +159,8 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
   // rows of one KV head are counted in 32 bits
   const int64_t rows = s->T * (q_heads / c->heads);
   if (rows > (1 << 30)) return Q_EUNSUPPORTED;
-  // weights of the line of work stay below 2^52: 16 per 128 keys of a tile of 16 rows or more
-  if ((double)(rows / 16 + s->B) * (double)((s->max_pages * c->page_size + prefix_len) / 8 + 16) * 512.0 > 4e15)
+  // weights of the line of work times 512 pieces stay below 2^52: half a weight for a key of a tile of 8 rows or more
+  if ((double)(rows / 8 + s->B) * (double)((s->max_pages * c->page_size + prefix_len) / 2 + 512) * 512.0 > 4e15)
     return Q_EUNSUPPORTED;
   *ws_bytes = qg::kv_attend_ws_bytes(s->B, s->T, s->max_pages, __builtin_ctz((unsigned)c->page_size), c->heads, q_heads / c->heads, c->head_dim, prefix_len);
   return Q_OK;

@@ -26,9 +26,9 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // fp16 times fp32 in one instruction (v_fma_mix_f32; a plain product would convert first)
 __device__ __forceinline__ float mix_mul(float h, float x) { return __builtin_fmaf(h, x, 0.f); }
 
-// bf16 pair times 2^64
-__device__ __forceinline__ uint32_t up_pair(uint32_t w) {
-  const float lo = bf16_lo_to_f32(w) * kUp, hi = bf16_hi_to_f32(w) * kUp;
+// bf16 pair times a power of two
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, float f) {
+  const float lo = bf16_lo_to_f32(w) * f, hi = bf16_hi_to_f32(w) * f;
   return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xFFFF0000u);
 }
 
@@ -39,16 +39,21 @@ __device__ __forceinline__ V ld_nt(const uint8_t* base, uint32_t off) {
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// A workgroup goes through the tiles (16 NT rows) of its piece; its four waves
+// A workgroup goes through the tiles (RT rows) of its piece; its four waves
 // take a quarter of a tile's keys each, 32 keys a step.  Lane l, r = l % 16, kg = l / 16:
 //   K operand: key r, a quarter kg of the coordinates, straight from memory
 //   logits:    query r, keys 4 kg .. 4 kg + 3 of both halves of the step
 //   V operand: coordinates r D/16 .. of exactly those eight keys (the order of
 //              the contraction is free), so the weights never leave their lane
-// The row constants of a lane's eight keys come with four 16-byte loads.
-template <int D, int BITS, int NT>
-__global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(AttendArgs x) {
-  constexpr int RT = 16 * NT;
+// A lane brings in the constants of one key (K's in lanes 0 .. 31, V's in the
+// others); they go round through 256 bytes of LDS while the logits are formed.
+// RT = 8 (one token of a group of up to 8 heads): both halves of the 16 columns
+// hold the same rows, one with the high and one with the low parts of the
+// weights, so that one product does for two.
+template <int D, int BITS, int RT>
+__global__ __launch_bounds__(256, (RT > 16 ? 2 : 1) * D > 128 ? 1 : 2) void kv_rows_kernel(AttendArgs x) {
+  constexpr int NT = RT > 16 ? 2 : 1;
+  constexpr bool PACK = RT == 8;
   constexpr int ROWB = D * BITS / 8;       // bytes of a cache row
   constexpr int KB = ROWB / 4;             // bytes of a K row per lane
   constexpr int KW = KB / 4;
@@ -58,6 +63,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
   constexpr int PITCH = D + 4;
   __shared__ __align__(16) float os[4][RT][PITCH];
   __shared__ float ms[4][RT], ls[4][RT];
+  __shared__ __align__(16) uint32_t consts[4][64];
   const KvAttend& a = x.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
@@ -93,18 +99,20 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
   struct Raw {
     uint32_t k[2][KW];
     uint32_t v[8][VW];
-    u32x4_t km[2], vm[2];
+    uint32_t mt;                           // constants of K's key lane, of V's key lane - 32
     int bad;                               // halves whose page is not in the cache
   };
   auto load = [&](int key, Raw& w_) {
     if (((key + 16) >> shift) - pbase >= 64) refill(key >> shift);
     w_.bad = 0;
+    int64_t rows[2];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int kk = key + 16 * hf;
       const int id = __builtin_amdgcn_readlane(ids, (kk >> shift) - pbase);
       if (id < 0) w_.bad |= 1 << hf;
       const int64_t row = (((int64_t)(id < 0 ? 0 : id) * heads + h) << shift) + (kk & pmask);
+      rows[hf] = row;
       const uint8_t* kc = a.c.codes[0] + row * ROWB;
       const uint8_t* vc = a.c.codes[1] + row * ROWB;
       if constexpr (KB == 32) {
@@ -133,9 +141,9 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
           w_.v[4 * hf + i][0] = ld_nt<uint16_t>(vc, off);
         }
       }
-      w_.km[hf] = *reinterpret_cast<const u32x4_t*>(a.c.meta[0] + row + 4 * kg);
-      w_.vm[hf] = *reinterpret_cast<const u32x4_t*>(a.c.meta[1] + row + 4 * kg);
     }
+    const uint32_t* mp = lane < 32 ? a.c.meta[0] : a.c.meta[1];
+    w_.mt = mp[((lane & 16) ? rows[1] : rows[0]) + r];
   };
 
   // the first keys are on their way while the queries are made ready
@@ -154,7 +162,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
   const float c0 = a.scale * 1.4426950408889634f, c1 = c0 * kCode;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int row = w.row0 + 16 * n + r;
+    const int row = w.row0 + (PACK ? r % 8 : 16 * n + r);
     const bool ok = row < w.rows;
     const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
     const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D;
@@ -168,14 +176,16 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sum += bf16_lo_to_f32(v[e]) + bf16_hi_to_f32(v[e]);
-        v[e] = up_pair(v[e]);
+        v[e] = scale_pair(v[e], kUp);
       }
-      if constexpr (BITS == 4) {           // pairs (j, j + 4), as a nibble mask leaves them
-        const u32x4_t t = v;
+      if constexpr (BITS == 4) {           // pairs (j, j + 4), as a nibble mask leaves them; odd nibbles
+        const u32x4_t t = v;               // stay where they are, as 16 times their code
         v[0] = __builtin_amdgcn_perm(t[2], t[0], 0x05040100u);
         v[1] = __builtin_amdgcn_perm(t[2], t[0], 0x07060302u);
         v[2] = __builtin_amdgcn_perm(t[3], t[1], 0x05040100u);
         v[3] = __builtin_amdgcn_perm(t[3], t[1], 0x07060302u);
+        v[1] = scale_pair(v[1], 0x1p-4f);
+        v[3] = scale_pair(v[3], 0x1p-4f);
       }
       qf[n][s] = v;
     }
@@ -190,7 +200,18 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
   }
   limmin = __builtin_amdgcn_readfirstlane(limmin);
 
+  const float low = r < 8 ? 0.f : -1.f;    // PACK: which part of the weights this lane's column holds
   auto compute = [&](int key, const Raw& w_) {
+    u32x4_t km[2], vmr[2];                 // of this lane's keys 4 kg .. + 3 of both halves
+    consts[wave][lane] = w_.mt;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      km[hf] = *reinterpret_cast<const u32x4_t*>(&consts[wave][16 * hf + 4 * kg]);
+      vmr[hf] = *reinterpret_cast<const u32x4_t*>(&consts[wave][32 + 16 * hf + 4 * kg]);
+    }
     f32x4_t z[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -209,7 +230,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = (w_.k[hf][s] >> (4 * e)) & 0x000F000Fu;
+          for (int e = 0; e < 4; ++e) f[e] = (w_.k[hf][s] >> (8 * (e / 2))) & (e % 2 ? 0x00F000F0u : 0x000F000Fu);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -228,8 +249,8 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t km = w_.km[j / 4][j % 4];
-        t[n][j] = __builtin_fmaf(z[n][j / 4][j % 4], mix_mul(f16_lo(km), c1), mix_mul(f16_hi(km), qs[n]));
+        const uint32_t kc = km[j / 4][j % 4];
+        t[n][j] = __builtin_fmaf(z[n][j / 4][j % 4], mix_mul(f16_lo(kc), c1), mix_mul(f16_hi(kc), qs[n]));
       }
       if (masked) {
         asm volatile("");                  // a branch: the selects must not run in every step
@@ -266,7 +287,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
       const float base = m[n] == -INFINITY ? 0.f : m[n] - 64.0f;
       uint32_t vm[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) vm[j] = w_.vm[j / 4][j % 4];
+      for (int j = 0; j < 8; ++j) vm[j] = vmr[j / 4][j % 4];
       if (masked) {                        // constants of slots that are not seen may be anything
         asm volatile("");
 #pragma unroll
@@ -283,7 +304,11 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         wh[n][e] = cvt_pk_bf16(wv[2 * e], wv[2 * e + 1]);
-        wl[n][e] = cvt_pk_bf16(wv[2 * e] - bf16_lo_to_f32(wh[n][e]), wv[2 * e + 1] - bf16_hi_to_f32(wh[n][e]));
+        if constexpr (PACK)                // columns 8 .. 15: what the high part leaves
+          wh[n][e] = cvt_pk_bf16(__builtin_fmaf(low, bf16_lo_to_f32(wh[n][e]), wv[2 * e]),
+                                 __builtin_fmaf(low, bf16_hi_to_f32(wh[n][e]), wv[2 * e + 1]));
+        else
+          wl[n][e] = cvt_pk_bf16(wv[2 * e] - bf16_lo_to_f32(wh[n][e]), wv[2 * e + 1] - bf16_hi_to_f32(wh[n][e]));
       }
     }
     u32x4_t pair = {0u, 0u, 0u, 0u};       // 4 bits: the halves of the current four coordinates
@@ -298,15 +323,16 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
         } else {
           if (q % 4 == 0)
             pair[e] = __builtin_amdgcn_perm(w_.v[2 * e + 1][0], w_.v[2 * e][0], q == 0 ? 0x05040100u : 0x07060302u);
-          f[e] = (pair[e] >> (4 * (q % 4))) & 0x000F000Fu;
+          f[e] = (pair[e] >> (8 * (q % 4 / 2))) & (q % 2 ? 0x00F000F0u : 0x000F000Fu);
         }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         acc[n][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f),
                                                             __builtin_bit_cast(bf16x8_t, wh[n]), acc[n][q], 0, 0, 0);
-        acc[n][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f),
-                                                            __builtin_bit_cast(bf16x8_t, wl[n]), acc[n][q], 0, 0, 0);
+        if constexpr (!PACK)
+          acc[n][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                              __builtin_bit_cast(bf16x8_t, wl[n]), acc[n][q], 0, 0, 0);
       }
     }
   };
@@ -334,11 +360,18 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
     l[n] += __shfl_xor(l[n], 32);
     po[n] += __shfl_xor(po[n], 16);
     po[n] += __shfl_xor(po[n], 32);
-    if (kg == 0) ms[wave][16 * n + r] = m[n];
+    if constexpr (PACK) {                  // high and low parts meet
+#pragma unroll
+      for (int q = 0; q < TILES; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][q][i] += dpp_f32<0x128>(acc[n][q][i]);   // row_ror:8
+    }
+    if (kg == 0 && (!PACK || r < 8)) ms[wave][16 * n + r] = m[n];
   }
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
+    if (PACK && r >= 8) continue;
     const int row = 16 * n + r;
     const float mm = fmaxf(fmaxf(ms[0][row], ms[1][row]), fmaxf(ms[2][row], ms[3][row]));
     const float f = m[n] == -INFINITY ? 0.f : exp2_hw(m[n] - mm);
@@ -349,7 +382,7 @@ __global__ __launch_bounds__(256, NT * D > 128 ? 1 : 2) void kv_rows_kernel(Atte
       for (int q = 0; q < TILES; q += 4) {
         f32x4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (acc[n][q + e][i] * kCode + po[n] * kDown) * f;
+        for (int e = 0; e < 4; ++e) v[e] = (acc[n][q + e][i] * (BITS == 4 && e % 2 ? kCode / 16 : kCode) + po[n] * kDown) * f;
         *reinterpret_cast<f32x4_t*>(&os[wave][row][TILES * (4 * kg + i) + q]) = v;
       }
   }
@@ -555,11 +588,12 @@ __global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, Att
 // ------------------------------------------------------------------ launch
 hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
   const dim3 grid((unsigned)(x.rule.wgs * x.a.c.heads));
-#define ROWS(D, B, N) hipLaunchKernelGGL((kv_rows_kernel<D, B, N>), grid, dim3(256), 0, st, x)
-#define ROWS_N(D, B)                   \
-  do {                                 \
-    if (x.rule.rt == 16) ROWS(D, B, 1); \
-    else ROWS(D, B, 2);                \
+#define ROWS(D, B, R) hipLaunchKernelGGL((kv_rows_kernel<D, B, R>), grid, dim3(256), 0, st, x)
+#define ROWS_N(D, B)                          \
+  do {                                        \
+    if (x.rule.rt == 8) ROWS(D, B, 8);        \
+    else if (x.rule.rt == 16) ROWS(D, B, 16); \
+    else ROWS(D, B, 32);                      \
   } while (0)
   if (head_dim == 128) {
     if (bits == 8) ROWS_N(128, 8);
@@ -579,10 +613,16 @@ namespace {
 // kernel for few rows, one of the other.
 constexpr int kRowWorkgroups = 512;
 constexpr int kTileWorkgroups = 256;
+#ifndef KLOW
+#define KLOW 128
+#endif
+constexpr int kLow = KLOW;
 // Page tables of up to so many positions leave their tiles whole: a second
 // launch to join parts would cost more than the keys.
 constexpr int kWholeKeys = 768;
-
+// What a tile costs beside its keys, in steps of keys / kSub: about two steps
+// of either kernel (4 us; 12 us of the tile kernel's 4.4 us a step).
+constexpr int kRowsExtra = 128, kTileExtra = 128;
 // Keys are decoded beforehand where at least this many rows of a sequence meet
 // them (4 tiles) and the images, sized for full page tables, fit this many bytes.
 constexpr int64_t kImageRows = 1024;
@@ -605,14 +645,14 @@ struct CallPlan {
 SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
   SplitRule r{};
   r.group = group;
-  r.rt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  r.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kLow ? 128 : 256;
   r.ku = 128;
   r.cap = cap;
   r.sloped = r.rt > 32;
-  r.grain = r.sloped && cap > r.ku ? 1 : kSub;
-  r.whole = r.rt <= 32 && cap <= kWholeKeys && !must_cut;
+  r.whole = !must_cut && cap <= (r.rt <= 32 ? kWholeKeys : r.ku);
+  r.extra = r.whole || must_cut ? 0 : r.rt <= 32 ? kRowsExtra : kTileExtra;
   const int64_t most = (total_rows / r.rt + seqs) * (r.whole ? 1 : ceil_div(cap > 0 ? cap : 1, r.ku));   // steps of keys, at most
-  int64_t n = (r.rt > 32 ? kTileWorkgroups : kRowWorkgroups) / heads;
+  int64_t n = (r.rt == 256 ? kTileWorkgroups : kRowWorkgroups) / heads;
   if (n > most) n = most;
   r.wgs = (int)(n < 1 ? 1 : n);
   return r;
@@ -626,15 +666,14 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   const int64_t tiles = T * group / p.own.rt + B;           // at most, over all sequences
   p.shared = prefix_len > 0;
   p.own_slots = p.shared ? p.own.wgs + tiles : 2 * p.own.wgs;
-  p.join = p.shared || (cap > p.own.ku && !p.own.whole && p.own.wgs > 1);   // a tile of one step is never cut
+  p.join = p.shared || (!p.own.whole && p.own.wgs > 1);
   if (!p.join) p.own_slots = 0;
   if (p.shared) {
     p.pre = rule_for(T * group, T * group, 1, group, heads, (int)prefix_len, true);
     p.pre.sloped = false;                                   // every row sees all of it
-    p.pre.grain = kSub;
     p.pre_slots = p.pre.wgs + ceil_div(T * group, p.pre.rt);
-    p.pre_line = Line{ceil_div(T * group, p.pre.rt) * ceil_div(prefix_len, p.pre.ku), p.pre.wgs, kSub};
-    if (p.pre_line.U < p.pre_line.N) p.pre_line.N = (int)p.pre_line.U;
+    p.pre_line = Line{ceil_div(T * group, p.pre.rt) * ceil_div(prefix_len, p.pre.ku) * kSub, p.pre.wgs, 1};
+    if (p.pre_line.U / kSub < p.pre_line.N) p.pre_line.N = (int)(p.pre_line.U / kSub);
   }
   if (p.own.rt == 256 && ceil_div(T, B) * group >= kImageRows) {
     p.images = B * ceil_div(cap, 128);

@@ -4,8 +4,9 @@
 //
 // A KV head's rows of one sequence are its tokens times `group` query heads,
 // row = token * group + g; they are cut into tiles of RT rows.  Tile t of a
-// sequence weighs A + S t, about the keys it sees in steps of KU / 16 (later
-// tokens see more, so S > 0 where a tile holds a good part of a step).  All
+// sequence weighs A + S t, about the keys it sees in steps of KU / 64 (later
+// tokens see more, so S > 0 where a tile holds a good part of a step) and what
+// starting and ending a tile costs.  All
 // tiles of the batch form one line of U weights per KV head, which is cut into
 // N equal pieces, one per workgroup, wherever the cuts fall: no workgroup has
 // more to do than another, however unequal the sequences are.  A tile that a
@@ -18,7 +19,7 @@
 
 namespace qg {
 
-constexpr int kSub = 16;       // weight of KU keys
+constexpr int kSub = 64;       // weight of KU keys
 
 struct SplitRule {
   int group, rt, ku;           // query heads per KV head, rows per tile, keys per step
@@ -26,8 +27,7 @@ struct SplitRule {
   int cap;                     // positions the page table holds
   bool whole;                  // tiles are never cut: each weighs one step
   bool sloped;                 // weigh a sequence's tiles by what each sees
-  int grain;                   // cuts lie at multiples of this weight; kSub where all tiles weigh
-                               // whole steps, so that a tile of one step is never cut
+  int extra;                   // weight of what a tile costs beside its keys
 };
 
 struct SeqRows {
@@ -75,6 +75,7 @@ __device__ __forceinline__ Weights weights_of(const SplitRule& p, const SeqRows&
     if (first >= kSub) { w.S = s; w.A = (int)first; }
     else { w.S = (w.A - kSub) / (w.tiles - 1); w.A -= w.S * (w.tiles - 1); }
   }
+  w.A += p.extra;
   return w;
 }
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // The cut line.  Quotients go through fp64: with all products below 2^52 the
 // rounded quotient never reaches the next integer.
 struct Line {
-  int64_t U;                   // in grains
+  int64_t U;                   // in grains: kSub where tiles are not cut, else 1
   int N, grain;
   __device__ __forceinline__ int64_t cut(int i) const {
     return uniform((int64_t)((double)i * (double)U / (double)N)) * grain;
@@ -128,8 +129,8 @@ __device__ __forceinline__ Line line_of(const SeqView& s, const SplitRule& p, in
   }
   Line l;
   u = lane_i64(wave_scan(u), 63);
-  l.grain = p.grain;
-  l.U = p.grain == 1 ? u : u / kSub;
+  l.grain = p.whole ? kSub : 1;
+  l.U = p.whole ? u / kSub : u;
   const int64_t n = u / kSub;                              // a piece is a step of keys at least
   l.N = n < p.wgs ? (int)n : p.wgs;
   if (l.N < 1) l.N = 1;

@@ -416,7 +416,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     mx[0] = mx[1] = -INFINITY;
     read_k(0, 0);
     read_v(0, 0);
-    int buf = 0, prev_holes = 0;
+    int buf = 0;
+    uint32_t before = 0;                   // holes of the 32 keys before
     for (int key = w.k0; key < w.k1; key += KT, buf ^= 1) {
       uint32_t holes = 0;
 #pragma unroll
@@ -429,9 +430,11 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
 #pragma unroll
       for (int kb = 0; kb < KBS; ++kb) {
         const int k = key + 32 * kb;
-        bounds(B{}, k - 32, kb == 0 ? (uint32_t)prev_holes : (holes >> (2 * kb - 2)) & 3u);
+        if (kb > 0 && k >= w.k1) break;    // the last step's keys may end early
+        bounds(B{}, k - 32, before);
+        before = (holes >> (2 * kb)) & 3u;
         turn(B{}, none, none);             // softmax B (before); O_A, S_A
-        bounds(A{}, k, (holes >> (2 * kb)) & 3u);
+        bounds(A{}, k, before);
         turn(A{}, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); }, [&] { read_v(buf, kb); });
         if constexpr (!IMAGE) {
           if (kb == KBS - 2 && more) dec.keys(key + KT, r, ksh + (buf ^ 1) * KBUF, gone[buf ^ 1]);
@@ -444,13 +447,11 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
           }
         }
       }
-      prev_holes = (int)((holes >> (2 * KBS - 2)) & 3u);
       __syncthreads();
       if (more) read_k(buf ^ 1, 0);
     }
     // what is left: the last keys' products and block B's softmax
-    const int last = w.k0 + (w.k1 - w.k0 + KT - 1) / KT * KT - 32;
-    bounds(B{}, last, (uint32_t)prev_holes);
+    bounds(B{}, w.k0 + (w.k1 - w.k0 + 31) / 32 * 32 - 32, before);
     turn(B{}, none, none);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
