@@ -140,12 +140,21 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvView c, SeqView sv, con
   const int lane = threadIdx.x & 63, sub = threadIdx.x % LPR;
   const int t = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
   if (t >= sv.T) return;                           // whole row groups leave together
+  const int h0 = blockIdx.y * hpw, h1 = h0 + hpw < c.heads ? h0 + hpw : c.heads;
+  // the rows are on their way while the token's place is looked up, and the
+  // next head's while this one's codes are made
+  auto rows = [&](int h, Raw8<F32> (&x)[2]) {
+    x[0] = load8<F32>(K, t * k_stride + h * D + sub * 8);
+    x[1] = load8<F32>(V, t * v_stride + h * D + sub * 8);
+  };
+  Raw8<F32> next[2];
+  rows(h0, next);
   bool owned;
   const int64_t slot = slot_of_row<LPR>(c, sv, t, sub, lane, &owned);
   if (slot < 0) return;
-  const int h0 = blockIdx.y * hpw, h1 = h0 + hpw < c.heads ? h0 + hpw : c.heads;
   for (int h = h0; h < h1; ++h) {
-    const Raw8<F32> x[2] = {load8<F32>(K, t * k_stride + h * D + sub * 8), load8<F32>(V, t * v_stride + h * D + sub * 8)};
+    const Raw8<F32> x[2] = {next[0], next[1]};
+    if (h + 1 < h1) rows(h + 1, next);
     const int64_t row = cache_row(c, slot, h);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {

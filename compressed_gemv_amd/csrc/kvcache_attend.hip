@@ -613,10 +613,6 @@ namespace {
 // kernel for few rows, one of the other.
 constexpr int kRowWorkgroups = 512;
 constexpr int kTileWorkgroups = 256;
-#ifndef KLOW
-#define KLOW 128
-#endif
-constexpr int kLow = KLOW;
 // Page tables of up to so many positions leave their tiles whole: a second
 // launch to join parts would cost more than the keys.
 constexpr int kWholeKeys = 768;
@@ -645,7 +641,7 @@ struct CallPlan {
 SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
   SplitRule r{};
   r.group = group;
-  r.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kLow ? 128 : 256;
+  r.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
   r.ku = 128;
   r.cap = cap;
   r.sloped = r.rt > 32;
