@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256, (RT > 16 ? 2 : 1) * D > 128 ? 1 : 2) void kv_r
   const int heads = a.c.heads, h = blockIdx.x % heads;
   Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
   Work w;
-  while (next_work(x, pieces, w, lane)) {
+  while (next_work<false>(x, pieces, w, lane)) {
   f32x4_t acc[NT][TILES];
   float m[NT], l[NT], po[NT];              // maximum, sum of weights, sum of weights times offsets
 #pragma unroll
@@ -617,8 +617,8 @@ constexpr int kTileWorkgroups = 256;
 // launch to join parts would cost more than the keys.
 constexpr int kWholeKeys = 768;
 // What a tile costs beside its keys, in steps of keys / kSub: about two steps
-// of either kernel (4 us; 12 us of the tile kernel's 4.4 us a step).
-constexpr int kRowsExtra = 128, kTileExtra = 128;
+// of the kernel for few rows (4 us), one and a half of the other's 4 us.
+constexpr int kRowsExtra = 128, kTileExtra = 96;
 // Keys are decoded beforehand where at least this many rows of a sequence meet
 // them (4 tiles) and the images, sized for full page tables, fit this many bytes.
 constexpr int64_t kImageRows = 1024;
@@ -649,6 +649,7 @@ SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, in
   r.extra = r.whole || must_cut ? 0 : r.rt <= 32 ? kRowsExtra : kTileExtra;
   const int64_t most = (total_rows / r.rt + seqs) * (r.whole ? 1 : ceil_div(cap > 0 ? cap : 1, r.ku));   // steps of keys, at most
   int64_t n = (r.rt == 256 ? kTileWorkgroups : kRowWorkgroups) / heads;
+  r.single = r.whole && n >= most;
   if (n > most) n = most;
   r.wgs = (int)(n < 1 ? 1 : n);
   return r;

@@ -20,7 +20,7 @@ struct AttendArgs {
 
 // Wave-uniform description of one tile's part in one piece.
 struct Work {
-  int slot;                    // partial slot
+  int slot;                    // partial slot, of a tile that is not direct
   int row0, rows;              // first row (token * group + g) of the tile and rows of the sequence in all
   int t0, vis0;
   int k0, k1;                  // keys of this part that some row of the tile may see
@@ -36,13 +36,23 @@ struct Pieces {
   Line line;
   int piece;
   int64_t x, end;              // weights still to do
+  TileAt t;                    // the last tile; b < 0: none yet
 };
 
 __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int lane) {
   Pieces p;
+  if (x.rule.single) {                     // found without a look at the other sequences' weights
+    p.line = Line{};
+    p.piece = piece;
+    p.x = (int64_t)piece * kSub;
+    p.end = p.x + kSub;
+    p.t.b = -1;
+    return p;
+  }
   p.line = x.s.lens ? line_of(x.s, x.rule, lane) : x.line;
   p.piece = piece;
   p.x = p.end = 0;
+  p.t.b = -1;
   if (piece < p.line.N) {
     p.x = p.line.cut(piece);
     p.end = p.line.cut(piece + 1);
@@ -50,15 +60,18 @@ __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int 
   return p;
 }
 
-template <bool STEPS = false>
+// ADVANCE: from tile to tile of a sequence without a search, for which a piece
+// of many tiles keeps more state (a prompt's tiles 267 -> 251 us; the kernel for
+// few rows, whose tiles are mostly sequences, is 1 % slower with it).
+template <bool ADVANCE, bool STEPS = false>
 __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& w, int lane) {
   while (p.x < p.end) {
-    const TileAt t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane);
+    if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane);
+    const TileAt& t = p.t;
     if (t.b < 0) return false;
     w.steps = t.steps;
     const int64_t from = p.x;
     const bool whole = t.lo >= from && t.hi <= p.end;
-    const int64_t slot = slot_of(p.line, t, p.piece, x.keep);
     w.t0 = t.r.t0;
     w.rows = t.r.count * x.a.group;
     w.vis0 = t.r.vis0;
@@ -67,7 +80,6 @@ __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& 
     w.direct = whole && !x.keep;
     w.pages = x.s.pages + (int64_t)t.b * x.s.max_pages;
     w.max_pages = x.s.max_pages;
-    w.slot = (int)slot;
     w.row0 = t.tile * x.rule.rt;
     // the last row of the tile sees the most
     int last = w.row0 + x.rule.rt - 1;
@@ -86,7 +98,10 @@ __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& 
     w.k1 = u1 * x.rule.ku < vis ? u1 * x.rule.ku : vis;
     if (w.k0 > w.k1) w.k0 = w.k1;
     p.x = t.hi;
-    if (w.direct || slot < x.part.slots) return true;
+    if (w.direct) return true;
+    const int64_t slot = slot_of(p.line, t, p.piece, x.keep);
+    w.slot = (int)slot;
+    if (slot < x.part.slots) return true;
   }
   return false;
 }
@@ -107,8 +122,9 @@ __device__ __forceinline__ float* part_ml(const AttendArgs& x, int slot, int h, 
 }
 
 // Four neighbouring outputs of a row.
+template <bool F32>
 __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const f32x4_t& v) {
-  if (a.out_f32) {
+  if constexpr (F32) {
     *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + at) = v;
   } else {
     uint2 p;
@@ -116,6 +132,10 @@ __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const 
     p.y = cvt_pk_bf16(v[2], v[3]);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = p;
   }
+}
+__device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const f32x4_t& v) {
+  if (a.out_f32) store_out4<true>(a, at, v);
+  else store_out4<false>(a, at, v);
 }
 
 hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st);

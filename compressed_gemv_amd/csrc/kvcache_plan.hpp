@@ -26,6 +26,7 @@ struct SplitRule {
   int wgs;                     // workgroups per KV head in the grid
   int cap;                     // positions the page table holds
   bool whole;                  // tiles are never cut: each weighs one step
+  bool single;                 // and there is a workgroup for every tile there can be: piece i is tile i
   bool sloped;                 // weigh a sequence's tiles by what each sees
   int extra;                   // weight of what a tile costs beside its keys
 };
@@ -40,13 +41,14 @@ __device__ __forceinline__ SeqRows seq_rows(const SeqView& s, int b, int cap) {
   SeqRows r{0, 0, 0, 0};
   if (b >= s.B) return r;
   if (!s.lens) return SeqRows{0, s.T, cap, cap};        // a shared prefix: every row sees all of it
+  const int64_t len = s.lens[b];                        // on its way beside the starts
   int64_t s0 = b, s1 = b + 1;
   if (s.starts) { s0 = s.starts[b]; s1 = s.starts[b + 1]; }
   const int64_t end = s1 < s.T ? s1 : s.T, t0 = s0 < 0 ? 0 : s0;
   if (end <= t0) return r;
   r.t0 = (int)t0;
   r.count = (int)(end - t0);
-  const int64_t len = s.lens[b], low = -((int64_t)1 << 30);
+  const int64_t low = -((int64_t)1 << 30);
   const int64_t v0 = len - (s1 - t0) + 1, v1 = len - (s1 - end);
   r.vis0 = (int)(v0 < low ? low : (v0 > cap ? cap : v0));
   r.need = (int)(v1 < 0 ? 0 : (v1 > cap ? cap : v1));
@@ -145,6 +147,16 @@ struct TileAt {
   int64_t lo, hi;              // its weights
   int64_t steps;               // steps of keys of the sequences before b
   SeqRows r;
+  Weights v;                   // of the sequence
+  int64_t base;                // weight before it
+  __device__ __forceinline__ bool advance() {              // to the sequence's next tile
+    if (tile + 1 >= v.tiles) return false;
+    ++tile;
+    ++index;
+    lo = hi;
+    hi = base + v.before(tile + 1);
+    return true;
+  }
 };
 
 template <bool BY_INDEX = false, bool STEPS = false>
@@ -161,11 +173,12 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
     const uint64_t m = __ballot(BY_INDEX ? tiles + tinc > x : carry + inc > x);
     if (m) {
       const int l = __ffsll((unsigned long long)m) - 1;
-      Weights v;
+      Weights& v = a.v;
       v.tiles = __builtin_amdgcn_readlane(w.tiles, l);
       v.A = __builtin_amdgcn_readlane(w.A, l);
       v.S = __builtin_amdgcn_readlane(w.S, l);
       const int64_t base = carry + lane_i64(inc, l) - lane_i64(u, l), first = tiles + lane_i64(tinc, l) - v.tiles;
+      a.base = base;
       int lo = 0;
       if (BY_INDEX) {
         lo = (int)(x - first);

@@ -41,6 +41,7 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
     __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    \
   }
 
+constexpr int kNoLoads = 0x0F70;           // s_waitcnt vmcnt(0), the other counters as they are
 constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 1024, -1024
 
 }  // namespace
@@ -216,32 +217,67 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   const int heads = a.c.heads, h = blockIdx.x % heads;
   Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
   Work w;
-  while (next_work<IMAGE>(x, pieces, w, lane)) {
+  while (next_work<true, IMAGE>(x, pieces, w, lane)) {
+  Dec dec(a.c, h, tid);
+  dec.pages = w.pages;
+  dec.max_pages = w.max_pages;
+  dec.k1 = w.k1;
+
+  // An image is copied to LDS as it lies, 1 KB a wave and instruction, without
+  // passing through registers; each wave waits for its own copies before the
+  // barrier, which by itself waits for what the wave did in LDS only.
+  auto fetch = [&](int key0, int buf) {
+    const int64_t step = w.steps + key0 / KT;
+    const uint8_t* src = x.image + (step * heads + h) * kv_image_bytes(D) + lane * 16;
+    auto put = [&](const uint8_t* from, uint8_t* to) {
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    };
+    for (int i = wave; i < KBUF / 1024; i += NW) put(src + i * 1024, ksh + buf * KBUF + i * 1024);
+    for (int i = wave; i < VBUF / 1024; i += NW) put(src + KBUF + i * 1024, vsh + buf * VBUF + i * 1024);
+    if (wave == 0) put(src + KBUF + VBUF, reinterpret_cast<uint8_t*>(gone[buf]));
+  };
+  // the first keys are on their way while the queries come
+  typename Dec::Codes r;
+  if (w.k0 < w.k1) {                       // workgroup-uniform
+    if constexpr (IMAGE) {
+      fetch(w.k0, 0);
+    } else {
+      dec.find_pages(w.k0);
+      dec.load(w.k0, r);
+      dec.find_pages(w.k0 + KT);
+    }
+  }
+
   // queries: rows scaled by a power of two to a largest value in [1, 2) (exact
   // up to 2^-25 of it), what each row sees, and the factor back
   f16x8_t qf[2][STEPS];
+  u32x4_t raw[2][STEPS];
   float cq[2];
   int lim[2], limmin = w.k1;
   const float c0 = fabsf(a.scale) * 1.4426950408889634f;
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    const int row = w.row0 + wave * 64 + n * 32 + col;
-    const bool ok = row < w.rows;
-    const int tok = ok ? row / a.group : 0, g = ok ? row - tok * a.group : 0;
-    const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D;
-    u32x4_t raw[STEPS];
+    int row = w.row0 + wave * 64 + n * 32 + col;
+    row = row < w.rows ? row : w.rows - 1; // behind the last row it is repeated, and not stored
+    const int tok = row / a.group, g = row - tok * a.group;
+    const uint16_t* q = a.Q + (int64_t)(w.t0 + tok) * a.q_stride + (int64_t)(h * a.group + g) * D + 8 * hh;
+    lim[n] = row_sees(w, tok);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) raw[n][s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+  }
+  __builtin_amdgcn_sched_barrier(0);       // all of them under way before the first is used
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
     uint32_t big = 0;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      raw[s] = u32x4_t{0u, 0u, 0u, 0u};
-      if (ok) raw[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s + 8 * hh);
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = raw[s][e] & 0x7F80u, hi = (raw[s][e] >> 16) & 0x7F80u;
+        const uint32_t lo = raw[n][s][e] & 0x7F80u, hi = (raw[n][s][e] >> 16) & 0x7F80u;
         big = lo > big ? lo : big;
         big = hi > big ? hi : big;
       }
-    }
     const uint32_t other = (uint32_t)__shfl_xor((int)big, 32);
     big = other > big ? other : big;
     int ex = (int)(big >> 7) - 127;
@@ -252,17 +288,16 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     for (int s = 0; s < STEPS; ++s) {
       u32x4_t v;
       if constexpr (BITS == 4) {           // pairs (j, j + 4), as a nibble mask leaves the keys
-        const u32x4_t t = raw[s];
-        raw[s][0] = __builtin_amdgcn_perm(t[2], t[0], 0x05040100u);
-        raw[s][1] = __builtin_amdgcn_perm(t[2], t[0], 0x07060302u);
-        raw[s][2] = __builtin_amdgcn_perm(t[3], t[1], 0x05040100u);
-        raw[s][3] = __builtin_amdgcn_perm(t[3], t[1], 0x07060302u);
+        const u32x4_t t = raw[n][s];
+        raw[n][s][0] = __builtin_amdgcn_perm(t[2], t[0], 0x05040100u);
+        raw[n][s][1] = __builtin_amdgcn_perm(t[2], t[0], 0x07060302u);
+        raw[n][s][2] = __builtin_amdgcn_perm(t[3], t[1], 0x05040100u);
+        raw[n][s][3] = __builtin_amdgcn_perm(t[3], t[1], 0x07060302u);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = cvt_pk_f16(bf16_lo_to_f32(raw[s][e]) * down, bf16_hi_to_f32(raw[s][e]) * down);
+      for (int e = 0; e < 4; ++e) v[e] = cvt_pk_f16(bf16_lo_to_f32(raw[n][s][e]) * down, bf16_hi_to_f32(raw[n][s][e]) * down);
       qf[n][s] = __builtin_bit_cast(f16x8_t, v);
     }
-    lim[n] = ok ? row_sees(w, tok) : w.k1;
     int lo = lim[n];                       // the least of the wave's rows
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -293,24 +328,6 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     p[n][0] = p[n][1] = u32x4_t{0u, 0u, 0u, 0u};
   }
 
-  Dec dec(a.c, h, tid);
-  dec.pages = w.pages;
-  dec.max_pages = w.max_pages;
-  dec.k1 = w.k1;
-
-  // An image is copied to LDS as it lies, 1 KB a wave and instruction, without
-  // passing through registers; __syncthreads waits for it.
-  auto fetch = [&](int key0, int buf) {
-    const int64_t step = w.steps + key0 / KT;
-    const uint8_t* src = x.image + (step * heads + h) * kv_image_bytes(D) + lane * 16;
-    auto put = [&](const uint8_t* from, uint8_t* to) {
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
-    };
-    for (int i = wave; i < KBUF / 1024; i += NW) put(src + i * 1024, ksh + buf * KBUF + i * 1024);
-    for (int i = wave; i < VBUF / 1024; i += NW) put(src + KBUF + i * 1024, vsh + buf * VBUF + i * 1024);
-    if (wave == 0) put(src + KBUF + VBUF, reinterpret_cast<uint8_t*>(gone[buf]));
-  };
   const uint8_t* kread = ksh + col * KP + hh * 16;
   const uint8_t* vread = vsh + col * VP + hh * 16;
   f16x8_t kf[STEPS], vf[2][DT];
@@ -394,14 +411,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   using B = std::integral_constant<int, 1>;
   auto none = [] {};
 
-  if (w.k0 < w.k1) {                       // workgroup-uniform
-    typename Dec::Codes r;
+  if (w.k0 < w.k1) {
     if constexpr (IMAGE) {
-      fetch(w.k0, 0);
+      __builtin_amdgcn_s_waitcnt(kNoLoads);
     } else {
-      dec.find_pages(w.k0);
-      dec.load(w.k0, r);
-      dec.find_pages(w.k0 + KT);
       dec.keys(w.k0, r, ksh, gone[0]);
       dec.values(w.k0, r, vsh);
       if (w.k0 + KT < w.k1) {
@@ -447,6 +460,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
           }
         }
       }
+      if constexpr (IMAGE) __builtin_amdgcn_s_waitcnt(kNoLoads);
       __syncthreads();
       if (more) read_k(buf ^ 1, 0);
     }
@@ -470,22 +484,29 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     if (row >= w.rows) continue;
     const int tok = row / a.group, g = row - tok * a.group;
     const float inv = w.direct ? (l[n] == 0.f ? 0.f : 1.0f / l[n]) : 1.0f;
-    const int64_t at = (int64_t)(w.t0 + tok) * a.o_stride + (int64_t)(h * a.group + g) * D;
-    float* po = w.direct ? nullptr : part_o<D>(x, w.slot, h, trow);
+    auto each = [&](auto&& put) {
 #pragma unroll
-    for (int e0 = 0; e0 < 2; ++e0)
+      for (int e0 = 0; e0 < 2; ++e0)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d0 = DPT * (8 * e0 + 4 * hh + j);
+        for (int j = 0; j < 4; ++j) {
+          const int d0 = DPT * (8 * e0 + 4 * hh + j);
 #pragma unroll
-        for (int q = 0; q < DPT; q += 4) {
-          f32x4_t v;
+          for (int q = 0; q < DPT; q += 4) {
+            f32x4_t v;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = acc[n][(q + i) / 2][4 * (e0 + 2 * ((q + i) % 2)) + j] * inv;
-          if (w.direct) store_out4(a, at + d0 + q, v);
-          else *reinterpret_cast<f32x4_t*>(po + d0 + q) = v;
+            for (int i = 0; i < 4; ++i) v[i] = acc[n][(q + i) / 2][4 * (e0 + 2 * ((q + i) % 2)) + j] * inv;
+            put(d0 + q, v);
+          }
         }
-      }
+    };
+    if (w.direct) {
+      const int64_t at = (int64_t)(w.t0 + tok) * a.o_stride + (int64_t)(h * a.group + g) * D;
+      if (a.out_f32) each([&](int d, const f32x4_t& v) { store_out4<true>(a, at + d, v); });
+      else each([&](int d, const f32x4_t& v) { store_out4<false>(a, at + d, v); });
+    } else {
+      float* po = part_o<D>(x, w.slot, h, trow);
+      each([&](int d, const f32x4_t& v) { *reinterpret_cast<f32x4_t*>(po + d) = v; });
+    }
     if (!w.direct && hh == 0) {
       float* ml = part_ml(x, w.slot, h, trow);
       ml[0] = m[n];
