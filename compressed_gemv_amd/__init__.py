@@ -725,7 +725,8 @@ def _cache_seqs(cache: qcache, T: int, pages, lens, starts) -> qseqs:
     if pages.dim() != 2 or pages.dtype != torch.int32:
         raise ValueError("pages must be int32 [B][max_pages]")
     B, width = pages.shape
-    _need_numel(lens, B, "lens", (torch.int32,))
+    if lens is None or lens.dtype != torch.int32 or lens.numel() != B:
+        _need_numel(lens, B, "lens", (torch.int32,))
     if starts is not None:
         _need_numel(starts, B + 1, "starts", (torch.int32,))
     elif T != B:
@@ -765,7 +766,7 @@ def _cache_call(cache: qcache, stream, fresh, what, fn, *args):
     binding allocated, which a stream other than the current one must be
     recorded on before they can be reused."""
     idx = cache._index
-    if stream is None and idx == torch.cuda.current_device():
+    if stream is None and idx == torch._C._cuda_getDevice():
         status = fn(cache._ref, *args, torch._C._cuda_getCurrentRawStream(idx))
     else:
         if stream is None:
@@ -808,23 +809,27 @@ def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = N
     call does not look at device data).  Rows no sequence owns are not
     written."""
     fresh = ()
+    heads, D = cache.heads, cache.head_dim
     if K is None and V is None:
         if rows is None:
             if starts is not None:
                 raise ValueError("rows: missing, and no outputs given")
             rows = pages.shape[0]
-        K, V = torch.empty((2, rows, cache.heads, cache.head_dim), dtype=dtype, device=cache._device).unbind(0)
-        fresh = (K, V)
+        if dtype not in _OUT:
+            raise ValueError(f"dtype {dtype}, expected one of {_OUT}")
+        K, V = fresh = torch.empty((2, rows, heads, D), dtype=dtype, device=cache._device).unbind(0)
+        T, ks, vs = rows, heads * D, heads * D
     elif K is None or V is None:
         raise ValueError("K and V: both outputs or neither")
-    ks = _cache_rows(K, cache.heads, cache.head_dim, _OUT, "K")
-    vs = _cache_rows(V, cache.heads, cache.head_dim, (K.dtype,), "V")
-    T = K.shape[0]
-    if V.shape[0] != T:
-        raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
+    else:
+        ks = _cache_rows(K, heads, D, _OUT, "K")
+        vs = _cache_rows(V, heads, D, (K.dtype,), "V")
+        T = K.shape[0]
+        if V.shape[0] != T:
+            raise ValueError(f"V: {V.shape[0]} rows, K has {T}")
+        _on_device(cache, False, K, V)
     seqs = _cache_seqs(cache, T, pages, lens, starts)
     _on_device(cache, True, pages, lens, starts)
-    _on_device(cache, False, K, V)
     if T == 0:
         return K, V
     _cache_call(cache, stream, fresh, "qcache_read", load().qcache_read, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
@@ -858,10 +863,14 @@ def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_d
     seqs = _cache_seqs(cache, T, pages, lens, starts)
     fresh_out = fresh_ws = None
     if out is None:
+        if out_dtype not in _OUT:
+            raise ValueError(f"out_dtype {out_dtype}, expected one of {_OUT}")
         out = fresh_out = torch.empty((T, q_heads, D), dtype=out_dtype, device=Q.device)
-    o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
-    if out.shape[0] != T:
-        raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
+        o_stride = q_heads * D
+    else:
+        o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
+        if out.shape[0] != T:
+            raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
     _on_device(cache, True, pages, lens, starts)
     _on_device(cache, False, Q, out)
     if T == 0:
@@ -869,7 +878,7 @@ def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_d
     n_prefix = prefix[1] if prefix else 0
     need = _attend_ws(cache.page_size, heads, D, cache.bits, seqs.B, T, seqs.max_pages, q_heads, n_prefix)
     if ws is None:
-        ws = fresh_ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        ws = fresh_ws = torch.empty(need, dtype=torch.uint8, device=cache._device)
         ws_bytes = need
     else:
         _need_bytes(ws, need, "ws")
