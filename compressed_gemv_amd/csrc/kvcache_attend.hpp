@@ -37,10 +37,12 @@ struct Pieces {
   int piece;
   int64_t x, end;              // weights still to do
   TileAt t;                    // the last tile; b < 0: none yet
+  Cursor from;
 };
 
 __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int lane) {
   Pieces p;
+  p.from = Cursor{};
   if (x.rule.single) {                     // found without a look at the other sequences' weights
     p.line = Line{};
     p.piece = piece;
@@ -66,7 +68,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int 
 template <bool ADVANCE, bool STEPS = false>
 __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& w, int lane) {
   while (p.x < p.end) {
-    if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane);
+    if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane, p.from);
     const TileAt& t = p.t;
     if (t.b < 0) return false;
     w.steps = t.steps;

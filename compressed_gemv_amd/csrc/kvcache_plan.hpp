@@ -139,6 +139,13 @@ __device__ __forceinline__ Line line_of(const SeqView& s, const SplitRule& p, in
   return l;
 }
 
+// Where a search begins: the 64 sequences that the one before ended in, and
+// what lies before them.
+struct Cursor {
+  int b0;
+  int64_t carry, tiles, steps; // weights, tiles, steps of keys
+};
+
 // The tile that weight x of the line lies in, or (BY_INDEX) tile number x of
 // it; b < 0: none.
 struct TileAt {
@@ -160,11 +167,11 @@ struct TileAt {
 };
 
 template <bool BY_INDEX = false, bool STEPS = false>
-__device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, int64_t x, int lane) {
+__device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, int64_t x, int lane, Cursor& at) {
   TileAt a{};
   a.b = -1;
-  int64_t carry = 0, tiles = 0, steps = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 64) {
+  int64_t carry = at.carry, tiles = at.tiles, steps = at.steps;
+  for (int b0 = at.b0; b0 < s.B; b0 += 64) {
     const SeqRows r = seq_rows(s, b0 + lane, p.cap);
     const Weights w = weights_of(p, r);
     const int k = steps_of(p, r);
@@ -190,6 +197,7 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
           else n = half;
         }
       }
+      at = Cursor{b0, carry, tiles, steps};
       a.b = b0 + l;
       a.tile = lo;
       a.steps = STEPS ? steps + lane_i64(kinc, l) - __builtin_amdgcn_readlane(k, l) : 0;
@@ -207,6 +215,12 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
     if (STEPS) steps += lane_i64(kinc, 63);
   }
   return a;
+}
+
+template <bool BY_INDEX = false>
+__device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, int64_t x, int lane) {
+  Cursor from{};
+  return tile_at<BY_INDEX>(s, p, x, lane, from);
 }
 
 // Step x of all the sequences' steps of keys; b < 0: none.
