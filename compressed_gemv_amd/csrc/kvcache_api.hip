@@ -36,8 +36,8 @@ int cache_ok(const qcache* c) {
 // sizes alone: what the workspace query reads
 int seq_sizes_ok(const qcache* c, const qseqs* s) {
   if (!s || s->B < 1 || s->B > 65536 || s->T < 1 || s->max_pages < 1) return Q_EINVAL;
-  // rows and positions are 32-bit
-  if (s->T > (1 << 28) || s->max_pages > ((int64_t)1 << 30) / c->page_size) return Q_EUNSUPPORTED;
+  // rows and positions are 32-bit, and a grid of 256 threads for 16 rows stays below 2^32 threads
+  if (s->T > (1 << 27) || s->max_pages > ((int64_t)1 << 30) / c->page_size) return Q_EUNSUPPORTED;
   return Q_OK;
 }
 
@@ -162,7 +162,8 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
   // weights of the line of work times 512 pieces stay below 2^52: half a weight for a key of a tile of 8 rows or more
   if ((double)(rows / 8 + s->B) * (double)((s->max_pages * c->page_size + prefix_len) / 2 + 512) * 512.0 > 4e15)
     return Q_EUNSUPPORTED;
-  *ws_bytes = qg::kv_attend_ws_bytes(s->B, s->T, s->max_pages, __builtin_ctz((unsigned)c->page_size), c->heads, q_heads / c->heads, c->head_dim, prefix_len);
+  *ws_bytes = qg::kv_attend_ws_bytes(s->B, s->T, s->max_pages, __builtin_ctz((unsigned)c->page_size), c->heads,
+                                     q_heads / c->heads, c->head_dim, prefix_len);
   return Q_OK;
 }
 

@@ -549,39 +549,43 @@ __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
   }
 }
 
-// Every row's own parts and its prefix's: workgroups of `rpw` rows of a tile, a wave per row.
+// Every row's own parts and its prefix's: `rpw` rows of a tile and KV head are
+// a unit, a wave takes a row.
 template <int D>
-__global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, AttendArgs pre, int rpw) {
+__global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, AttendArgs pre, int rpw, int64_t units) {
   constexpr int LPR = D / 4, GRP = 64 / LPR;
   const KvAttend& a = own.a;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPR;
   const int per_tile = own.rule.rt / rpw;
-  const int h = blockIdx.x % a.c.heads, u = blockIdx.x / a.c.heads;
-  const TileAt t = tile_at<true>(own.s, own.rule, u / per_tile, lane);
-  if (t.b < 0) return;
-  const int row0 = t.tile * own.rule.rt, rows = t.r.count * a.group;
-  const int first = row0 + u % per_tile * rpw;
-  if (first >= rows) return;
-  const Line line = line_of(own.s, own.rule, lane), pline = pre.line;
-  const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
-  const int slot0 = (int)(i0 + t.index);
-  if (slot0 + parts > own.part.slots) return;
-  const int64_t A = (int64_t)(pre.a.prefix_len + pre.rule.ku - 1) / pre.rule.ku * kSub;   // weight of a tile of the prefix
-  const int last = first + rpw < rows ? first + rpw : rows;
-  for (int R = first + wave; R < last; R += 4) {
-    const int64_t P = (int64_t)t.r.t0 * a.group + R;
-    const int pt = (int)(P / pre.rule.rt), prow = (int)(P % pre.rule.rt);
-    const int p0 = pline.piece(A * pt), np = pline.piece(A * (pt + 1) - 1) - p0 + 1;
-    if (p0 + pt + np > pre.part.slots) continue;
-    auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
-      const bool p = c < np;
-      px = p ? &pre : &own;
-      slot = p ? p0 + pt + c : slot0 + c - np;
-      r = p ? prow : R - row0;
-    };
-    RowSum s = sum_parts<D, 8>(at, lane / LPR, GRP, np + parts, h, sub);
-    join_groups<D>(s);
-    if (lane < LPR) store_row<D>(a, t.r, R, h, sub, s);
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int h = (int)(unit % a.c.heads);
+    const int64_t u = unit / a.c.heads;
+    const TileAt t = tile_at<true>(own.s, own.rule, u / per_tile, lane);
+    if (t.b < 0) return;
+    const int row0 = t.tile * own.rule.rt, rows = t.r.count * a.group;
+    const int first = row0 + (int)(u % per_tile) * rpw;
+    if (first >= rows) continue;
+    const Line line = line_of(own.s, own.rule, lane), pline = pre.line;
+    const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
+    const int slot0 = (int)(i0 + t.index);
+    if (slot0 + parts > own.part.slots) continue;
+    const int64_t A = (int64_t)(pre.a.prefix_len + pre.rule.ku - 1) / pre.rule.ku * kSub;   // weight of a tile of the prefix
+    const int last = first + rpw < rows ? first + rpw : rows;
+    for (int R = first + wave; R < last; R += 4) {
+      const int64_t P = (int64_t)t.r.t0 * a.group + R;
+      const int pt = (int)(P / pre.rule.rt), prow = (int)(P % pre.rule.rt);
+      const int p0 = pline.piece(A * pt), np = pline.piece(A * (pt + 1) - 1) - p0 + 1;
+      if (p0 + pt + np > pre.part.slots) continue;
+      auto at = [&](int c, const AttendArgs*& px, int& slot, int& r) {
+        const bool p = c < np;
+        px = p ? &pre : &own;
+        slot = p ? p0 + pt + c : slot0 + c - np;
+        r = p ? prow : R - row0;
+      };
+      RowSum s = sum_parts<D, 8>(at, lane / LPR, GRP, np + parts, h, sub);
+      join_groups<D>(s);
+      if (lane < LPR) store_row<D>(a, t.r, R, h, sub, s);
+    }
   }
 }
 
@@ -674,7 +678,7 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   }
   if (p.own.rt == 256 && ceil_div(T, B) * group >= kImageRows) {
     p.images = B * ceil_div(cap, 128);
-    if (p.images * heads * kv_image_bytes(head_dim) > kImageBytes) p.images = 0;
+    if (p.images > kImageBytes / (heads * kv_image_bytes(head_dim))) p.images = 0;
   }
   size_t at = 0;
   auto take = [&](int64_t floats) {
@@ -719,9 +723,10 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
   if (p.shared) {
     const int rpw = own.rule.rt <= 32 ? 8 : 16;
     const int64_t tiles = p.own_slots - p.own.wgs;
-    const dim3 grid((unsigned)(tiles * (own.rule.rt / rpw) * a.c.heads));
-    if (head_dim == 128) hipLaunchKernelGGL((kv_join_prefix_kernel<128>), grid, dim3(256), 0, st, own, pre, rpw);
-    else hipLaunchKernelGGL((kv_join_prefix_kernel<64>), grid, dim3(256), 0, st, own, pre, rpw);
+    const int64_t units = tiles * (own.rule.rt / rpw) * a.c.heads;
+    const dim3 grid((unsigned)(units < (1 << 20) ? units : 1 << 20));
+    if (head_dim == 128) hipLaunchKernelGGL((kv_join_prefix_kernel<128>), grid, dim3(256), 0, st, own, pre, rpw, units);
+    else hipLaunchKernelGGL((kv_join_prefix_kernel<64>), grid, dim3(256), 0, st, own, pre, rpw, units);
   } else {
     const dim3 grid((unsigned)((p.own.wgs - 1) * a.c.heads), (unsigned)ceil_div(own.rule.rt, 64));
     if (head_dim == 128) hipLaunchKernelGGL((kv_join_cuts_kernel<128>), grid, dim3(256), 0, st, own);

@@ -57,8 +57,8 @@ typedef struct qcache {
 
 typedef struct qseqs {
   int64_t B;                 /* sequences, 1 .. 65536 */
-  int64_t T;                 /* rows of K, V, Q and the outputs, starts[B] <= T */
-  int64_t max_pages;         /* width of the page table */
+  int64_t T;                 /* rows of K, V, Q and the outputs, 1 .. 2^27, starts[B] <= T */
+  int64_t max_pages;         /* width of the page table, max_pages * page_size <= 2^30 */
   const int32_t* pages;      /* [B][max_pages], device */
   const int32_t* lens;       /* [B], device; positions behind the table have no place */
   const int32_t* starts;     /* [B+1] nondecreasing, device, or NULL */
@@ -88,8 +88,9 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
 
 /* out[t][hq][:] = sum_j softmax_j(scale <Q[t][hq][:], k_j>) v_j over the
  * positions j of the row's own sequence up to the row's own position, KV head
- * hq / (q_heads / heads); q_heads a multiple of heads.  Q and out are bf16 or
- * out is fp32 (out_dtype), rows of one token contiguous, q_stride and o_stride
+ * hq / (q_heads / heads); q_heads a multiple of heads, at most 64 times it.
+ * Q is bf16, of magnitudes below 2^63 (2^-57 and less may count as 0), out
+ * bf16 or fp32 (out_dtype); rows of one token contiguous, q_stride and o_stride
  * elements between tokens; Q and out 16-byte aligned, strides a multiple of
  * 16 bytes.  A row that sees nothing is zero.  Sums, maxima and the softmax
  * statistics are fp32.  ws: device, 16-byte aligned, >= the
