@@ -51,7 +51,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 // hold the same rows, one with the high and one with the low parts of the
 // weights, so that one product does for two.
 template <int D, int BITS, int RT>
-__global__ __launch_bounds__(256, (RT > 16 ? 2 : 1) * D > 128 ? 1 : 2) void kv_rows_kernel(AttendArgs x) {
+__device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
   constexpr int NT = RT > 16 ? 2 : 1;
   constexpr bool PACK = RT == 8;
   constexpr int ROWB = D * BITS / 8;       // bytes of a cache row
@@ -67,8 +67,8 @@ __global__ __launch_bounds__(256, (RT > 16 ? 2 : 1) * D > 128 ? 1 : 2) void kv_r
   const KvAttend& a = x.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
-  const int heads = a.c.heads, h = blockIdx.x % heads;
-  Pieces pieces = pieces_of(x, blockIdx.x / heads, lane);
+  const int heads = a.c.heads, h = block % heads;
+  Pieces pieces = pieces_of(x, block / heads, lane);
   Work w;
   while (next_work<false>(x, pieces, w, lane)) {
   f32x4_t acc[NT][TILES];
@@ -413,6 +413,30 @@ __global__ __launch_bounds__(256, (RT > 16 ? 2 : 1) * D > 128 ? 1 : 2) void kv_r
   }
 }
 
+constexpr int rows_wgs_per_cu(int d, int rt) { return (rt > 16 ? 2 : 1) * d > 128 ? 1 : 2; }
+
+template <int D, int BITS, int RT>
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, RT)) void kv_rows_kernel(AttendArgs x) {
+  rows_body<D, BITS, RT>(x, blockIdx.x);
+}
+
+// Two sets of tiles of one height, a short prefix's and the sequences' own:
+// one launch of both is 22 -> 17 us for 6 sequences of 40 behind 701 tokens.
+// A kernel of its own, since the choice costs the other 4 % of 131072 keys.
+template <int D, int BITS, int RT>
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, RT)) void kv_rows_pair_kernel(AttendArgs one, AttendArgs two,
+                                                                                  unsigned split) {
+  AttendArgs x;
+  unsigned block = blockIdx.x;
+  if (block < split) {
+    x = one;
+  } else {
+    x = two;
+    block -= split;
+  }
+  rows_body<D, BITS, RT>(x, block);
+}
+
 // ------------------------------------------------------------------- join
 // out = sum_c 2^(m_c - M) o_c over sum_c 2^(m_c - M) l_c, c the parts of a row.
 // All latency: D / 4 lanes hold a row, and a lane group takes its parts in
@@ -590,9 +614,14 @@ __global__ __launch_bounds__(256) void kv_join_prefix_kernel(AttendArgs own, Att
 }
 
 // ------------------------------------------------------------------ launch
-hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st) {
-  const dim3 grid((unsigned)(x.rule.wgs * x.a.c.heads));
-#define ROWS(D, B, R) hipLaunchKernelGGL((kv_rows_kernel<D, B, R>), grid, dim3(256), 0, st, x)
+hipError_t launch_kv_rows(const AttendArgs& x, const AttendArgs* y, int head_dim, int bits, hipStream_t st) {
+  const unsigned split = (unsigned)(x.rule.wgs * x.a.c.heads);
+  const dim3 grid(split + (y ? (unsigned)(y->rule.wgs * y->a.c.heads) : 0u));
+#define ROWS(D, B, R)                                                                                         \
+  do {                                                                                                        \
+    if (y) hipLaunchKernelGGL((kv_rows_pair_kernel<D, B, R>), grid, dim3(256), 0, st, x, *y, split);          \
+    else hipLaunchKernelGGL((kv_rows_kernel<D, B, R>), grid, dim3(256), 0, st, x);                            \
+  } while (0)
 #define ROWS_N(D, B)                          \
   do {                                        \
     if (x.rule.rt == 8) ROWS(D, B, 8);        \
@@ -635,17 +664,20 @@ struct CallPlan {
   SplitRule own, pre;
   int64_t own_slots, pre_slots;      // per KV head
   bool shared, join;
+  bool pair;                         // prefix and own keys in one launch
   int64_t images;                    // steps of keys to decode beforehand
   Line pre_line;
   size_t o_own, ml_own, o_pre, ml_pre, image, bytes;
 };
 
-// Tile height and workgroups by the rows a KV head has against one run of
-// keys, at most `tiles` tiles of at most cap keys.
-SplitRule rule_for(int64_t rows, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
+// Tile height by the rows a KV head has against one run of keys.
+int tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
+
+// The division of tiles of rt rows of `seqs` sequences with at most cap keys each.
+SplitRule rule_for(int rt, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
   SplitRule r{};
   r.group = group;
-  r.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  r.rt = rt;
   r.ku = 128;
   r.cap = cap;
   r.sloped = r.rt > 32;
@@ -663,17 +695,21 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
                    int64_t prefix_len) {
   CallPlan p{};
   const int64_t cap = max_pages << page_shift;
-  p.own = rule_for(ceil_div(T, B) * group, T * group, B, group, heads, (int)cap, false);
-  const int64_t tiles = T * group / p.own.rt + B;           // at most, over all sequences
   p.shared = prefix_len > 0;
+  int rt = tile_rows(ceil_div(T, B) * group);
+  const int pre_rt = tile_rows(T * group);
+  p.pair = p.shared && pre_rt <= 32 && cap <= kWholeKeys;
+  if (p.pair) rt = pre_rt;
+  p.own = rule_for(rt, T * group, B, group, heads, (int)cap, false);
+  const int64_t tiles = T * group / rt + B;                 // at most, over all sequences
   p.own_slots = p.shared ? p.own.wgs + tiles : 2 * p.own.wgs;
   p.join = p.shared || (!p.own.whole && p.own.wgs > 1);
   if (!p.join) p.own_slots = 0;
   if (p.shared) {
-    p.pre = rule_for(T * group, T * group, 1, group, heads, (int)prefix_len, true);
+    p.pre = rule_for(pre_rt, T * group, 1, group, heads, (int)prefix_len, true);
     p.pre.sloped = false;                                   // every row sees all of it
-    p.pre_slots = p.pre.wgs + ceil_div(T * group, p.pre.rt);
-    p.pre_line = Line{ceil_div(T * group, p.pre.rt) * ceil_div(prefix_len, p.pre.ku) * kSub, p.pre.wgs, 1};
+    p.pre_slots = p.pre.wgs + ceil_div(T * group, pre_rt);
+    p.pre_line = Line{ceil_div(T * group, pre_rt) * ceil_div(prefix_len, p.pre.ku) * kSub, p.pre.wgs, 1};
     if (p.pre_line.U / kSub < p.pre_line.N) p.pre_line.N = (int)(p.pre_line.U / kSub);
   }
   if (p.own.rt == 256 && ceil_div(T, B) * group >= kImageRows) {
@@ -714,11 +750,15 @@ hipError_t launch_kv_attend(const KvAttend& a, int head_dim, int bits, void* ws,
   const AttendArgs pre{a, prefix, p.pre, Partials{at(p.o_pre), at(p.ml_pre), (int)p.pre_slots}, true, p.pre_line, nullptr, 0};
   hipError_t e;
   auto launch = [&](const AttendArgs& x) {
-    return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, st) : launch_kv_rows(x, head_dim, bits, st);
+    return x.rule.rt > 32 ? launch_kv_tiles(x, head_dim, bits, st) : launch_kv_rows(x, nullptr, head_dim, bits, st);
   };
-  if (p.shared && (e = launch(pre)) != hipSuccess) return e;
-  if (own.image && (e = launch_kv_images(own, head_dim, bits, st)) != hipSuccess) return e;
-  if ((e = launch(own)) != hipSuccess) return e;
+  if (p.pair) {
+    if ((e = launch_kv_rows(pre, &own, head_dim, bits, st)) != hipSuccess) return e;
+  } else {
+    if (p.shared && (e = launch(pre)) != hipSuccess) return e;
+    if (own.image && (e = launch_kv_images(own, head_dim, bits, st)) != hipSuccess) return e;
+    if ((e = launch(own)) != hipSuccess) return e;
+  }
   if (!p.join) return hipSuccess;
   if (p.shared) {
     const int rpw = own.rule.rt <= 32 ? 8 : 16;

@@ -140,7 +140,8 @@ __device__ __forceinline__ void store_out4(const KvAttend& a, int64_t at, const 
   else store_out4<false>(a, at, v);
 }
 
-hipError_t launch_kv_rows(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
+// y: a second set of tiles of the same height in the same launch, or null
+hipError_t launch_kv_rows(const AttendArgs& x, const AttendArgs* y, int head_dim, int bits, hipStream_t st);
 hipError_t launch_kv_tiles(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
 hipError_t launch_kv_images(const AttendArgs& x, int head_dim, int bits, hipStream_t st);
 // Bytes of one image (128 keys of one KV head): the LDS rows of the keys, those
