@@ -643,18 +643,26 @@ hipError_t launch_kv_rows(const AttendArgs& x, const AttendArgs* y, int head_dim
 namespace {
 
 // Workgroups in all: as many as are resident at once on 256 CUs, two of the
-// kernel for few rows, one of the other.
+// kernel for few rows (four: 66 -> 78 us for 32 sequences of 8000), one of the
+// kernel for tiles of 256 rows, two for those of 128.
 constexpr int kRowWorkgroups = 512;
 constexpr int kTileWorkgroups = 256;
-// Page tables of up to so many positions leave their tiles whole: a second
-// launch to join parts would cost more than the keys.
-constexpr int kWholeKeys = 768;
+// Page tables of up to so many positions leave their tiles whole, each with one
+// workgroup: a second launch to join parts costs more than an even division
+// saves.  8 heads, whole against cut: 1 / 8 sequences of 1000 keys 14.3 / 15.0
+// against 15.4 / 18.3 us, 1 / 8 / 24 / 65 of 1500 keys 18.4 / 19.6 / 22 / 56
+// against 17.0 / 20.8 / 30 / 52 us.  Tiles of 32 rows take twice as long for a
+// key (2 sequences of 1500, 32 rows, 4 bits: 26 against 18 us), so half as many.
+constexpr int kWholeKeys = 1536;
 // What a tile costs beside its keys, in steps of keys / kSub: about two steps
 // of the kernel for few rows (4 us), one and a half of the other's 4 us.
 constexpr int kRowsExtra = 128, kTileExtra = 96;
 // Keys are decoded beforehand where at least this many rows of a sequence meet
-// them (4 tiles) and the images, sized for full page tables, fit this many bytes.
-constexpr int64_t kImageRows = 1024;
+// them (8 tiles) and the images, sized for full page tables, fit this many
+// bytes.  8 heads, with images against without: 4 x 1120 rows on 4000 keys
+// 150 against 141 us, 4 x 2048 rows on 4000 keys 211 against 215, 2 x 4096 rows
+// on 8000 keys 318 against 343, 8192 rows on 8000 keys 320 against 357.
+constexpr int64_t kImageRows = 2048;
 constexpr int64_t kImageBytes = (int64_t)1 << 30;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -670,7 +678,12 @@ struct CallPlan {
   size_t o_own, ml_own, o_pre, ml_pre, image, bytes;
 };
 
-// Tile height by the rows a KV head has against one run of keys.
+// Tile height by the rows a KV head has against one run of keys.  Up to 8 rows
+// share a product's 16 columns with their low parts (32 sequences of 8000, 8
+// bits: 66 us either way; 4 of 131072, 4 bits: 105 against 112 us).  33 .. 64
+// rows cost the same in tiles of 32 and of 128 (16 sequences of 3000, 48 rows:
+// 64 us); 96 rows 58 us in tiles of 128 and 66 in tiles of 256, 200 rows 73 us
+// in tiles of 256 and 89 in tiles of 128 (8 sequences of 4000).
 int tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
 
 // The division of tiles of rt rows of `seqs` sequences with at most cap keys each.
@@ -681,7 +694,7 @@ SplitRule rule_for(int rt, int64_t total_rows, int64_t seqs, int group, int head
   r.ku = 128;
   r.cap = cap;
   r.sloped = r.rt > 32;
-  r.whole = !must_cut && cap <= (r.rt <= 32 ? kWholeKeys : r.ku);
+  r.whole = !must_cut && cap <= (r.rt <= 16 ? kWholeKeys : r.rt <= 32 ? kWholeKeys / 2 : r.ku);
   r.extra = r.whole || must_cut ? 0 : r.rt <= 32 ? kRowsExtra : kTileExtra;
   const int64_t most = (total_rows / r.rt + seqs) * (r.whole ? 1 : ceil_div(cap > 0 ? cap : 1, r.ku));   // steps of keys, at most
   int64_t n = (r.rt == 256 ? kTileWorkgroups : kRowWorkgroups) / heads;
@@ -698,7 +711,7 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   p.shared = prefix_len > 0;
   int rt = tile_rows(ceil_div(T, B) * group);
   const int pre_rt = tile_rows(T * group);
-  p.pair = p.shared && pre_rt <= 32 && cap <= kWholeKeys;
+  p.pair = p.shared && pre_rt <= 32 && cap <= kWholeKeys / 2;
   if (p.pair) rt = pre_rt;
   p.own = rule_for(rt, T * group, B, group, heads, (int)cap, false);
   const int64_t tiles = T * group / rt + B;                 // at most, over all sequences

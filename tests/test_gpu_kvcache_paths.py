@@ -53,7 +53,7 @@ def test_every_height(gpu, tokens, head_dim, bits):
     rng = np.random.default_rng(tokens * 7 + head_dim + bits)
     say(f"height {tokens} tokens d{head_dim} b{bits}")
     new = [tokens + 3, 0, tokens - 3, tokens + tokens // 2, tokens // 2]
-    lens = [tokens + 903, 0, tokens - 3, tokens // 2 + 77, tokens // 2 + 401]    # the fourth has rows before its start
+    lens = [tokens + 1703, 0, tokens - 3, tokens // 2 + 77, tokens // 2 + 401]    # the fourth has rows before its start
     new = [n + tokens // 4 + 1 for n in new[:1]] + new[1:]
     b = Batch(rng, lens, new, 32, 1, head_dim, bits, lead=2)
     b.pages[4, 1] = -3                     # a hole
@@ -72,7 +72,7 @@ def test_decoded_beforehand(gpu, page_size, head_dim, bits):
     if page_size == 16:
         b.pages[0, 5] = -1
     _nan_where_no_token_is(b)
-    _attend(gpu, b.device(gpu), rng, 8)
+    _attend(gpu, b.device(gpu), rng, 16)
 
 
 def test_rows_of_sequences_that_are_not_whole_tiles(gpu):
@@ -112,11 +112,11 @@ def test_many_sequences(gpu, page_size, width):
 def test_many_rows_of_many_sequences(gpu):
     """Ragged chunks of 70 sequences, keys decoded beforehand: steps are counted over more than 64 sequences."""
     rng = np.random.default_rng(70)
-    new = [int(n) for n in rng.integers(1, 50, 70)]
+    new = [int(n) for n in rng.integers(20, 60, 70)]
     lens = [n + int(k) for n, k in zip(new, rng.integers(0, 150, 70))]
     b = Batch(rng, lens, new, 16, 1, 64, 8)
     _nan_where_no_token_is(b)
-    _attend(gpu, b.device(gpu), rng, 48)
+    _attend(gpu, b.device(gpu), rng, 64)
 
 
 def test_far_pages(gpu):
@@ -177,7 +177,7 @@ def test_the_same_pages_in_several_tables(gpu):
 def test_captured_ragged(gpu, tokens):
     """Chunks captured once and replayed with other lens and starts: the work is divided on the device."""
     rng = np.random.default_rng(tokens)
-    H, D, G, B = 1, 64, 8, 4
+    H, D, G, B = 1, 64, 16, 4
     b = Batch(rng, [tokens * 5] * B, [tokens] * B, 16, H, D, 8, prefix=50).device(gpu)
     T = tokens * B
     Q = torch.empty(T, H * G, D, dtype=torch.bfloat16, device="cuda")
