@@ -13,6 +13,14 @@
 // The weights p_j s_j enter as bf16 hi + lo (two products): with one rounding
 // to 8 bits the offset form would lose three times what a plain bf16
 // probability does, since codes count from the row's minimum.
+//
+// Measured (8 KV heads of 128, 8 query heads each): 32 sequences of 1000 .. 8000
+// tokens at 8 bits 57 us, 5.4 TB/s of codes and constants, 6.2 over longer
+// ones, bound by memory; 4 of 100000 .. 131072 at 4 bits 98 us, 5.1 TB/s, where
+// the vector unit's decoding and softmax (about 260 instructions for 32 keys)
+// take as long as the loads.  A third step in flight at 4 bits was no faster.
+// One sequence of 517 tokens takes 11 us, nearly all of it latency: lens,
+// page table, codes and the join of the waves one after the other.
 #include "common.hpp"
 #include "kvcache_attend.hpp"
 
@@ -654,9 +662,11 @@ constexpr int kTileWorkgroups = 256;
 // against 17.0 / 20.8 / 30 / 52 us.  Tiles of 32 rows take twice as long for a
 // key (2 sequences of 1500, 32 rows, 4 bits: 26 against 18 us), so half as many.
 constexpr int kWholeKeys = 1536;
-// What a tile costs beside its keys, in steps of keys / kSub: about two steps
-// of the kernel for few rows (4 us), one and a half of the other's 4 us.
-constexpr int kRowsExtra = 128, kTileExtra = 96;
+// What a tile costs beside its keys, in steps of keys / kSub: one step of the
+// kernel for few rows (32 sequences of 8000: 63.4 us with 0 and with 64, 64.7
+// with 128), one and a half of the other's 4 us (prompts of 999 .. 2500: 289 us
+// with 0, 268 with 64, 266 with 96, 271 with 192).
+constexpr int kRowsExtra = 64, kTileExtra = 96;
 // Keys are decoded beforehand where at least this many rows of a sequence meet
 // them (8 tiles) and the images, sized for full page tables, fit this many
 // bytes.  8 heads, with images against without: 4 x 1120 rows on 4000 keys
