@@ -252,3 +252,40 @@ def test_query_range(gpu, power):
                                      out_dtype=torch.float32))
         ref, mag, owned = b.ref.attend(q, b.pages, b.lens, b.starts, scale)
         check_attend(b, q, out, ref, mag, owned, scale)
+
+
+@pytest.mark.parametrize("below", [10.4, 24.6, 31.0])
+@pytest.mark.parametrize("new", [1, 60])
+def test_many_small_weights(gpu, below, new):
+    """One key far above all the others, whose weights of 2^-below each make the whole output: the first key's value
+    is zero, all others are one."""
+    rng = np.random.default_rng(1)
+    n, H, D, G = 3000, 1, 128, 4
+    b = Batch(rng, [n], [new], 64, H, D, 8, fill=False)
+    k, v = np.zeros((n, H, D)), np.ones((n, H, D))
+    k[0], v[0] = 1.0, 0.0
+    b.ref.write(k, v, b.pages, b.lens, np.array([0, n]))
+    b.device(gpu)
+    q, bits = bf16(np.full((new, H * G, D), below * np.log(2) * 128 ** -0.5))
+    out = host(gpu.qcache_attend(b.cache, dev_bf16(bits), b.d_pages, b.d_lens, b.d_starts, out_dtype=torch.float32))
+    ref, mag, owned = b.ref.attend(q, b.pages, b.lens, b.starts)
+    assert ref.max() < 1e-3 * 2.0 ** (10.4 - below) * 3000
+    check_attend(b, q, out, ref, mag, owned, 128 ** -0.5)
+
+
+def test_queries_that_are_not_finite(gpu):
+    """A query row with a NaN or an infinity comes out not finite, the rows beside it as ever."""
+    rng = np.random.default_rng(2)
+    for lens, new in (([300, 33], [1, 1]), ([200, 90], [50, 90])):
+        b = Batch(rng, lens, new, 32, 2, 64, 8).device(gpu)
+        q, bits = bf16(rng.standard_normal((b.T, 8, 64)))
+        bits = bits.copy()
+        bad = np.zeros((b.T, 8), bool)
+        for t, h, word in ((0, 1, 0x7FC0), (1, 6, 0x7F80), (b.T - 1, 3, 0xFF80)):
+            bits[t, h, 5] = word
+            bad[t, h] = True
+        out = host(gpu.qcache_attend(b.cache, dev_bf16(bits), b.d_pages, b.d_lens, b.d_starts, out_dtype=torch.float32))
+        ref, mag, owned = b.ref.attend(q, b.pages, b.lens, b.starts)
+        assert not np.isfinite(out[bad]).all(-1).any()
+        out[bad] = ref[bad]
+        check_attend(b, q, out, ref, mag, owned, 64 ** -0.5)
