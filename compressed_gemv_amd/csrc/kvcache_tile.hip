@@ -8,11 +8,11 @@
 // row by row, values transposed.  fp16 and not bf16 for values and weights: the
 // roundings of both then stay an eighth of the output's own.
 //
-// Measured (8 KV heads of 128, 8 query heads each): 0.95 PFLOP/s for 1024 tokens
-// in front of 33000 cached ones (a large matrix product reaches 1.2 here; all
-// SIMDs multiplying random numbers lower the clock to about two thirds), 0.89 for
-// a prompt of 16000.  Shorter calls pay for starting and ending a tile, about
-// 6 us: 0.81 for chunks of 700 .. 1024 behind 4500 .. 6001, 0.64 for prompts of
+// Measured (8 KV heads of 128, 8 query heads each): 0.92 to 0.96 PFLOP/s for 1024
+// tokens in front of 33000 cached ones (a large matrix product reaches 1.2 here;
+// all SIMDs multiplying random numbers lower the clock to about two thirds), 0.89
+// for a prompt of 16000.  Shorter calls pay for starting and ending a tile, about
+// 6 us: 0.79 for chunks of 700 .. 1024 behind 4500 .. 6001, 0.63 for prompts of
 // 999 .. 2500.
 #include <type_traits>
 
