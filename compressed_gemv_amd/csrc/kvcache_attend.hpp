@@ -70,7 +70,7 @@ __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& 
   while (p.x < p.end) {
     if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane, p.from);
     const TileAt& t = p.t;
-    if (t.b < 0) return false;
+    if (t.b < 0 || t.hi <= p.x) return false;              // (weights that overflow under starts that make no sense)
     w.steps = t.steps;
     const int64_t from = p.x;
     const bool whole = t.lo >= from && t.hi <= p.end;

@@ -289,3 +289,45 @@ def test_queries_that_are_not_finite(gpu):
         assert not np.isfinite(out[bad]).all(-1).any()
         out[bad] = ref[bad]
         check_attend(b, q, out, ref, mag, owned, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("lens", [[30, 3], [1700, 3]])
+def test_long_prefix_for_few(gpu, lens):
+    """A prefix much longer than what follows it, cut into many parts; own tables short (one launch) and long."""
+    for bits, group in ((8, 8), (4, 16), (8, 2)):
+        rng = np.random.default_rng(bits * group)
+        b = Batch(rng, lens, [1, 1], 64, 2, 128, bits, starts=False, prefix=5003)
+        _nan_where_no_token_is(b)
+        _attend(gpu, b.device(gpu), rng, group, shared=True)
+
+
+def test_more_heads_than_workgroups(gpu):
+    rng = np.random.default_rng(600)
+    b = Batch(rng, [40, 7], [1, 1], 16, 600, 64, 8, starts=False, prefix=20).device(gpu)
+    _attend(gpu, b, rng, 2)
+    _attend(gpu, b, rng, 2, shared=True)
+    b = Batch(rng, [170, 7], [30, 1], 16, 600, 64, 4, prefix=20).device(gpu)
+    _attend(gpu, b, rng, 2)
+    _attend(gpu, b, rng, 2, shared=True)
+    x, bits = bf16(rows(rng, (31, 600, 64)))
+    b.ref.write(x, x, b.pages, b.lens, b.starts)
+    gpu.qcache_write(b.cache, dev_bf16(bits), dev_bf16(bits), b.d_pages, b.d_lens, b.d_starts)
+    codes, meta = b.host_buffers()
+    for i in range(2):
+        assert np.array_equal(meta[i], b.ref.meta[i]) and np.array_equal(codes[i], b.ref.codes[i])
+
+
+def test_lens_that_make_no_sense(gpu):
+    """Negative and huge lengths: nothing, and as far as the table goes."""
+    rng = np.random.default_rng(8)
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    for new, starts in (([1] * 5, False), ([9, 4, 30, 1, 2], True)):
+        b = Batch(rng, [33, 48, 20, 48, 5], new, 16, 2, 64, 8, starts=starts, prefix=20).device(gpu)
+        b.lens = np.array([lo, hi, -1, 1000, 5], np.int32)
+        b.d_lens = dev(b.lens)
+        _attend(gpu, b, rng, 4)
+        _attend(gpu, b, rng, 4, shared=True)
+        T = b.T
+        K, V = gpu.qcache_read(b.cache, b.d_pages, b.d_lens, b.d_starts, rows=T, dtype=torch.float32)
+        k, v, owned = b.ref.read(T, b.pages, b.lens, b.starts)
+        assert owned.all() and np.array_equal(host(K), k.astype(np.float32)) and np.array_equal(host(V), v.astype(np.float32))
