@@ -58,7 +58,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 // RT = 8 (one token of a group of up to 8 heads): both halves of the 16 columns
 // hold the same rows, one with the high and one with the low parts of the
 // weights, so that one product does for two.
-template <int D, int BITS, int RT>
+template <int D, int BITS, int RT, bool SPREAD = false>
 __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
   constexpr int NT = RT > 16 ? 2 : 1;
   constexpr bool PACK = RT == 8;
@@ -76,9 +76,9 @@ __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
   const int heads = a.c.heads, h = block % heads;
-  Pieces pieces = pieces_of(x, block / heads, lane);
+  Pieces pieces = pieces_of<SPREAD>(x, block / heads, lane);
   Work w;
-  while (next_work<false>(x, pieces, w, lane)) {
+  while (next_work<false, false, SPREAD>(x, pieces, w, lane)) {
   f32x4_t acc[NT][TILES];
   float m[NT], l[NT], po[NT];              // maximum, sum of weights, sum of weights times offsets
 #pragma unroll
@@ -428,6 +428,13 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, RT)) void kv_rows_kernel(At
   rows_body<D, BITS, RT>(x, blockIdx.x);
 }
 
+// For few tiles: no piece holds parts of two.  A kernel of its own, since the
+// second way to find work costs the other 1 %.
+template <int D, int BITS, int RT>
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, RT)) void kv_rows_spread_kernel(AttendArgs x) {
+  rows_body<D, BITS, RT, true>(x, blockIdx.x);
+}
+
 // Two sets of tiles of one height, a short prefix's and the sequences' own:
 // one launch of both is 22 -> 17 us for 6 sequences of 40 behind 701 tokens.
 // A kernel of its own, since the choice costs the other 4 % of 131072 keys.
@@ -540,11 +547,23 @@ __global__ __launch_bounds__(256) void kv_join_cuts_kernel(AttendArgs x) {
   const int h = blockIdx.x % a.c.heads, i = blockIdx.x / a.c.heads + 1;
   const Line line = line_of(x.s, x.rule, lane);
   if (i >= line.N) return;
-  const int64_t cut = line.cut(i);
-  const TileAt t = tile_at(x.s, x.rule, cut, lane);
-  if (t.b < 0 || t.lo == cut) return;
-  const int i0 = line.piece(t.lo), parts = line.piece(t.hi - 1) - i0 + 1;
-  const int slot0 = (int)slot_of(line, t, i0, false);
+  TileAt t;
+  int i0, parts, slot0;
+  if (x.rule.spread) {
+    const PartAt p = part_at(x.s, x.rule, line, i, lane);
+    if (p.t.b < 0 || p.first == i) return;
+    t = p.t;
+    i0 = p.first;
+    parts = p.parts;
+    slot0 = 2 * i0;
+  } else {
+    const int64_t cut = line.cut(i);
+    t = tile_at(x.s, x.rule, cut, lane);
+    if (t.b < 0 || t.lo == cut) return;
+    i0 = line.piece(t.lo);
+    parts = line.piece(t.hi - 1) - i0 + 1;
+    slot0 = (int)slot_of(line, t, i0, false);
+  }
   if (2 * (i0 + parts) > x.part.slots) return;
   const int row0 = t.tile * x.rule.rt, rows = t.r.count * a.group - row0, n = rows < x.rule.rt ? rows : x.rule.rt;
   // the tile's rows go round the workgroups of its cuts, gridDim.y of them each
@@ -628,6 +647,7 @@ hipError_t launch_kv_rows(const AttendArgs& x, const AttendArgs* y, int head_dim
 #define ROWS(D, B, R)                                                                                         \
   do {                                                                                                        \
     if (y) hipLaunchKernelGGL((kv_rows_pair_kernel<D, B, R>), grid, dim3(256), 0, st, x, *y, split);          \
+    else if (x.rule.spread) hipLaunchKernelGGL((kv_rows_spread_kernel<D, B, R>), grid, dim3(256), 0, st, x);  \
     else hipLaunchKernelGGL((kv_rows_kernel<D, B, R>), grid, dim3(256), 0, st, x);                            \
   } while (0)
 #define ROWS_N(D, B)                          \
@@ -697,7 +717,8 @@ struct CallPlan {
 int tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
 
 // The division of tiles of rt rows of `seqs` sequences with at most cap keys each.
-SplitRule rule_for(int rt, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut) {
+SplitRule rule_for(int rt, int64_t total_rows, int64_t seqs, int group, int heads, int cap, bool must_cut,
+                   bool keep) {
   SplitRule r{};
   r.group = group;
   r.rt = rt;
@@ -711,6 +732,13 @@ SplitRule rule_for(int rt, int64_t total_rows, int64_t seqs, int group, int head
   r.single = r.whole && n >= most;
   if (n > most) n = most;
   r.wgs = (int)(n < 1 ? 1 : n);
+  // Few tiles of few keys, four or more pieces each: a piece with parts of two
+  // tiles takes 4 us longer than the others, and pieces of one tile only have up
+  // to N / (N - T) of an even share of the keys, which is more where there are
+  // many (5 rows of 8 sequences of 200 .. 3001, 4 bits: 25.2 -> 20.4 us; 7 of 3008
+  // 26.6 -> 23.9; but 3 of 20000, 15 steps by this count, 35 -> 38).
+  const int64_t tiles = total_rows / rt + seqs;
+  r.spread = r.rt <= 32 && !r.whole && !must_cut && !keep && tiles * 4 <= r.wgs && tiles * ceil_div(cap, r.ku) <= 6 * r.wgs;
   return r;
 }
 
@@ -723,13 +751,13 @@ CallPlan plan_call(int64_t B, int64_t T, int64_t max_pages, int page_shift, int 
   const int pre_rt = tile_rows(T * group);
   p.pair = p.shared && pre_rt <= 32 && cap <= kWholeKeys / 2;
   if (p.pair) rt = pre_rt;
-  p.own = rule_for(rt, T * group, B, group, heads, (int)cap, false);
+  p.own = rule_for(rt, T * group, B, group, heads, (int)cap, false, p.shared);
   const int64_t tiles = T * group / rt + B;                 // at most, over all sequences
   p.own_slots = p.shared ? p.own.wgs + tiles : 2 * p.own.wgs;
   p.join = p.shared || (!p.own.whole && p.own.wgs > 1);
   if (!p.join) p.own_slots = 0;
   if (p.shared) {
-    p.pre = rule_for(pre_rt, T * group, 1, group, heads, (int)prefix_len, true);
+    p.pre = rule_for(pre_rt, T * group, 1, group, heads, (int)prefix_len, true, true);
     p.pre.sloped = false;                                   // every row sees all of it
     p.pre_slots = p.pre.wgs + ceil_div(T * group, pre_rt);
     p.pre_line = Line{ceil_div(T * group, pre_rt) * ceil_div(prefix_len, p.pre.ku) * kSub, p.pre.wgs, 1};

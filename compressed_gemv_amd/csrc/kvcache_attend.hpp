@@ -40,10 +40,11 @@ struct Pieces {
   Cursor from;
 };
 
+template <bool SPREAD = false>
 __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int lane) {
   Pieces p;
   p.from = Cursor{};
-  if (x.rule.single) {                     // found without a look at the other sequences' weights
+  if (!SPREAD && x.rule.single) {                     // found without a look at the other sequences' weights
     p.line = Line{};
     p.piece = piece;
     p.x = (int64_t)piece * kSub;
@@ -55,7 +56,9 @@ __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int 
   p.piece = piece;
   p.x = p.end = 0;
   p.t.b = -1;
-  if (piece < p.line.N) {
+  if constexpr (SPREAD) {
+    p.end = piece < p.line.N ? 1 : 0;      // one tile
+  } else if (piece < p.line.N) {
     p.x = p.line.cut(piece);
     p.end = p.line.cut(piece + 1);
   }
@@ -65,25 +68,19 @@ __device__ __forceinline__ Pieces pieces_of(const AttendArgs& x, int piece, int 
 // ADVANCE: from tile to tile of a sequence without a search, for which a piece
 // of many tiles keeps more state (a prompt's tiles 267 -> 251 us; the kernel for
 // few rows, whose tiles are mostly sequences, is 1 % slower with it).
-template <bool ADVANCE, bool STEPS = false>
+// SPREAD: for rules that say so.
+template <bool ADVANCE, bool STEPS = false, bool SPREAD = false>
 __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& w, int lane) {
-  while (p.x < p.end) {
-    if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane, p.from);
-    const TileAt& t = p.t;
-    if (t.b < 0 || t.hi <= p.x) return false;              // (weights that overflow under starts that make no sense)
-    w.steps = t.steps;
-    const int64_t from = p.x;
-    const bool whole = t.lo >= from && t.hi <= p.end;
+  // the tile's rows and the steps of keys that its last row, which sees the most, needs
+  auto tile = [&](const TileAt& t) {
     w.t0 = t.r.t0;
     w.rows = t.r.count * x.a.group;
     w.vis0 = t.r.vis0;
     w.need = t.r.need;
     w.causal = x.s.lens != nullptr;
-    w.direct = whole && !x.keep;
     w.pages = x.s.pages + (int64_t)t.b * x.s.max_pages;
     w.max_pages = x.s.max_pages;
     w.row0 = t.tile * x.rule.rt;
-    // the last row of the tile sees the most
     int last = w.row0 + x.rule.rt - 1;
     if (last >= w.rows) last = w.rows - 1;
     int vis = w.need;
@@ -91,14 +88,40 @@ __device__ __forceinline__ bool next_work(const AttendArgs& x, Pieces& p, Work& 
       const int v = w.vis0 + last / x.a.group;
       vis = v < 0 ? 0 : (v < w.need ? v : w.need);
     }
+    return vis;
+  };
+  auto keys = [&](int u0, int u1, int vis) {
+    w.k0 = u0 * x.rule.ku;
+    w.k1 = u1 * x.rule.ku < vis ? u1 * x.rule.ku : vis;
+    if (w.k0 > w.k1) w.k0 = w.k1;
+  };
+  if constexpr (SPREAD) {
+    if (p.x >= p.end) return false;
+    p.x = p.end;
+    const PartAt a = part_at(x.s, x.rule, p.line, p.piece, lane);
+    if (a.t.b < 0) return false;
+    const int vis = tile(a.t), units = (vis + x.rule.ku - 1) / x.rule.ku, c = p.piece - a.first;
+    keys((int)((int64_t)units * c / a.parts), (int)((int64_t)units * (c + 1) / a.parts), vis);
+    w.steps = 0;
+    w.direct = a.parts == 1;
+    w.slot = 2 * p.piece;
+    return w.direct || w.slot < x.part.slots;
+  }
+  while (p.x < p.end) {
+    if (!ADVANCE || p.t.b < 0 || !p.t.advance()) p.t = tile_at<false, STEPS>(x.s, x.rule, p.x, lane, p.from);
+    const TileAt& t = p.t;
+    if (t.b < 0 || t.hi <= p.x) return false;              // (weights that overflow under starts that make no sense)
+    w.steps = t.steps;
+    const int64_t from = p.x;
+    const bool whole = t.lo >= from && t.hi <= p.end;
+    w.direct = whole && !x.keep;
+    const int vis = tile(t);
     // the cuts, from weights to whole steps of the tile's keys
     const int units = (vis + x.rule.ku - 1) / x.rule.ku;
     const double per = (double)units / (double)(t.hi - t.lo);
     const int u0 = from <= t.lo ? 0 : __builtin_amdgcn_readfirstlane((int)((double)(from - t.lo) * per));
     const int u1 = p.end >= t.hi ? units : __builtin_amdgcn_readfirstlane((int)((double)(p.end - t.lo) * per));
-    w.k0 = u0 * x.rule.ku;
-    w.k1 = u1 * x.rule.ku < vis ? u1 * x.rule.ku : vis;
-    if (w.k0 > w.k1) w.k0 = w.k1;
+    keys(u0, u1, vis);
     p.x = t.hi;
     if (w.direct) return true;
     const int64_t slot = slot_of(p.line, t, p.piece, x.keep);

@@ -10,8 +10,10 @@
 // tiles of the batch form one line of U weights per KV head, which is cut into
 // N equal pieces, one per workgroup, wherever the cuts fall: no workgroup has
 // more to do than another, however unequal the sequences are.  A tile that a
-// cut goes through leaves partial results, which the join adds up.  All of it
-// in integers, so every wave of every kernel finds the same cuts.
+// cut goes through leaves partial results, which the join adds up.  Where there
+// are few tiles the line is spread instead: every tile gets pieces of its own,
+// about its share of them.  All of it in integers and in fp64 products that are
+// the same everywhere, so every wave of every kernel finds the same cuts.
 #pragma once
 
 #include "common.hpp"
@@ -28,6 +30,7 @@ struct SplitRule {
   bool whole;                  // tiles are never cut: each weighs one step
   bool single;                 // and there is a workgroup for every tile there can be: piece i is tile i
   bool sloped;                 // weigh a sequence's tiles by what each sees
+  bool spread;                 // no piece holds parts of two tiles
   int extra;                   // weight of what a tile costs beside its keys
 };
 
@@ -113,6 +116,11 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 struct Line {
   int64_t U;                   // in grains: kSub where tiles are not cut, else 1
   int N, grain;
+  double rate;                 // spread: pieces for a weight beside one for each tile
+  // spread: the first piece of what begins at weight x as tile number `tile`.
+  // Pieces of a tile: 1 + about its share of the N - T left over, so each has
+  // at most U / (N - T) to do.
+  __device__ __forceinline__ int first(int64_t x, int64_t tile) const { return (int)(tile + (int64_t)((double)x * rate)); }
   __device__ __forceinline__ int64_t cut(int i) const {
     return uniform((int64_t)((double)i * (double)U / (double)N)) * grain;
   }
@@ -124,10 +132,11 @@ struct Line {
 };
 
 __device__ __forceinline__ Line line_of(const SeqView& s, const SplitRule& p, int lane) {
-  int64_t u = 0;
+  int64_t u = 0, tiles = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
     const Weights w = weights_of(p, seq_rows(s, b0 + lane, p.cap));
     u += w.before(w.tiles);
+    tiles += w.tiles;
   }
   Line l;
   u = lane_i64(wave_scan(u), 63);
@@ -136,6 +145,11 @@ __device__ __forceinline__ Line line_of(const SeqView& s, const SplitRule& p, in
   const int64_t n = u / kSub;                              // a piece is a step of keys at least
   l.N = n < p.wgs ? (int)n : p.wgs;
   if (l.N < 1) l.N = 1;
+  l.rate = 0.;
+  if (p.spread) {
+    tiles = lane_i64(wave_scan(tiles), 63);
+    if (tiles < l.N) l.rate = (double)(l.N - tiles) / (double)u;
+  }
   return l;
 }
 
@@ -223,6 +237,58 @@ __device__ __forceinline__ TileAt tile_at(const SeqView& s, const SplitRule& p, 
   return tile_at<BY_INDEX>(s, p, x, lane, from);
 }
 
+// The tile that piece number `piece` of a spread line belongs to, its first
+// piece and its number of pieces; t.b < 0: none.
+struct PartAt {
+  TileAt t;
+  int first, parts;
+};
+
+__device__ __forceinline__ PartAt part_at(const SeqView& s, const SplitRule& p, const Line& line, int piece, int lane) {
+  PartAt a{};
+  a.t.b = -1;
+  int64_t carry = 0, tiles = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    const SeqRows r = seq_rows(s, b0 + lane, p.cap);
+    const Weights w = weights_of(p, r);
+    const int64_t u = w.before(w.tiles), inc = wave_scan(u), tinc = wave_scan((int64_t)w.tiles);
+    const uint64_t m = __ballot(line.first(carry + inc, tiles + tinc) > piece);
+    if (m) {
+      const int l = __ffsll((unsigned long long)m) - 1;
+      Weights& v = a.t.v;
+      v.tiles = __builtin_amdgcn_readlane(w.tiles, l);
+      v.A = __builtin_amdgcn_readlane(w.A, l);
+      v.S = __builtin_amdgcn_readlane(w.S, l);
+      a.t.base = carry + lane_i64(inc, l) - lane_i64(u, l);
+      const int64_t first = tiles + lane_i64(tinc, l) - v.tiles;
+      auto begin = [&](int tile) {
+        return __builtin_amdgcn_readfirstlane(line.first(a.t.base + v.before(tile), first + tile));
+      };
+      int lo = 0, n = v.tiles;                             // last tile that begins at or before the piece
+      while (n > 1) {
+        const int half = n >> 1;
+        if (begin(lo + half) <= piece) { lo += half; n -= half; }
+        else n = half;
+      }
+      a.t.tile = lo;
+      a.t.index = first + lo;
+      a.first = begin(lo);
+      a.parts = begin(lo + 1) - a.first;
+      // (starts that overlap can make more tiles than there are numbers)
+      if (a.first < 0 || a.first > piece || piece - a.first >= a.parts) return a;
+      a.t.b = b0 + l;
+      a.t.r.t0 = __builtin_amdgcn_readlane(r.t0, l);
+      a.t.r.count = __builtin_amdgcn_readlane(r.count, l);
+      a.t.r.vis0 = __builtin_amdgcn_readlane(r.vis0, l);
+      a.t.r.need = __builtin_amdgcn_readlane(r.need, l);
+      return a;
+    }
+    carry += lane_i64(inc, 63);
+    tiles += lane_i64(tinc, 63);
+  }
+  return a;
+}
+
 // Step x of all the sequences' steps of keys; b < 0: none.
 struct StepAt {
   int b, step, need;
@@ -248,7 +314,8 @@ __device__ __forceinline__ StepAt step_at(const SeqView& s, const SplitRule& p, 
 // Partial results: slots of RT rows, per row the unnormalised sum of D values,
 // its maximum (log2 domain) and its sum of weights.  A piece has at most two
 // tiles that a cut goes through, its first and its last; where everything is
-// kept (a shared prefix joins in), piece + tile index numbers the parts.
+// kept (a shared prefix joins in), piece + tile index numbers the parts; in a
+// spread line piece i has slot 2 i.
 struct Partials {
   float* o;                    // [slot][head][rt][D]
   float* ml;                   // [slot][head][rt][2]

@@ -331,3 +331,16 @@ def test_lens_that_make_no_sense(gpu):
         K, V = gpu.qcache_read(b.cache, b.d_pages, b.d_lens, b.d_starts, rows=T, dtype=torch.float32)
         k, v, owned = b.ref.read(T, b.pages, b.lens, b.starts)
         assert owned.all() and np.array_equal(host(K), k.astype(np.float32)) and np.array_equal(host(V), v.astype(np.float32))
+
+
+@pytest.mark.parametrize("B", [1, 2, 3, 7])
+def test_few_long_sequences(gpu, B):
+    """A few sequences with many workgroups each, of very different lengths, some without tokens: one row and more."""
+    rng = np.random.default_rng(B)
+    lens = [4001, 1, 2047, 0, 129, 3100, 640][:B]
+    for bits, group, new in ((8, 8, 1), (4, 5, 3), (8, 4, 7), (4, 16, 1)):
+        say(f"{B} sequences, b{bits} g{group}, {new} tokens")
+        b = Batch(rng, lens, [min(n, new) if new > 1 else 1 for n in lens], 16, 2, 128 if bits == 8 else 64, bits,
+                  starts=new > 1)
+        _nan_where_no_token_is(b)
+        _attend(gpu, b.device(gpu), rng, group)
