@@ -711,7 +711,6 @@ def make_qcache(n_pages: int, page_size: int, heads: int, head_dim: int, bits: i
     c = qcache(n_pages, page_size, heads, head_dim, bits, *(t.data_ptr() for t in given))
     c._tensors = given
     c._device, c._index = given[0].device, given[0].get_device()
-    c._ref = ctypes.byref(c)
     return c
 
 
@@ -767,7 +766,7 @@ def _cache_call(cache: qcache, stream, fresh, what, fn, *args):
     recorded on before they can be reused."""
     idx = cache._index
     if stream is None and idx == torch._C._cuda_getDevice():
-        status = fn(cache._ref, *args, torch._C._cuda_getCurrentRawStream(idx))
+        status = fn(cache, *args, torch._C._cuda_getCurrentRawStream(idx))
     else:
         if stream is None:
             stream = torch.cuda.current_stream(cache._device)
@@ -777,7 +776,7 @@ def _cache_call(cache: qcache, stream, fresh, what, fn, *args):
             if t is not None:
                 t.record_stream(stream)
         with torch.cuda.device(cache._device):
-            status = fn(cache._ref, *args, stream.cuda_stream)
+            status = fn(cache, *args, stream.cuda_stream)
     if status != Q_OK:
         raise QError(status, what)
 
