@@ -760,21 +760,34 @@ def _on_device(cache: qcache, dense: bool, *ts):
             raise ValueError("pages, lens, starts and ws must be contiguous")
 
 
-def _cache_call(cache: qcache, stream, fresh, what, fn, *args):
-    """fn(cache, *args, stream) on the cache's device.  fresh: tensors this
-    binding allocated, which a stream other than the current one must be
-    recorded on before they can be reused."""
+def _stream_of(cache: qcache, stream):
+    if stream.device != cache._device:
+        raise ValueError(f"stream on {stream.device}, tensors on {cache._device}")
+    return stream
+
+
+def _fresh(cache: qcache, stream, shape, dtype, returned: bool) -> torch.Tensor:
+    """A tensor for a call on `stream` (None: the current one), out of that
+    stream's memory pool: a block that the current stream's pool hands out may
+    still be used by work queued there, which `stream` does not wait for.  A
+    result is recorded on the current stream as well, where the caller goes on
+    to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache._device)
+    with torch.cuda.stream(_stream_of(cache, stream)):
+        t = torch.empty(shape, dtype=dtype, device=cache._device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(cache._device))
+    return t
+
+
+def _cache_call(cache: qcache, stream, what, fn, *args):
+    """fn(cache, *args, stream) on the cache's device."""
     idx = cache._index
     if stream is None and idx == torch._C._cuda_getDevice():
         status = fn(cache, *args, torch._C._cuda_getCurrentRawStream(idx))
     else:
-        if stream is None:
-            stream = torch.cuda.current_stream(cache._device)
-        elif stream.device != cache._device:
-            raise ValueError(f"stream on {stream.device}, tensors on {cache._device}")
-        for t in fresh:
-            if t is not None:
-                t.record_stream(stream)
+        stream = torch.cuda.current_stream(cache._device) if stream is None else _stream_of(cache, stream)
         with torch.cuda.device(cache._device):
             status = fn(cache, *args, stream.cuda_stream)
     if status != Q_OK:
@@ -796,7 +809,7 @@ def qcache_write(cache: qcache, K: torch.Tensor, V: torch.Tensor, pages, lens, s
     _on_device(cache, False, K, V)
     if T == 0:
         return
-    _cache_call(cache, stream, (), "qcache_write", load().qcache_write, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
+    _cache_call(cache, stream, "qcache_write", load().qcache_write, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
                 _dtype_code(K))
 
 
@@ -806,17 +819,17 @@ def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = N
     starts[b+1] - starts[b] tokens of each sequence, the last one without
     starts.  rows: starts[B] when no outputs are given (host knowledge; the
     call does not look at device data).  Rows no sequence owns are not
-    written."""
-    fresh = ()
+    written.  Outputs allocated here belong to `stream`: another stream waits
+    for it before it reads them."""
     heads, D = cache.heads, cache.head_dim
-    if K is None and V is None:
+    given = K is not None or V is not None
+    if not given:
         if rows is None:
             if starts is not None:
                 raise ValueError("rows: missing, and no outputs given")
             rows = pages.shape[0]
         if dtype not in _OUT:
             raise ValueError(f"dtype {dtype}, expected one of {_OUT}")
-        K, V = fresh = torch.empty((2, rows, heads, D), dtype=dtype, device=cache._device).unbind(0)
         T, ks, vs = rows, heads * D, heads * D
     elif K is None or V is None:
         raise ValueError("K and V: both outputs or neither")
@@ -829,9 +842,11 @@ def qcache_read(cache: qcache, pages, lens, starts=None, rows: Optional[int] = N
         _on_device(cache, False, K, V)
     seqs = _cache_seqs(cache, T, pages, lens, starts)
     _on_device(cache, True, pages, lens, starts)
+    if not given:
+        K, V = _fresh(cache, stream, (2, T, heads, D), dtype, True).unbind(0)
     if T == 0:
         return K, V
-    _cache_call(cache, stream, fresh, "qcache_read", load().qcache_read, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
+    _cache_call(cache, stream, "qcache_read", load().qcache_read, seqs, K.data_ptr(), ks, V.data_ptr(), vs,
                 _dtype_code(K))
     return K, V
 
@@ -860,11 +875,9 @@ def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_d
     T, q_heads, _ = shape
     q_stride = _cache_rows(Q, q_heads, D, _Q16, "Q")
     seqs = _cache_seqs(cache, T, pages, lens, starts)
-    fresh_out = fresh_ws = None
     if out is None:
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype {out_dtype}, expected one of {_OUT}")
-        out = fresh_out = torch.empty((T, q_heads, D), dtype=out_dtype, device=Q.device)
         o_stride = q_heads * D
     else:
         o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
@@ -872,12 +885,14 @@ def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_d
             raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
     _on_device(cache, True, pages, lens, starts)
     _on_device(cache, False, Q, out)
+    if out is None:
+        out = _fresh(cache, stream, (T, q_heads, D), out_dtype, True)
     if T == 0:
         return out
     n_prefix = prefix[1] if prefix else 0
     need = _attend_ws(cache.page_size, heads, D, cache.bits, seqs.B, T, seqs.max_pages, q_heads, n_prefix)
     if ws is None:
-        ws = fresh_ws = torch.empty(need, dtype=torch.uint8, device=cache._device)
+        ws = _fresh(cache, stream, need, torch.uint8, False)
         ws_bytes = need
     else:
         _need_bytes(ws, need, "ws")
@@ -887,10 +902,9 @@ def _cache_attend(what, cache, Q, prefix, pages, lens, starts, scale, out, out_d
             Q_F32 if out.dtype == torch.float32 else Q_BF16, ws.data_ptr(), ws_bytes)
     if prefix:
         _on_device(cache, True, prefix[0])
-        _cache_call(cache, stream, (fresh_out, fresh_ws), what, load().qcache_attend_shared, seqs, prefix[0].data_ptr(),
-                    n_prefix, *rest)
+        _cache_call(cache, stream, what, load().qcache_attend_shared, seqs, prefix[0].data_ptr(), n_prefix, *rest)
     else:
-        _cache_call(cache, stream, (fresh_out, fresh_ws), what, load().qcache_attend, seqs, *rest)
+        _cache_call(cache, stream, what, load().qcache_attend, seqs, *rest)
     return out
 
 
@@ -900,7 +914,8 @@ def qcache_attend(cache: qcache, Q: torch.Tensor, pages, lens, starts=None, scal
     """out [T][q_heads][head_dim] (bf16 or fp32): causal attention of rows Q
     (bf16) over the cached tokens of their sequences; pages, lens and starts
     as qcache_write's, whose rows these are.  scale: head_dim^-1/2 by
-    default.  Calls that may overlap need a workspace each."""
+    default.  Calls that may overlap need a workspace each.  An output that is
+    allocated here belongs to `stream`: another stream waits for it first."""
     return _cache_attend("qcache_attend", cache, Q, (), pages, lens, starts, scale, out, out_dtype, ws, stream)
 
 
