@@ -89,8 +89,10 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
 /* out[t][hq][:] = sum_j softmax_j(scale <Q[t][hq][:], k_j>) v_j over the
  * positions j of the row's own sequence up to the row's own position, KV head
  * hq / (q_heads / heads); q_heads a multiple of heads, at most 64 times it.
- * Q is bf16, of magnitudes below 2^63 (2^-57 and less may count as 0), out
- * bf16 or fp32 (out_dtype); rows of one token contiguous, q_stride and o_stride
+ * scale is finite (else Q_EINVAL) and of magnitude 2^45 at most (else
+ * Q_EUNSUPPORTED); |scale| sum_i |Q_i k_i| has to stay below 2^120.  Q is bf16,
+ * of magnitudes below 2^63 (2^-57 and less may count as 0), out bf16 or fp32
+ * (out_dtype); rows of one token contiguous, q_stride and o_stride
  * elements between tokens; Q and out 16-byte aligned, strides a multiple of
  * 16 bytes.  A row that sees nothing is zero.  Sums, maxima and the softmax
  * statistics are fp32.  ws: device, 16-byte aligned, >= the

@@ -3,6 +3,7 @@ call's temporaries come from."""
 import gc
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -115,3 +116,18 @@ def test_a_stream_of_another_device_is_refused(lib):
                  lambda: cg.qcache_attend_shared(cache, Q, pages[0], 20, pages, lens, stream=other)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_a_scale_beyond_the_kernels_constants_is_refused(lib):
+    """scale * log2(e) * 2^69 * s is held in fp32: finite up to a scale of 2^45 for the largest s there is."""
+    largest = 2 * 65280 / 15
+    with np.errstate(over="ignore"):
+        product = [np.float32(2.0 ** p * np.log2(np.e)) * np.float32(2.0 ** 69) * np.float32(largest) for p in (45, 46)]
+    assert np.isfinite(product[0]) and np.isinf(product[1])
+    c, s = cg.qcache(4, 16, 2, 64, 8, *(0x10000,) * 4), cg.qseqs(3, 7, 2, *(0x10000,) * 3)
+    for scale, status in ((2.0 ** 45, cg.Q_EWORKSPACE), (-2.0 ** 45, cg.Q_EWORKSPACE), (2.0 ** 45 * 1.001, cg.Q_EUNSUPPORTED),
+                          (-2.0 ** 59, cg.Q_EUNSUPPORTED), (3e38, cg.Q_EUNSUPPORTED)):
+        # a good scale gets as far as the workspace, which is missing
+        assert lib.qcache_attend(c, s, 0x10000, 512, 8, scale, 0x10000, 512, cg.Q_BF16, None, 0, None) == status, scale
+        assert lib.qcache_attend_shared(c, s, 0x10000, 5, 0x10000, 512, 8, scale, 0x10000, 512, cg.Q_BF16, None, 0,
+                                        None) == status, scale
