@@ -697,7 +697,9 @@ def make_qcache(n_pages: int, page_size: int, heads: int, head_dim: int, bits: i
                 v_codes=None, v_meta=None, device=None) -> qcache:
     """A cache descriptor over the given buffers, or over new ones (zeros) on
     device when none are given; it keeps references to the tensors it points
-    into (._tensors: k_codes, k_meta, v_codes, v_meta)."""
+    into (._tensors: k_codes, k_meta, v_codes, v_meta).  Buffers that hold
+    anything but what qcache_write put there keep to its range: see
+    include/qcache.h."""
     cb, mb = qcache_sizes(n_pages, page_size, heads, head_dim, bits)
     given = (k_codes, k_meta, v_codes, v_meta)
     if all(t is None for t in given):
@@ -923,8 +925,9 @@ def qcache_attend_shared(cache: qcache, Q: torch.Tensor, prefix_pages, prefix_le
                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                          out_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None, stream=None):
     """qcache_attend behind a prefix of prefix_len tokens (pages prefix_pages,
-    int32) that all rows see, read once for the whole batch.  pages and lens
-    describe the sequences' own tokens only."""
+    int32) that all rows see, read once for every 256 rows of a KV head and not
+    for every sequence.  pages and lens describe the sequences' own tokens
+    only."""
     if prefix_pages is None or prefix_pages.dtype != torch.int32:
         raise ValueError("prefix_pages must be int32")
     if prefix_len < 1:

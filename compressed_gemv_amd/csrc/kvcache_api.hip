@@ -86,7 +86,7 @@ int attend(const qcache* c, const qseqs* s, const int32_t* prefix_pages, int64_t
   size_t need = 0;
   if ((st = qcache_attend_ws(c, s, q_heads, prefix_len, &need)) != Q_OK) return st;
   if (!isfinite(scale) || (out_dtype != Q_BF16 && out_dtype != Q_F32)) return Q_EINVAL;
-  // the kernel for few rows holds scale * log2(e) * 2^69 * s in fp32, s at most 8704 (a 4-bit row of +-65280)
+  // the kernel for few rows holds scale * log2(e) * 2^69 * s in fp32, s at most 8734 (a 4-bit row over +-65504)
   if (fabsf(scale) > 0x1p45f) return Q_EUNSUPPORTED;
   const int64_t width = (int64_t)q_heads * c->head_dim;
   if ((st = rows_ok(Q, q_stride, width, 2)) != Q_OK) return st;

@@ -21,7 +21,11 @@
  * (fp64), q = rint((x - o)/s) in fp64, ties to even.  Values beyond +-65280
  * are stored as +-65280, so that no level leaves fp16.  A row that holds an
  * infinity or a NaN gets s = o = NaN and codes 0: it reads back as NaN, and an
- * attention row that sees it comes out as NaN.
+ * attention row that sees it comes out as NaN.  Buffers that are filled by
+ * other means have to keep to the same range: in every row that holds a token
+ * o and s*(2^b - 1) + o lie within +-65504, or s and o are NaN (qcache_attend
+ * forms values in fp16, and one beyond it would reach rows that do not see its
+ * token).  Rows that hold no token may be anything.
  *
  * Sequences: every call takes the batch as a qseqs.  Rows of K, V, Q and the
  * outputs are ragged: sequence b owns rows starts[b] .. starts[b+1]-1, its
@@ -92,19 +96,32 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
  * scale is finite (else Q_EINVAL) and of magnitude 2^45 at most (else
  * Q_EUNSUPPORTED); |scale| sum_i |Q_i k_i| has to stay below 2^120.  Q is bf16,
  * of magnitudes below 2^63 (2^-57 and less may count as 0), out bf16 or fp32
- * (out_dtype); rows of one token contiguous, q_stride and o_stride
- * elements between tokens; Q and out 16-byte aligned, strides a multiple of
- * 16 bytes.  A row that sees nothing is zero.  Sums, maxima and the softmax
- * statistics are fp32.  ws: device, 16-byte aligned, >= the
- * qcache_attend_ws value; calls that may overlap need one each. */
+ * (out_dtype); rows of one token contiguous, q_stride and o_stride elements
+ * between tokens; Q and out 16-byte aligned, strides a multiple of 16 bytes.
+ * A row that sees nothing is zero.
+ * Precision: sums, maxima and the softmax statistics are fp32.  Let R be
+ * ceil(T / B) * q_heads / heads, the rows of a KV head and sequence on average
+ * (qcache_attend_shared: T * q_heads / heads for the prefix's keys, and for all
+ * where that is at most 32 and tables hold at most 768 positions).  For R <= 32
+ * keys and values enter as they are and weights with 16 bits; beyond, keys,
+ * values and weights are rounded to 11 bits and queries to 2^-25 of their row's
+ * largest, also where the output is fp32.  So a row's last bits depend on the
+ * other rows of the call, but not on when or how often it runs.
+ * Speed: which kernels run is chosen on the host from B, T and max_pages (the
+ * lengths stay on the device), so a page table no wider than the longest
+ * sequence can become is the fastest, and decode steps and chunks of prompts
+ * are faster in a call each than in one together.
+ * ws: device, 16-byte aligned, >= the qcache_attend_ws value; calls that may
+ * overlap need one each. */
 int qcache_attend(const qcache* c, const qseqs* s, const void* Q, int64_t q_stride, int q_heads, float scale,
                   void* out, int64_t o_stride, int out_dtype, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* The same with a prefix that every row of the call sees before its own
  * sequence: prefix_len tokens (>= 1) in the pages prefix_pages (device,
- * ceil(prefix_len / page_size) entries).  Its rows are read once for the whole batch.
- * lens, starts and pages describe each sequence's own tokens only, and
- * lens[b] = 0 is a sequence that so far is the prefix alone. */
+ * ceil(prefix_len / page_size) entries).  Its rows are read once for every 256
+ * attention rows of a KV head (T * q_heads / heads in all), not once for every
+ * sequence.  lens, starts and pages describe each sequence's own tokens only,
+ * and lens[b] = 0 is a sequence that so far is the prefix alone. */
 int qcache_attend_shared(const qcache* c, const qseqs* s, const int32_t* prefix_pages, int64_t prefix_len,
                          const void* Q, int64_t q_stride, int q_heads, float scale, void* out,
                          int64_t o_stride, int out_dtype, void* ws, size_t ws_bytes, hipStream_t stream);

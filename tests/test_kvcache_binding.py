@@ -120,7 +120,7 @@ def test_a_stream_of_another_device_is_refused(lib):
 
 def test_a_scale_beyond_the_kernels_constants_is_refused(lib):
     """scale * log2(e) * 2^69 * s is held in fp32: finite up to a scale of 2^45 for the largest s there is."""
-    largest = 2 * 65280 / 15
+    largest = 2 * 65504 / 15
     with np.errstate(over="ignore"):
         product = [np.float32(2.0 ** p * np.log2(np.e)) * np.float32(2.0 ** 69) * np.float32(largest) for p in (45, 46)]
     assert np.isfinite(product[0]) and np.isinf(product[1])
