@@ -7,10 +7,12 @@
 // IEEE implementation of the definition.
 //
 // Measured (8 heads of 128): four prompts of 517 .. 4096 tokens at 4 bits are
-// written in 17 us, about 12 of them the vector unit's instructions, and read
-// back in 10 (4.9 TB/s read and written); 16 sequences of 300 .. 4000 tokens at
-// 8 bits are read back in 47 us, 4.5 TB/s, next to a plain copy's 4.8.  16 single
-// tokens take 3.5 us either way, a launch's own time.
+// written in 18 us, in which a SIMD issues 6800 vector instructions (counted),
+// 13 us at 4 clocks each and 2.1 GHz, beside 10 us of memory at a copy's rate,
+// and read back in 10.6 (4.5 TB/s read and written).  16 sequences of 300 .. 4000
+// tokens at 8 bits are read back in 47 us, 4.5 TB/s next to a plain copy's 4.8,
+// or in 39 into a block that was just written (the last-level cache takes the
+// stores).  16 single tokens take 3.6 us either way, a launch's own time.
 #pragma clang fp contract(off)
 
 #include "common.hpp"

@@ -15,10 +15,11 @@
 // probability does, since codes count from the row's minimum.
 //
 // Measured (8 KV heads of 128, 8 query heads each): 32 sequences of 1000 .. 8000
-// tokens at 8 bits 57 us, 5.4 TB/s of codes and constants, 6.2 over longer
-// ones, bound by memory; 4 of 100000 .. 131072 at 4 bits 98 us, 5.1 TB/s, where
-// the vector unit's decoding and softmax (about 260 instructions for 32 keys)
-// take as long as the loads.  A third step in flight at 4 bits was no faster.
+// tokens at 8 bits 58 us, 5.2 TB/s of codes and constants, 6.4 over 32000 each,
+// bound by memory; 4 of 100000 .. 131072 at 4 bits 96 us, 5.2 TB/s, where
+// decoding, products and softmax are 270 vector instructions for 32 keys
+// (counted), 58 us of a SIMD's issue at 4 clocks each and 2.1 GHz, beside the 71
+// us that a plain read would take.  A third step in flight was no faster there.
 // One sequence of 517 tokens takes 11 us, nearly all of it latency: lens,
 // page table, codes and the join of the waves one after the other.
 #include "common.hpp"

@@ -1,19 +1,20 @@
 // Attention over the quantized, paged KV cache with many rows per KV head: a
 // chunk or a whole prompt, or a batch in front of a shared prefix.
 //
-// Bound by the matrix cores and, next to them, by the softmax's vector work,
-// so a cached row is decoded once per workgroup and used by all its rows:
+// Bound by what a SIMD's one wave issues, products and the softmax's vector
+// work, so a cached row is decoded once per workgroup and used by all its rows:
 // codes become fp16 values s q + o in LDS (one rounding to 11 bits; s and o are
 // multiples of 2^-24 below fp16's normal range, so small rows stay exact), keys
 // row by row, values transposed.  fp16 and not bf16 for values and weights: the
 // roundings of both then stay an eighth of the output's own.
 //
-// Measured (8 KV heads of 128, 8 query heads each): 0.92 to 0.96 PFLOP/s for 1024
-// tokens in front of 33000 cached ones (a large matrix product reaches 1.2 here;
-// all SIMDs multiplying random numbers lower the clock to about two thirds), 0.89
-// for a prompt of 16000.  Shorter calls pay for starting and ending a tile, about
-// 6 us: 0.79 for chunks of 700 .. 1024 behind 4500 .. 6001, 0.63 for prompts of
-// 999 .. 2500.
+// Measured (8 KV heads of 128, 8 query heads each): 1.00 PFLOP/s for 1024 tokens
+// that see 33000 cached ones (0.93 over the call; a large matrix product reaches
+// 1.2 here).  A product then takes 75 clocks of its SIMD, of which the matrix core
+// works 32 (counted: 43 % busy), at 2.24 GHz; with all numbers zero the clocks are
+// the same, at 2.39 GHz.  A prompt of 16000 0.90 over the call.  Shorter calls
+// pay for starting and ending a tile, about 6 us: 0.80 for chunks of 700 .. 1024
+// behind 4500 .. 6001, 0.63 for prompts of 999 .. 2500.
 #include <type_traits>
 
 #include "common.hpp"
@@ -39,8 +40,7 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
 
 // The order of a turn's instructions: after each product the vector work of one
 // logit (a fused multiply-add, an exponential, a sum, half a conversion) and a
-// read from LDS; the products then run without a pause and the vector unit
-// fills their time.
+// read from LDS, so that the vector unit has work while a product runs.
 #define KV_SCHED                                          \
   _Pragma("unroll") for (int i_ = 0; i_ < 16; ++i_) {     \
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    \
@@ -51,9 +51,8 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
 // Weights are held times 2^9, with a maximum that may lag by 6: at most 2^15, so
 // inside fp16, whose subnormals then begin at 2^-23 of the largest weight and
 // lose 2^-34 of it for a key.  With plain weights and a lag of 8, thousands of
-// keys of weight 2^-25 would count as nothing; that was 1 to 2 % faster (fewer
-// bits set, a higher clock).  A lag of 2 moves the maximum often: prompts of
-// 999 .. 2500 281 us, against 263.
+// keys of weight 2^-25 would count as nothing; that was 1 to 2 % faster.  A lag
+// of 2 moves the maximum often: prompts of 999 .. 2500 281 us, against 263.
 constexpr float kLift = 9.0f, kLag = 6.0f;
 constexpr int kNoLoads = 0x0F70;           // s_waitcnt vmcnt(0), the other counters as they are
 constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 1024, -1024

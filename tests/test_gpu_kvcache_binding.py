@@ -47,3 +47,31 @@ def test_temporaries_of_another_stream(gpu):
         K, V = gpu.qcache_read(b.cache, b.d_pages, b.d_lens, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(K, kv[0]) and torch.equal(V, kv[1])
+
+
+def test_captured_on_an_explicit_stream(gpu):
+    """The capturing stream named explicitly, outputs and workspaces from the graph's own memory, replayed beside eager
+    work on the current stream."""
+    rng = np.random.default_rng(2)
+    b = Batch(rng, [3000, 60], [1, 1], 64, 2, 128, 8, starts=False, prefix=100).device(gpu)
+    Q = dev_bf16(bf16(rng.standard_normal((2, 16, 128)))[1])
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def calls(stream):
+        return [gpu.qcache_attend(b.cache, Q, b.d_pages, b.d_lens, stream=stream),
+                gpu.qcache_attend_shared(b.cache, Q, b.d_prefix, 100, b.d_pages, b.d_lens, stream=stream),
+                *gpu.qcache_read(b.cache, b.d_pages, b.d_lens, stream=stream)]
+
+    calls(None)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        outs = calls(s)
+    for i in range(3):
+        Q.normal_()
+        b.d_lens -= 7
+        want = calls(None)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want)), f"replay {i}"
