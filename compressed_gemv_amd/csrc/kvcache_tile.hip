@@ -13,7 +13,7 @@
 // 1.2 here).  A product then takes 75 clocks of its SIMD, of which the matrix core
 // works 32 (counted: 43 % busy), at 2.24 GHz; with all numbers zero the clocks are
 // the same, at 2.39 GHz.  A prompt of 16000 0.90 over the call.  Shorter calls
-// pay for starting and ending a tile, about 6 us: 0.80 for chunks of 700 .. 1024
+// pay for starting and ending a tile, 7 us or so: 0.80 for chunks of 700 .. 1024
 // behind 4500 .. 6001, 0.63 for prompts of 999 .. 2500.
 #include <type_traits>
 

@@ -101,12 +101,11 @@ int qcache_attend_ws(const qcache* c, const qseqs* s, int q_heads, int64_t prefi
  * A row that sees nothing is zero.
  * Precision: sums, maxima and the softmax statistics are fp32.  Let R be
  * ceil(T / B) * q_heads / heads, the rows of a KV head and sequence on average
- * (qcache_attend_shared: T * q_heads / heads for the prefix's keys, and for all
- * where that is at most 32 and tables hold at most 768 positions).  For R <= 32
- * keys and values enter as they are and weights with 16 bits; beyond, keys,
- * values and weights are rounded to 11 bits and queries to 2^-25 of their row's
- * largest, also where the output is fp32.  So a row's last bits depend on the
- * other rows of the call, but not on when or how often it runs.
+ * (T * q_heads / heads for the prefix's keys of qcache_attend_shared).  For
+ * R <= 32 keys and values enter as they are and weights with 16 bits; beyond,
+ * keys, values and weights are rounded to 11 bits and queries to 2^-25 of their
+ * row's largest, also where the output is fp32.  So a row's last bits depend on
+ * the other rows of the call, but not on when or how often it runs.
  * Speed: which kernels run is chosen on the host from B, T and max_pages (the
  * lengths stay on the device), so a page table no wider than the longest
  * sequence can become is the fastest, and decode steps and chunks of prompts
