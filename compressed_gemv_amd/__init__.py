@@ -1,7 +1,7 @@
 """Python binding of libqgemv (the MI355X compressed-weight product).
 
-Thin marshalling over the C ABI in include/qgemv.h and include/qcache.h: every function here has
-the name of the C entry point it calls, takes torch tensors that already
+Thin marshalling over the C ABI in include/qgemv.h, include/qcache.h and include/qlayer.h: every
+function here has the name of the C entry point it calls, takes torch tensors that already
 live on the GPU, allocates outputs with torch when none are given, passes
 raw device pointers and torch's current HIP stream, and raises QError on a
 non-zero status.  All arithmetic runs in the HIP kernels; there is no CPU
@@ -26,6 +26,7 @@ __all__ = [
     "qstream_read", "qgemm_prefill_ws", "qgemm_prefill", "Q_F32", "Q_BF16", "Q_FMT_GROUP", "Q_FMT_BINLR",
     "qcache_sizes", "make_qcache", "qcache_write", "qcache_read", "qcache_attend_ws", "qcache_attend",
     "qcache_attend_shared",
+    "make_qadapters", "qadapt_ws", "qadapt", "qnorm_rope", "qprompt_attend_ws", "qprompt_attend",
 ]
 
 Q_OK, Q_EINVAL, Q_EALIGN, Q_EUNSUPPORTED, Q_ERANGE, Q_EWORKSPACE, Q_EHIP = 0, -1, -2, -3, -4, -5, -6
@@ -76,6 +77,21 @@ class qseqs(ctypes.Structure):
     _fields_ = [
         ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("max_pages", ctypes.c_int64),
         ("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+    ]
+
+
+class qadapters(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("rank", ctypes.c_int),
+        ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+    ]
+
+
+class qrope(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("rot", ctypes.c_int),
+        ("pairs", ctypes.c_int), ("freqs", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("offset", ctypes.c_int64),
     ]
 
 
@@ -131,6 +147,14 @@ def load() -> ctypes.CDLL:
         "qcache_attend_ws": (I32, [CA, SQ, I32, I64, SZ]),
         "qcache_attend": (I32, [CA, SQ, P, I64, I32, F32, P, I64, I32, P, U64, P]),
         "qcache_attend_shared": (I32, [CA, SQ, P, I64, P, I64, I32, F32, P, I64, I32, P, U64, P]),
+    })
+    AD, RP = ctypes.POINTER(qadapters), ctypes.POINTER(qrope)
+    sig.update({
+        "qadapt_ws": (I32, [AD, I64, I64, SZ]),
+        "qadapt": (I32, [AD, I64, I64, P, P, P, I64, P, I64, P, I64, I32, P, U64, P]),
+        "qnorm_rope": (I32, [RP, I64, I64, P, P, P, I64, P, I64, I32, P, I64, P, I64, I32, P]),
+        "qprompt_attend_ws": (I32, [I32, I32, I32, I64, I64, SZ]),
+        "qprompt_attend": (I32, [I32, I32, I32, I64, I64, P, P, I64, P, I64, P, I64, F32, P, I64, I32, P, U64, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -783,17 +807,22 @@ def _fresh(cache: qcache, stream, shape, dtype, returned: bool) -> torch.Tensor:
     return t
 
 
-def _cache_call(cache: qcache, stream, what, fn, *args):
-    """fn(cache, *args, stream) on the cache's device."""
-    idx = cache._index
+def _call_on(place, stream, what, fn, *args):
+    """fn(*args, stream) on place's device (a handle's, or a _Place)."""
+    idx = place._index
     if stream is None and idx == torch._C._cuda_getDevice():
-        status = fn(cache, *args, torch._C._cuda_getCurrentRawStream(idx))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
     else:
-        stream = torch.cuda.current_stream(cache._device) if stream is None else _stream_of(cache, stream)
-        with torch.cuda.device(cache._device):
-            status = fn(cache, *args, stream.cuda_stream)
+        stream = torch.cuda.current_stream(place._device) if stream is None else _stream_of(place, stream)
+        with torch.cuda.device(place._device):
+            status = fn(*args, stream.cuda_stream)
     if status != Q_OK:
         raise QError(status, what)
+
+
+def _cache_call(cache: qcache, stream, what, fn, *args):
+    """fn(cache, *args, stream) on the cache's device."""
+    _call_on(cache, stream, what, fn, cache, *args)
 
 
 def qcache_write(cache: qcache, K: torch.Tensor, V: torch.Tensor, pages, lens, starts=None, stream=None) -> None:
@@ -935,3 +964,251 @@ def qcache_attend_shared(cache: qcache, Q: torch.Tensor, prefix_pages, prefix_le
     _need_numel(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages", (torch.int32,), exact=False)
     return _cache_attend("qcache_attend_shared", cache, Q, (prefix_pages, prefix_len), pages, lens, starts, scale, out,
                          out_dtype, ws, stream)
+
+
+# ------------------------------------- between the projections and the cache
+class _Place:
+    """The device of a call without a handle: that of its first tensor."""
+    __slots__ = ("_device", "_index")
+
+    def __init__(self, t: torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA (HIP) tensors")
+        self._device, self._index = t.device, t.get_device()
+
+
+def _here(place, **ts):
+    """Every tensor is on place's device, and contiguous."""
+    for what, t in ts.items():
+        if t is None:
+            continue
+        if t.get_device() != place._index:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA (HIP) tensors")
+            raise ValueError(f"tensors on different devices: {place._device} and {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+
+
+def _matrix(t: torch.Tensor, T, width: int, dtypes, what: str) -> int:
+    """Row stride (elements) of [T][width] (T None: any number of rows): dense
+    within a row, any stride between rows."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or (T is not None and shape[0] != T):
+        raise ValueError(f"{what}: expected [{'T' if T is None else T}][{width}], got shape {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {dtypes}")
+    row, one = t.stride()
+    if (one != 1 and width > 1) or (shape[0] > 1 and row < width):
+        raise ValueError(f"{what}: the values of one row must be contiguous, got strides {t.stride()}")
+    return row if shape[0] > 1 else width
+
+
+def _starts_of(starts, B: int, what: str = "starts"):
+    """Device pointer of starts [B+1], or None."""
+    if starts is None:
+        return None
+    _need_numel(starts, B + 1, what, (torch.int32,))
+    return starts.data_ptr()
+
+
+def make_qadapters(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor,
+                   ranks: Optional[torch.Tensor] = None) -> qadapters:
+    """A descriptor of n low-rank adapters of one projection: A bf16 [n][r][K],
+    B bf16 [n][N][r], scales fp32 [n], ranks int32 [n] where adapters are of
+    lower rank than r (what lies behind an adapter's rank is not looked at).
+    It keeps references to the tensors it points into."""
+    for t, what in ((A, "A"), (B, "B")):
+        if t.dim() != 3 or t.dtype != torch.bfloat16:
+            raise ValueError(f"{what} must be bf16 with three dimensions")
+    n, r, K = A.shape
+    N = B.shape[1]
+    if B.shape[0] != n or B.shape[2] != r:
+        raise ValueError(f"B: expected [{n}][N][{r}], got shape {tuple(B.shape)}")
+    _need_numel(scales, n, "scales", (torch.float32,))
+    if ranks is not None:
+        _need_numel(ranks, n, "ranks", (torch.int32,))
+    _need_cuda(A, B, scales, ranks)
+    _one_device(A, B, scales, ranks)
+    a = qadapters(n, K, N, r, A.data_ptr(), B.data_ptr(), scales.data_ptr(), None if ranks is None else ranks.data_ptr())
+    a._tensors = (A, B, scales, ranks)
+    a._device, a._index = A.device, A.get_device()
+    return a
+
+
+@functools.lru_cache(maxsize=1024)
+def _adapt_ws(n, K, N, rank, B, T) -> int:
+    out = ctypes.c_size_t()
+    a = qadapters(n, K, N, rank)
+    _check(load().qadapt_ws(ctypes.byref(a), B, T, ctypes.byref(out)), "qadapt_ws")
+    return out.value
+
+
+def qadapt_ws(adapters: qadapters, B: int, T: int) -> int:
+    """Workspace bytes for B requests with T rows in all."""
+    return _adapt_ws(adapters.n, adapters.K, adapters.N, adapters.rank, B, T)
+
+
+def qadapt(adapters: qadapters, x: torch.Tensor, y: torch.Tensor, ids, starts=None, out: Optional[torch.Tensor] = None,
+           ws: Optional[torch.Tensor] = None, stream=None):
+    """out[T][N] = y + scale * B_a (A_a x) with the adapter a = ids[b] of each
+    row's request (an id outside the set: y alone): x bf16 [T][K], y the shared
+    projection's output, fp32 or bf16 [T][N], ids int32 [B].  Rows starts[b] ..
+    starts[b+1]-1 are request b's, one row each without starts.  out=y adds in
+    place.  Calls that may overlap need a workspace each.  An output that is
+    allocated here belongs to `stream`: another stream waits for it first; rows
+    that no request owns are not written."""
+    xs = _matrix(x, None, adapters.K, _Q16, "x")
+    T = x.shape[0]
+    ys = _matrix(y, T, adapters.N, _OUT, "y")
+    B = ids.numel()
+    _need_numel(ids, B, "ids", (torch.int32,))
+    if starts is None and B != T:
+        raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} requests")
+    sp = _starts_of(starts, B)
+    os_ = adapters.N if out is None else _matrix(out, T, adapters.N, (y.dtype,), "out")
+    _here(adapters, ids=ids, starts=starts, ws=ws)
+    _on_device(adapters, False, x, y, out)
+    if out is None:
+        out = _fresh(adapters, stream, (T, adapters.N), y.dtype, True)
+    if T == 0:
+        return out
+    need = _adapt_ws(adapters.n, adapters.K, adapters.N, adapters.rank, B, T)
+    if ws is None:
+        ws = _fresh(adapters, stream, need, torch.uint8, False)
+    else:
+        _need_bytes(ws, need, "ws")
+    _call_on(adapters, stream, "qadapt", load().qadapt, adapters, B, T, ids.data_ptr(), sp, x.data_ptr(), xs, y.data_ptr(),
+             ys, out.data_ptr(), os_, Q_F32 if y.dtype == torch.float32 else Q_BF16, ws.data_ptr(), _nbytes(ws))
+    return out
+
+
+def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, starts=None, freqs=None, q_weight=None,
+               k_weight=None, eps: float = 1e-6, pairs: bool = False, offset: int = 0, Qo: Optional[torch.Tensor] = None,
+               Ko: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
+    """(Qo, Ko): rows Q [T][q_heads][D] and K [T][kv_heads][D] (bf16 or fp32; one
+    of them may be None) with each head's RMS norm (weights [D], bf16 or fp32;
+    None: no norm) and the rotation of the first 2 * len(freqs) values by
+    position * freqs (fp64, radians), as halves (i, i + len(freqs)) or as pairs
+    (2i, 2i + 1).  lens int32 [B] (the new tokens included) and starts as
+    qcache_write's, whose rows these are; offset is added to every position.
+    Outputs are allocated (out_dtype) unless given; an input may be its own
+    output.  Outputs that are allocated here belong to `stream`: another stream
+    waits for it first; rows that no sequence owns are not written."""
+    first = Q if Q is not None else K
+    if first is None:
+        raise ValueError("Q and K: both missing")
+    if first.dim() != 3:
+        raise ValueError(f"rows must be [T][heads][D], got shape {tuple(first.shape)}")
+    place, (T, _, D) = _Place(first), first.shape
+    heads, strides = [], []
+    for t, what in ((Q, "Q"), (K, "K")):
+        heads.append(0 if t is None else t.shape[1] if t.dim() == 3 else -1)
+        strides.append(0 if t is None else _cache_rows(t, heads[-1], D, (first.dtype,) if first.dtype in _OUT else _OUT, what))
+        if t is not None and t.shape[0] != T:
+            raise ValueError(f"{what}: {t.shape[0]} rows, Q has {T}")
+    B = lens.numel()
+    _need_numel(lens, B, "lens", (torch.int32,))
+    if starts is None and B != T:
+        raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} sequences")
+    sp = _starts_of(starts, B)
+    rot = 0
+    if freqs is not None:
+        _need_numel(freqs, freqs.numel(), "freqs", (torch.float64,))
+        rot = 2 * freqs.numel()
+    wd = torch.float32
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_numel(w, D, what, _OUT)
+            wd = w.dtype
+    if q_weight is not None and q_weight.dtype != wd:
+        raise ValueError("q_weight and k_weight: one dtype for both")
+    given = [t.dtype for t in (Qo, Ko) if t is not None]
+    dt = given[0] if given else out_dtype
+    if dt not in _OUT:
+        raise ValueError(f"out_dtype {dt}, expected one of {_OUT}")
+    _here(place, lens=lens, starts=starts, freqs=freqs, q_weight=q_weight, k_weight=k_weight)
+    _on_device(place, False, Q, K, Qo, Ko)
+    outs, ostrides = [], []
+    for t, o, h, what in ((Q, Qo, heads[0], "Qo"), (K, Ko, heads[1], "Ko")):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"{what}: given, and its input is missing")
+            ostrides.append(0)
+        elif o is None:
+            o = _fresh(place, stream, (T, h, D), dt, True)
+            ostrides.append(h * D)
+        else:
+            ostrides.append(_cache_rows(o, h, D, (dt,), what))
+            if o.shape[0] != T:
+                raise ValueError(f"{what}: {o.shape[0]} rows, its input has {T}")
+        outs.append(o)
+    if T == 0:
+        return tuple(outs)
+    p = qrope(D, heads[0], heads[1], rot, int(bool(pairs)), None if freqs is None else freqs.data_ptr(),
+              None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+              Q_F32 if wd == torch.float32 else Q_BF16, eps, offset)
+    _call_on(place, stream, "qnorm_rope", load().qnorm_rope, p, B, T, lens.data_ptr(), sp,
+             None if Q is None else Q.data_ptr(), strides[0], None if K is None else K.data_ptr(), strides[1],
+             Q_F32 if first.dtype == torch.float32 else Q_BF16, None if Q is None else outs[0].data_ptr(), ostrides[0],
+             None if K is None else outs[1].data_ptr(), ostrides[1], Q_F32 if dt == torch.float32 else Q_BF16)
+    return tuple(outs)
+
+
+@functools.lru_cache(maxsize=1024)
+def qprompt_attend_ws(head_dim: int, q_heads: int, kv_heads: int, B: int, T: int) -> int:
+    """Workspace bytes for B packed prompts of T tokens in all."""
+    n = ctypes.c_size_t()
+    _check(load().qprompt_attend_ws(head_dim, q_heads, kv_heads, B, T, ctypes.byref(n)), "qprompt_attend_ws")
+    return n.value
+
+
+def qprompt_attend(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts=None, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None,
+                   stream=None):
+    """out [T][q_heads][D] (bf16 or fp32): causal attention of packed prompts over
+    their own keys and values: Q bf16 [T][q_heads][D], K and V bf16
+    [T][kv_heads][D], sequence b's tokens are rows starts[b] .. starts[b+1]-1
+    (int32 [B+1]; one sequence of T tokens without it).  scale: D^-1/2 by
+    default.  Calls that may overlap need a workspace each.  An output that is
+    allocated here belongs to `stream`: another stream waits for it first; rows
+    that no sequence owns are not written."""
+    if K.dim() != 3 or Q.dim() != 3:
+        raise ValueError(f"Q and K must be [T][heads][D], got shapes {tuple(Q.shape)} and {tuple(K.shape)}")
+    T, kv_heads, D = K.shape
+    q_heads = Q.shape[1]
+    if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads:
+        raise ValueError(f"Q: {q_heads} heads, not a multiple of K's {kv_heads}")
+    place = _Place(Q)
+    strides = [_cache_rows(t, h, D, _Q16, what) for t, h, what in ((Q, q_heads, "Q"), (K, kv_heads, "K"), (V, kv_heads, "V"))]
+    for t, what in ((Q, "Q"), (V, "V")):
+        if t.shape[0] != T:
+            raise ValueError(f"{what}: {t.shape[0]} rows, K has {T}")
+    B = 1 if starts is None else starts.numel() - 1
+    if B < 1:
+        raise ValueError("starts: at least two entries")
+    sp = _starts_of(starts, B)
+    if out is None:
+        if out_dtype not in _OUT:
+            raise ValueError(f"out_dtype {out_dtype}, expected one of {_OUT}")
+        o_stride = q_heads * D
+    else:
+        o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
+        if out.shape[0] != T:
+            raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
+    _here(place, starts=starts, ws=ws)
+    _on_device(place, False, Q, K, V, out)
+    if out is None:
+        out = _fresh(place, stream, (T, q_heads, D), out_dtype, True)
+    if T == 0:
+        return out
+    need = qprompt_attend_ws(D, q_heads, kv_heads, B, T)
+    if ws is not None:
+        _need_bytes(ws, need, "ws")
+    elif need:
+        ws = _fresh(place, stream, need, torch.uint8, False)
+    _call_on(place, stream, "qprompt_attend", load().qprompt_attend, D, q_heads, kv_heads, B, T, sp, Q.data_ptr(), strides[0],
+             K.data_ptr(), strides[1], V.data_ptr(), strides[2], D ** -0.5 if scale is None else scale, out.data_ptr(),
+             o_stride, Q_F32 if out.dtype == torch.float32 else Q_BF16, None if ws is None else ws.data_ptr(),
+             0 if ws is None else _nbytes(ws))
+    return out

@@ -24,7 +24,7 @@ SOURCES = ["capi.hip", "pack.hip", "gemv_group.hip", "gemv_binlr.hip", "gemm_pre
            "gemv_codebook.hip", "gemm_prefill_codebook.hip",
            "turboquant.hip", "stream_read.hip",
            "kvcache_api.hip", "kvcache.hip", "kvcache_attend.hip",
-           "kvcache_tile.hip"]
+           "kvcache_tile.hip", "layer_api.hip", "norm_rope.hip", "adapt.hip", "prompt_attend.hip"]
 
 CXXFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -1,0 +1,433 @@
+// Low-rank adapters of many requests beside a shared projection:
+//   out[t] = y[t] + scale[a] * B_a (A_a x[t]).
+//
+// Two launches: `down` forms h = A_a x in fp32, split over K into partial sums;
+// `up` adds them, in the order of the splits, and forms y + scale * B_a h.  Few
+// rows are bound by reading A and B of each adapter once, many by reading x and y
+// and writing out; the products are small beside either, so both run on
+// v_mfma_f32_16x16x32_bf16 with operands straight from memory.  h goes in as bf16
+// hi + lo (bf16 alone would lose 2^-9 of it), which doubles a product of depth
+// `rank` only.
+//
+// Rows meet an adapter in tiles of up to 64.  With starts, tile k of request b is
+// number starts[b] / 64 + b + k of T / 64 + B: numbers that need no sum over the
+// requests, and of which at most B stay empty.  With a row for each request, a
+// block of 64 rows is divided by the adapters it names: workgroup `slot` takes
+// the slot-th of them (and every slots-th behind it), so an adapter that several
+// rows name is read once for all of them.
+#include "common.hpp"
+#include "layer.hpp"
+
+namespace qg {
+
+namespace {
+
+// y and out rows begin wherever N and the caller's strides put them; the
+// hardware takes wide accesses at any element.
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+
+constexpr int kTile = 64;                  // rows of a tile
+constexpr uint32_t kOut = 0x7FFFFFF0u;     // an offset behind every buffer: the load gives 0
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of a call and how its axes are cut, from sizes alone.
+struct AdaptPlan {
+  int64_t blocks;                          // tiles, or blocks of 64 rows
+  int slots;
+  int splits, kchunk;                      // of K, a multiple of 128
+  int nchunk;                              // of N, a multiple of 256
+  int R;                                   // rank padded to 16
+};
+
+AdaptPlan plan_adapt(bool segments, int64_t seqs, int64_t T, int64_t K, int64_t N, int rank) {
+  AdaptPlan p{};
+  p.R = (rank + 15) / 16 * 16;
+  int64_t tiles;
+  if (segments) {
+    p.blocks = T / kTile + seqs;
+    p.slots = 1;
+    tiles = T / kTile + (seqs < 16 ? seqs : 16);
+  } else {
+    p.blocks = ceil_div(T, kTile);
+    p.slots = T <= 1024 ? (int)(T < kTile ? T : kTile) : 4;
+    tiles = p.blocks * (p.slots < 16 ? p.slots : 16);
+  }
+  int64_t s = ceil_div(512, tiles);
+  const int64_t most = ceil_div(K, 256);
+  s = s > most ? most : s;
+  s = s > 32 ? 32 : s;
+  p.kchunk = (int)(ceil_div(ceil_div(K, s), 128) * 128);
+  p.splits = (int)ceil_div(K, p.kchunk);
+  int64_t c = ceil_div(N * tiles, 1024);
+  c = ceil_div(c, 256) * 256;
+  p.nchunk = (int)(c < 256 ? 256 : (c > 1024 ? 1024 : c));
+  return p;
+}
+
+// The rows a workgroup works on.
+struct Tile {
+  int a;                                   // adapter; -1: none
+  int row0;                                // of the tile or block
+  int n;                                   // rows; 0: nothing to do
+};
+
+// Tile number j of a call with starts: wave-uniform.
+__device__ __forceinline__ Tile segment_tile(const Adapt& p, int64_t j, int lane) {
+  int lo = 0, n = p.seqs;                  // largest b with starts[b] / 64 + b <= j
+  while (n > 1) {
+    const int step = (n + 63) / 64, i = lo + lane * step;
+    bool le = false;
+    if (lane * step < n) {
+      const int s = p.starts[i];
+      le = (int64_t)((s < 0 ? 0 : s) / kTile) + i <= j;
+    }
+    const int cnt = __popcll(__ballot(le)), k = cnt > 0 ? cnt - 1 : 0;
+    lo += k * step;
+    n = n - k * step < step ? n - k * step : step;
+    if (n < 1) n = 1;
+  }
+  int s0 = p.starts[lo], s1 = p.starts[lo + 1];
+  s0 = s0 < 0 ? 0 : s0;
+  s1 = s1 > p.T ? p.T : s1;
+  const int64_t k = j - ((int64_t)(s0 / kTile) + lo);
+  const int64_t row0 = s0 + k * kTile;
+  Tile t{-1, 0, 0};
+  if (k < 0 || row0 >= s1) return t;
+  t.row0 = (int)row0;
+  t.n = s1 - t.row0 < kTile ? s1 - t.row0 : kTile;
+  t.a = p.ids[lo];
+  return t;
+}
+
+// Walks a workgroup's tiles; rows[] (LDS) gets each tile's rows, relative to row0.
+struct Tiles {
+  uint64_t left = 0;                       // rows of the block not looked at
+  int id = 0, index = 0;                   // a lane's row's adapter; adapters passed
+  bool segment, done = false;
+  __device__ __forceinline__ int own_id(const Adapt& p, int a) const {
+    if (a < 0 || a >= p.n) return -1;
+    return p.ranks && p.ranks[a] <= 0 ? -1 : a;
+  }
+  __device__ __forceinline__ Tiles(const Adapt& p, int64_t block, int lane) {
+    segment = p.starts != nullptr;
+    if (segment) return;
+    const int64_t row = block * kTile + lane;
+    const bool on = row < p.T;
+    id = on ? own_id(p, p.ids[row]) : -1;
+    left = __ballot(on);
+  }
+  // All waves of the workgroup call it together; behind it rows[] may be read.
+  __device__ __forceinline__ bool next(const Adapt& p, int64_t block, int slot, int slots, int lane, uint8_t* rows, Tile& t) {
+    __syncthreads();                       // the tile before is done with rows[]
+    if (segment) {
+      if (done) return false;
+      done = true;
+      t = segment_tile(p, block, lane);
+      t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+      t.n = __builtin_amdgcn_readfirstlane(t.n);
+      if (t.n == 0) return false;
+      t.a = own_id(p, __builtin_amdgcn_readfirstlane(t.a));
+      if (threadIdx.x < kTile) rows[threadIdx.x] = (uint8_t)threadIdx.x;
+      __syncthreads();
+      return true;
+    }
+    while (left) {
+      const int a = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+      const uint64_t m = __ballot(id == a) & left;
+      left &= ~m;
+      if (index++ % slots != slot) continue;
+      t.a = a;
+      t.row0 = (int)(block * kTile);
+      t.n = __popcll(m);
+      if (threadIdx.x < kTile && ((m >> lane) & 1u)) rows[__popcll(m & ((1ull << lane) - 1ull))] = (uint8_t)lane;
+      __syncthreads();
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int rank_of(const Adapt& p, int a) {
+  if (!p.ranks) return p.rank;
+  const int k = p.ranks[a];
+  return k < p.rank ? k : p.rank;
+}
+
+__device__ __forceinline__ bf16x8_t frag(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  return u32x4_t{v[0], v[1], v[2], v[3]};
+}
+
+// ------------------------------------------------------------------- down
+// One workgroup: a tile, a range of K and up to 64 ranks (QT tiles of 16).  With
+// more than 16 rows each wave takes 16 of them; otherwise the waves share the
+// range of K and add up in LDS.  A lane's operands are 16 bytes: a rank's (a
+// row's) 8 inputs from 8 (lane / 16) on.
+template <int QT>
+__global__ __launch_bounds__(256) void adapt_down_kernel(Adapt p, int slots, int kchunk, int R) {
+  __shared__ uint8_t rows[kTile];
+  __shared__ __align__(16) float red[3][64][QT][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block = blockIdx.x / slots;
+  const int slot = blockIdx.x % slots, rank0 = blockIdx.z * 64;
+  const int k0 = blockIdx.y * kchunk, k1 = p.K - k0 < kchunk ? p.K : k0 + kchunk;
+  const int r16 = lane & 15, g = lane >> 4;
+  Tiles tiles(p, block, lane);
+  Tile t;
+  while (tiles.next(p, block, slot, slots, lane, rows, t)) {
+    if (t.a < 0) continue;
+    const int ranks = rank_of(p, t.a) - rank0;
+    if (ranks <= 0) continue;
+    const int held = ranks < 16 * QT ? ranks : 16 * QT;      // ranks of this workgroup
+    const bool wide = t.n > 16;                              // workgroup-uniform
+    const int at = wide ? wave * 16 + r16 : r16;             // the lane's place in the tile
+    const int row = at < t.n ? rows[at] : -1;
+    const int64_t xs = p.x_stride;
+    const auto xb = make_rsrc(p.x + (int64_t)t.row0 * xs, (uint32_t)(((p.T - t.row0 < kTile ? p.T - t.row0 : kTile) - 1) * xs + p.K) * 2u);
+    const auto ab = make_rsrc(p.A + ((int64_t)t.a * p.rank + rank0) * p.K, (uint32_t)held * (uint32_t)p.K * 2u);
+    const uint32_t xrow = row < 0 ? kOut : (uint32_t)(row * xs + 8 * g) * 2u;
+    uint32_t arow[QT];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) arow[q] = (uint32_t)((16 * q + r16) * p.K + 8 * g) * 2u;
+    f32x4_t acc[QT];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int step = wide ? 32 : 128;
+    constexpr int U = 4;
+    for (int k = k0 + (wide ? 0 : 32 * wave); k < k1; k += U * step) {
+      u32x4_t xv[U], av[U][QT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = k + u * step;
+        const bool in = kk + 8 * g < k1;                     // k1 is K, a multiple of 8, or of 32
+        xv[u] = load16(xb, in && row >= 0 ? xrow + 2u * kk : kOut);
+#pragma unroll
+        for (int q = 0; q < QT; ++q) av[u][q] = load16(ab, in ? arow[q] + 2u * kk : kOut);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(av[u][q]), frag(xv[u]), acc[q], 0, 0, 0);
+    }
+    if (!wide) {
+      if (wave > 0) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q) *reinterpret_cast<f32x4_t*>(red[wave - 1][lane][q]) = acc[q];
+      }
+      __syncthreads();
+      if (wave > 0) continue;
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int q = 0; q < QT; ++q) acc[q] += *reinterpret_cast<const f32x4_t*>(red[w][lane][q]);
+    }
+    // lane: ranks 16 q + 4 g .. + 3 of its row
+    if (row >= 0) {
+      float* to = p.part + ((int64_t)blockIdx.y * p.T + t.row0 + row) * R + rank0 + 4 * g;
+#pragma unroll
+      for (int q = 0; q < QT; ++q)
+        if (16 * q < held) *reinterpret_cast<f32x4_t*>(to + 16 * q) = acc[q];
+    }
+  }
+}
+
+// --------------------------------------------------------------------- up
+// One workgroup: a tile and a range of N.  h (all splits added, times scale)
+// lies in LDS as bf16, hi and lo: 32-deep blocks of hi, then those of lo, or for
+// ranks up to 16 both in one block, so that one product does.  A wave forms 64
+// outputs of 16 RT rows at a time: the four 16 x 16 products of a row tile give a
+// lane four neighbouring outputs of a row each (fp32: 16-byte accesses), or,
+// with the outputs of two products interleaved, eight (bf16).
+struct UpRows {
+  const uint8_t* rows;
+  const uint16_t* h;
+  int pitch, lo_at, blocks;                // of h: values per row, where lo begins, 32-deep blocks
+  int n, held;
+};
+
+template <bool F32, int RT>
+__device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpRows& u, int row_tile, int n0, int n1, int lane) {
+  const int r16 = lane & 15, g = lane >> 4;
+  const bool both = u.lo_at == 16;         // hi and lo in one block
+  const auto bb = make_rsrc(p.B + ((int64_t)t.a * p.N + n0) * p.rank, (uint32_t)(n1 - n0) * (uint32_t)p.rank * 2u);
+  // outputs of the wave, relative to n0: product c's row m is output perm(c, m)
+  auto perm = [](int c, int m) { return F32 ? 16 * c + m : 32 * (c / 2) + 8 * (m / 4) + 4 * (c % 2) + m % 4; };
+  f32x4_t acc[RT][4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int J = 0; J < u.blocks; ++J) {
+    const int j = both ? 8 * (g & 1) : 32 * J + 8 * g;       // ranks j .. j + 7 of the lane's operand
+    int c8 = u.held - j;
+    c8 = c8 < 0 ? 0 : (c8 > 8 ? 8 : c8);
+    u32x4_t bv[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) bv[c] = load16(bb, c8 > 0 ? (uint32_t)(perm(c, r16) * p.rank + j) * 2u : kOut);
+    if (c8 < 8) {                          // what lies behind the adapter's own rank may be anything
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t m = c8 >= 2 * w + 2 ? 0xFFFFFFFFu : (c8 == 2 * w + 1 ? 0xFFFFu : 0u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) bv[c][w] &= m;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const uint16_t* hr = u.h + (16 * (row_tile + i) + r16) * u.pitch + 32 * J + 8 * g;
+      const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(hr);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(hi), acc[i][c], 0, 0, 0);
+      if (!both) {
+        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(hr + u.lo_at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(lo), acc[i][c], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int at = 16 * (row_tile + i) + r16;
+    if (at >= u.n) continue;
+    const int64_t row = t.row0 + u.rows[at];
+    const int64_t yo = row * p.y_stride + n0, oo = row * p.o_stride + n0;
+    if constexpr (F32) {
+      const float* y = static_cast<const float*>(p.y) + yo;
+      float* o = static_cast<float*>(p.out) + oo;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int n = 16 * c + 4 * g;
+        if (n0 + n + 4 <= n1) {
+          *reinterpret_cast<f32x4_any*>(o + n) = *reinterpret_cast<const f32x4_any*>(y + n) + acc[i][c];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (n0 + n + k < n1) o[n + k] = y[n + k] + acc[i][c][k];
+        }
+      }
+    } else {
+      const uint16_t* y = static_cast<const uint16_t*>(p.y) + yo;
+      uint16_t* o = static_cast<uint16_t*>(p.out) + oo;
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        const int n = 16 * c + 8 * g;
+        if (n0 + n + 8 <= n1) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_any*>(y + n);
+          u32x4_t w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = cvt_pk_bf16(bf16_lo_to_f32(v[k]) + acc[i][c + k / 2][2 * (k % 2)],
+                               bf16_hi_to_f32(v[k]) + acc[i][c + k / 2][2 * (k % 2) + 1]);
+          *reinterpret_cast<u32x4_any*>(o + n) = w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (n0 + n + k < n1) o[n + k] = (uint16_t)cvt_pk_bf16(bf16_bits_to_f32(y[n + k]) + acc[i][c + k / 4][k % 4], 0.f);
+        }
+      }
+    }
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int splits, int nchunk, int R) {
+  __shared__ uint8_t rows[kTile];
+  extern __shared__ __align__(16) uint16_t hbuf[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block = blockIdx.x / slots;
+  const int slot = blockIdx.x % slots;
+  const int64_t first64 = (int64_t)blockIdx.y * nchunk;
+  const int first = (int)first64, last = p.N - first64 < nchunk ? p.N : first + nchunk;
+  const bool copies = p.out != p.y;
+  Tiles tiles(p, block, lane);
+  Tile t;
+  while (tiles.next(p, block, slot, slots, lane, rows, t)) {
+    if (t.a < 0) {                         // no adapter: y as it is
+      if (!copies) continue;
+      const int es = F32 ? 4 : 2;
+      for (int i = wave; i < t.n; i += 4) {
+        const int64_t row = t.row0 + rows[i];
+        const char* y = static_cast<const char*>(p.y) + (row * p.y_stride + first) * es;
+        char* o = static_cast<char*>(p.out) + (row * p.o_stride + first) * es;
+        const int bytes = (last - first) * es;
+        for (int b = lane * 16; b < bytes; b += 1024) {
+          if (b + 16 <= bytes) *reinterpret_cast<u32x4_any*>(o + b) = *reinterpret_cast<const u32x4_any*>(y + b);
+          else
+            for (int k = b; k < bytes; k += 2) *reinterpret_cast<uint16_t*>(o + k) = *reinterpret_cast<const uint16_t*>(y + k);
+        }
+      }
+      continue;
+    }
+    UpRows u;
+    u.rows = rows;
+    u.h = hbuf;
+    u.n = t.n;
+    u.held = rank_of(p, t.a);
+    const bool both = u.held <= 16;
+    const int deep = both ? 16 : (u.held + 31) / 32 * 32;
+    u.lo_at = deep;
+    u.blocks = both ? 1 : deep / 32;
+    u.pitch = 2 * deep + 8;                // 16 bytes more: neighbouring rows in other banks
+    const int tall = (t.n + 15) / 16 * 16, kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
+    const float scale = p.scales[t.a];
+    for (int i = threadIdx.x; i < tall * (deep / 4); i += 256) {
+      const int at = i / (deep / 4), j = 4 * (i % (deep / 4));
+      f32x4_t h = {0.f, 0.f, 0.f, 0.f};
+      if (at < t.n && j < kept) {
+        const float* from = p.part + ((int64_t)t.row0 + rows[at]) * R + j;
+        for (int s = 0; s < splits; ++s) h += *reinterpret_cast<const f32x4_t*>(from + (int64_t)s * p.T * R);
+        h *= scale;
+      }
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        hi[k] = cvt_pk_bf16(h[2 * k], h[2 * k + 1]);
+        lo[k] = cvt_pk_bf16(h[2 * k] - bf16_lo_to_f32(hi[k]), h[2 * k + 1] - bf16_hi_to_f32(hi[k]));
+      }
+      *reinterpret_cast<uint2*>(hbuf + at * u.pitch + j) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(hbuf + at * u.pitch + deep + j) = make_uint2(lo[0], lo[1]);
+    }
+    __syncthreads();
+    const int tiles16 = tall / 16;
+    for (int n0 = first + 64 * wave; n0 < last; n0 += 256) {
+      const int n1 = last - n0 < 64 ? last : n0 + 64;
+      if (tiles16 == 1) up_tile<F32, 1>(p, t, u, 0, n0, n1, lane);
+      else
+        for (int i = 0; i < tiles16; i += 2) {
+          if (i + 1 < tiles16) up_tile<F32, 2>(p, t, u, i, n0, n1, lane);
+          else up_tile<F32, 1>(p, t, u, i, n0, n1, lane);
+        }
+    }
+  }
+}
+
+}  // namespace
+
+size_t adapt_ws_bytes(int64_t seqs, int64_t T, int64_t K, int rank) {
+  // with and without starts: the larger of both
+  const AdaptPlan a = plan_adapt(true, seqs, T, K, 1, rank), b = plan_adapt(false, seqs, T, K, 1, rank);
+  return (size_t)(a.splits > b.splits ? a.splits : b.splits) * T * a.R * 4;
+}
+
+hipError_t launch_adapt(const Adapt& p, hipStream_t st) {
+  const AdaptPlan a = plan_adapt(p.starts != nullptr, p.seqs, p.T, p.K, p.N, p.rank);
+  const dim3 down((unsigned)(a.blocks * a.slots), (unsigned)a.splits, (unsigned)((p.rank + 63) / 64));
+  if (p.rank <= 16) hipLaunchKernelGGL((adapt_down_kernel<1>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
+  else if (p.rank <= 32) hipLaunchKernelGGL((adapt_down_kernel<2>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
+  else hipLaunchKernelGGL((adapt_down_kernel<4>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int deep = p.rank <= 16 ? 16 : (p.rank + 31) / 32 * 32;
+  const int64_t tall = p.T < kTile ? ceil_div(p.T, 16) * 16 : kTile;
+  const size_t lds = (size_t)tall * (2 * deep + 8) * 2;
+  const dim3 up((unsigned)(a.blocks * a.slots), (unsigned)ceil_div(p.N, a.nchunk));
+  if (p.f32) hipLaunchKernelGGL((adapt_up_kernel<true>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
+  else hipLaunchKernelGGL((adapt_up_kernel<false>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
+  return hipGetLastError();
+}
+
+}  // namespace qg
