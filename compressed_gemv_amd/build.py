@@ -34,11 +34,11 @@ CXXFLAGS = [
 ]
 
 
-# Flags of one file.  The cache's attention kernels use the results of most of
+# Flags of one file.  The attention kernels use the results of most of
 # their products in vector code at once: with products that write to ordinary
 # registers those results need no move out of the accumulation registers.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-FILE_FLAGS = {"kvcache_tile.hip": VGPR_FORM, "kvcache_attend.hip": VGPR_FORM}
+FILE_FLAGS = {"kvcache_tile.hip": VGPR_FORM, "kvcache_attend.hip": VGPR_FORM, "prompt_attend.hip": VGPR_FORM}
 
 
 def hipcc() -> str:

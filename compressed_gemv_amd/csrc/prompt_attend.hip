@@ -2,148 +2,464 @@
 // with grouped heads.
 //
 // A KV head's rows of one sequence are its tokens times `group` query heads,
-// row = token * group + g; a workgroup of four waves takes a tile of 128 of them
-// and walks the keys that its last token sees, 32 at a time.  S^T = K Q^T on
-// 32x32x16 products puts a row's logits of 16 keys into one lane, and the
-// weights go back in as the other operand of O^T = V^T P^T without leaving it.
-// Tile k of sequence b is number starts[b] * group / 128 + b + k: numbers that
-// need no sum over the sequences.
-#include "kvcache.hpp"
+// row = token * group + g; a workgroup takes a tile of 64 NW of them and walks
+// the keys that its last token sees, 32 NW at a time.
+#include <type_traits>
+
+#include "kvcache_plan.hpp"
 #include "layer.hpp"
 
 namespace qg {
 
 namespace {
 
-constexpr int kRows = 128, kKeys = 32;
-
+// Keys and values lie in LDS as they come from memory, 1 KB a wave and
+// instruction (4 keys of 128 values, 8 of 64), the 16-byte pieces of four keys
+// side by side: piece c of keys 4q .. 4q + 3 is one run of 64 bytes.  The runs of
+// a KB follow each other, with 64 (128) bytes between KBs, so that what a product
+// reads of 16 neighbouring keys lies in all banks once, and what a transposing
+// read takes of 4 keys and 32 coordinates (64 bytes of each) is 256 bytes in a
+// row; every address of the inner loop is one register plus a constant.
+// (64: the second four keys of a KB swap neighbouring pieces, for the same.)
 template <int D>
-__global__ __launch_bounds__(256) void prompt_kernel(Prompt p) {
-  constexpr int STEPS = D / 16, DT = D / 32;
-  constexpr int KP = D + 8, VP = kKeys + 8;                 // pitch of a key's and of a coordinate's row
-  __shared__ __align__(16) uint16_t ks[kKeys * KP], vs[D * VP];
-  __shared__ uint32_t bad;                                  // keys whose values are not finite
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, hh = lane >> 5;
-  const int h = blockIdx.x % p.heads;
-  const int64_t j = blockIdx.x / p.heads;
-  // the tile's sequence
-  int b = 0;
-  int64_t s0 = 0, s1 = p.T;
+struct Image {
+  static constexpr int KPB = 512 / D;                       // keys in a KB
+  static constexpr int PITCH = D == 128 ? 1024 + 64 : 1024 + 128;
+  static constexpr int bytes(int keys) { return keys / KPB * PITCH; }
+  // of key (a multiple of 16 added later is a constant) and piece
+  static __device__ __forceinline__ int at(int key, int c) {
+    if constexpr (D == 128) return key / 4 * PITCH + c * 64 + (key & 3) * 16;
+    const int q = (key >> 2) & 1;
+    return key / 8 * PITCH + q * 512 + (c ^ q) * 64 + (key & 3) * 16;
+  }
+  // the key and piece that lane of a KB holds
+  static __device__ __forceinline__ int key_of(int lane) { return D == 128 ? lane & 3 : 4 * (lane >> 5) + (lane & 3); }
+  static __device__ __forceinline__ int piece_of(int lane) { return D == 128 ? lane >> 2 : ((lane >> 2) & 7) ^ (lane >> 5); }
+};
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLag = 8.0f;               // the running maximum may lag so far: weights up to 2^8
+constexpr int kNoLoads = 0x0F70;           // s_waitcnt vmcnt(0), the other counters as they are
+
+__device__ __forceinline__ int wave_sum_i32(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+struct PromptTile {
+  int s0, rows;                            // first token and rows of the sequence; rows = 0: no tile
+  int row0;
+};
+
+__device__ __forceinline__ void bounds_of(const Prompt& p, int b, int& s0, int& s1) {
+  s0 = 0;
+  s1 = p.T;
   if (p.starts) {
-    int n = p.B;
+    const int a = p.starts[b], e = p.starts[b + 1];
+    s0 = a < 0 ? 0 : a;
+    s1 = e > p.T ? p.T : e;
+    if (s1 < s0) s1 = s0;
+  }
+}
+
+// Tile number j of the call, the costly ones first: those of up to 256 sequences
+// by the keys they see, of more sequences each one's own in that order.
+// Wave-uniform.
+template <int RT>
+__device__ __forceinline__ PromptTile tile_of(const Prompt& p, int64_t j, int lane) {
+  PromptTile t{0, 0, 0};
+  int s0, s1, k;
+  if (p.B <= 256) {
+    int tiles[4], most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 64 * i + lane;
+      tiles[i] = 0;
+      if (64 * i < p.B && b < p.B) {
+        bounds_of(p, b, s0, s1);
+        tiles[i] = (int)(((int64_t)(s1 - s0) * p.group + RT - 1) / RT);
+      }
+      most = tiles[i] > most ? tiles[i] : most;
+    }
+    // tiles of index k and more
+    auto above = [&](int k) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += tiles[i] > k ? tiles[i] - k : 0;
+      return wave_sum_i32(n);
+    };
+    if (j >= above(0)) return t;
+    int b = 0;
+    if (p.B == 1) {
+      k = __builtin_amdgcn_readlane(tiles[0], 0) - 1 - (int)j;
+    } else {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_xor(most, d);
+        most = o > most ? o : most;
+      }
+      k = 0;                               // the largest k with above(k) > j
+      for (int n = __builtin_amdgcn_readfirstlane(most); n > 1;) {
+        const int half = n >> 1;
+        if (above(k + half) > j) { k += half; n -= half; }
+        else n = half;
+      }
+      int r = (int)j - above(k + 1);       // the r-th sequence with more than k tiles
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t m = __ballot(tiles[i] > k);
+        const int n = __popcll(m);
+        if (r >= 0 && r < n) {
+          const uint64_t hit = __ballot(((m >> lane) & 1u) && __popcll(m & ((1ull << lane) - 1ull)) == r);
+          b = 64 * i + __ffsll((unsigned long long)hit) - 1;
+        }
+        r -= n;
+      }
+    }
+    bounds_of(p, b, s0, s1);
+  } else {
+    int b = 0, n = p.B;                    // the last b with starts[b] * group / RT + b <= j
     while (n > 1) {
       const int half = n >> 1;
       int64_t s = p.starts[b + half];
       s = s < 0 ? 0 : s;
-      if (s * p.group / kRows + b + half <= j) { b += half; n -= half; }
+      if (s * p.group / RT + b + half <= j) { b += half; n -= half; }
       else n = half;
     }
-    s0 = p.starts[b];
-    s1 = p.starts[b + 1];
-    s0 = s0 < 0 ? 0 : s0;
-    s1 = s1 > p.T ? p.T : s1;
+    bounds_of(p, b, s0, s1);
+    const int64_t i = j - ((int64_t)s0 * p.group / RT + b), tiles = ((int64_t)(s1 - s0) * p.group + RT - 1) / RT;
+    if (i < 0 || i >= tiles) return t;
+    k = (int)(tiles - 1 - i);
   }
-  const int64_t k = j - (s0 * p.group / kRows + b);
-  const int64_t rows = (s1 - s0) * p.group, row0 = k * kRows;
-  if (k < 0 || row0 >= rows) return;
-  const int64_t last = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-  const int keys = (int)(last / p.group) + 1;
-  const int64_t row = row0 + wave * 32 + col < rows ? row0 + wave * 32 + col : rows - 1;
-  const int tok = (int)(row / p.group), g = (int)(row % p.group);
-  bf16x8_t q[STEPS];
-  const uint16_t* qp = p.Q + (s0 + tok) * p.q_stride + (int64_t)(h * p.group + g) * D + 8 * hh;
+  t.s0 = __builtin_amdgcn_readfirstlane(s0);
+  t.rows = __builtin_amdgcn_readfirstlane((s1 - s0) * p.group);
+  t.row0 = __builtin_amdgcn_readfirstlane(k * RT);
+  return t;
+}
+
+// The order of a turn's instructions: after each product the vector work of one
+// logit and a read or two from LDS, so that the vector unit has work while a
+// product runs.
+template <int READS>
+__device__ __forceinline__ void sched_turn(int products) {
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    u32x4_t v = *reinterpret_cast<const u32x4_t*>(qp + 16 * s);
-    if (p.scale < 0.f) {
+  for (int i = 0; i < products; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+  }
+}
+
+// A workgroup: NW waves of 64 rows (two blocks of 32), one wave per SIMD with
+// all its registers; 32 NW keys a step, two LDS buffers.  S^T = K Q^T on
+// 32x32x16 products puts a row's logits of 16 keys into one lane; the weights go
+// back in as the other operand of O^T = V^T P^T without leaving the lane.  The
+// two blocks take turns, the products of one running while the vector unit does
+// the softmax of the other:
+//   turn 1 of 32 keys:  products  O_A += V P_A (the keys before), S_A (these)
+//                       vector    softmax of S_B (the keys before)
+//   turn 2:             products  O_B += V P_B (the keys before), S_B (these)
+//                       vector    softmax of S_A (these)
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t tiles) {
+  constexpr int KT = 32 * NW, KBS = NW, RT = 64 * NW;
+  constexpr int STEPS = D / 16, DT = D / 32;
+  using Im = Image<D>;
+  constexpr int BUF = Im::bytes(KT), KB32 = Im::bytes(32), KB16 = KB32 / 2, KB8 = KB32 / 4;
+  constexpr int LOADS = KT * D * 2 / 1024;                  // KBs of a step's keys
+  __shared__ __align__(16) uint8_t ksh[2 * BUF];
+  __shared__ __align__(16) uint8_t vsh[2 * BUF];
+  __shared__ uint32_t bad[2][KBS];                          // of masked steps: keys whose values are not finite
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int h = blockIdx.x % p.heads;
+  for (int64_t j = blockIdx.x / p.heads; j < tiles; j += gridDim.x / p.heads) {
+  const PromptTile w = tile_of<RT>(p, j, lane);
+  if (w.rows == 0) continue;
+  const int last_row = w.row0 + RT < w.rows ? w.row0 + RT - 1 : w.rows - 1;
+  const int k1 = last_row / p.group + 1;                    // keys the tile needs
+  const int sure = w.row0 / p.group + 1;                    // keys that all its rows see
+
+  const uint16_t* const kp = p.K + (int64_t)w.s0 * p.k_stride + (int64_t)h * D + Im::piece_of(lane) * 8;
+  const uint16_t* const vp = p.V + (int64_t)w.s0 * p.v_stride + (int64_t)h * D + Im::piece_of(lane) * 8;
+  auto fetch = [&](int key0, int buf) {
+    auto put = [&](const void* from, uint8_t* to) {
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    };
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] ^= 0x80008000u;
+    for (int i = 0; i < LOADS / NW; ++i) {
+      const int kb = wave + i * NW;
+      int key = key0 + kb * Im::KPB + Im::key_of(lane);
+      key = key < k1 ? key : k1 - 1;                        // behind the last key it is repeated, and masked
+      put(kp + (int64_t)key * p.k_stride, ksh + buf * BUF + kb * Im::PITCH);
+      put(vp + (int64_t)key * p.v_stride, vsh + buf * BUF + kb * Im::PITCH);
     }
-    q[s] = __builtin_bit_cast(bf16x8_t, v);
-  }
-  const float c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);   // positive also for a scale of 0
-  f32x16_t acc[DT];
+  };
+  // Values of keys that some row must not see: a weight of zero does not undo an
+  // infinity or a NaN, so they become zeros, and their key's logit NaN for the
+  // rows that do see it.
+  auto clean = [&](int buf) {
+    if (tid < KBS) bad[buf ^ 1][tid] = 0;
+    for (int i = tid; i < KT * D / 8; i += 64 * NW) {
+      u32x4_t* at = reinterpret_cast<u32x4_t*>(vsh + buf * BUF + i / 64 * Im::PITCH + i % 64 * 16);
+      u32x4_t v = *at;
+      bool off = false;
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int key0 = 0; key0 < keys; key0 += kKeys) {
-    __syncthreads();
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * D / 8; i += 256) {
-      const int kk = i / (D / 8), d = 8 * (i % (D / 8));
-      const int key = key0 + kk < keys ? key0 + kk : keys - 1;
-      const u32x4_t kv = *reinterpret_cast<const u32x4_t*>(p.K + (s0 + key) * p.k_stride + (int64_t)h * D + d);
-      const u32x4_t vv = *reinterpret_cast<const u32x4_t*>(p.V + (s0 + key) * p.v_stride + (int64_t)h * D + d);
-      *reinterpret_cast<u32x4_t*>(ks + kk * KP + d) = kv;
-      // place of key kk among a product's operands: the order in which lanes hold the weights
-      const int at = (kk & ~15) | ((kk & 4) << 1) | ((kk & 8) >> 1) | (kk & 3);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t v = (vv[e / 2] >> (16 * (e % 2))) & 0xFFFFu;
-        if ((v & 0x7F80u) == 0x7F80u) {
-          v = 0;
-          atomicOr(&bad, 1u << kk);
-        }
-        vs[(d + e) * VP + at] = (uint16_t)v;
+      for (int e = 0; e < 4; ++e) {
+        if ((v[e] & 0x7F80u) == 0x7F80u) { v[e] &= 0xFFFF0000u; off = true; }
+        if ((v[e] & 0x7F800000u) == 0x7F800000u) { v[e] &= 0xFFFFu; off = true; }
+      }
+      if (off) {
+        *at = v;
+        const int key = i / 64 * Im::KPB + Im::key_of(i % 64);
+        atomicOr(&bad[buf][key / 32], 1u << (key % 32));
       }
     }
-    __syncthreads();
-    f32x16_t z;
+  };
+  if (tid < 2 * KBS) bad[tid / KBS][tid % KBS] = 0;
+  fetch(0, 0);
+
+  bf16x8_t qf[2][STEPS];
+  int lim[2], limmin = k1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  for (int n = 0; n < 2; ++n) {
+    int row = w.row0 + wave * 64 + n * 32 + col;
+    row = row < w.rows ? row : w.rows - 1;                  // behind the last row it is repeated, and not stored
+    const int tok = row / p.group, g = row - tok * p.group;
+    const uint16_t* q = p.Q + (int64_t)(w.s0 + tok) * p.q_stride + (int64_t)(h * p.group + g) * D + 8 * hh;
+    lim[n] = tok + 1;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-      z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8_t*>(ks + col * KP + 16 * s + 8 * hh), q[s], z, 0, 0, 0);
-    const uint32_t nan = bad;
-    float mx = m;
+    for (int s = 0; s < STEPS; ++s) qf[n][s] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(q + 16 * s));
+  }
+  {
+    int row = w.row0 + wave * 64;                           // the wave's first row sees least
+    row = row < w.rows ? row : w.rows - 1;
+    limmin = row / p.group + 1;
+  }
+  if (p.scale < 0.f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int kk = 8 * (i / 4) + 4 * hh + i % 4;
-      z[i] = key0 + kk <= tok ? ((nan >> kk) & 1u ? NAN : z[i] * c) : -INFINITY;
-      mx = fmaxf(mx, z[i]);
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float base = mx == -INFINITY ? 0.f : mx, f = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - base);
-    m = mx;
-    l *= f;
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        u32x4_t v = __builtin_bit_cast(u32x4_t, qf[n][s]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] ^= 0x80008000u;
+        qf[n][s] = __builtin_bit_cast(bf16x8_t, v);
+      }
+  }
+  const float cq = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);   // positive also for a scale of 0: -inf stays -inf
+  // The queries never change and only products read them: accumulation
+  // registers hold them, the vector unit's stay free.
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) asm volatile("" : "+a"(qf[n][s]));
+
+  f32x16_t acc[2][DT], z[2];
+  float m[2], l[2], mx[2];
+  u32x4_t pw[2][2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[t][i] *= f;
-    u32x4_t w[2];
+      for (int i = 0; i < 16; ++i) acc[n][t][i] = 0.f;
+    // before the first keys: weights of zero, logits that add nothing
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      z[i] = __builtin_amdgcn_exp2f(z[i] - base);
-      l += z[i];
+    for (int i = 0; i < 16; ++i) z[n][i] = -INFINITY;
+    mx[n] = m[n] = -INFINITY;
+    l[n] = 0.f;
+    pw[n][0] = pw[n][1] = u32x4_t{0u, 0u, 0u, 0u};
+  }
+
+  // a lane's keys: row col of 32, values 16 s + 8 hh .. + 7
+  const uint8_t* const kread = ksh + Im::at(col, hh);
+  // a transposing read: 16 lanes take 4 keys and 16 coordinates; lane i brings 8
+  // bytes of key i / 4 and gets coordinate i of all four.  Its 4 coordinates are
+  // chosen so that a lane's results are runs of 8 (see the stores).
+  const int li = lane & 15, dh = (lane >> 4) & 1;
+  const uint8_t* const vread = vsh + Im::at(4 * hh + (li >> 2), 2 * dh + (li & 1)) + ((li >> 1) & 1) * 8;
+  bf16x8_t kf[STEPS], vf[2][DT];
+  auto read_k = [&](int buf, int kb) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const bf16x8_t*>(kread + buf * BUF + kb * KB32 + s * 128);
+  };
+  auto tr = [&](const uint8_t* at) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at));
+  };
+  auto read_v = [&](int buf, int kb) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < DT; ++t) {
+        const uint8_t* at = vread + buf * BUF + kb * KB32 + s * KB16 + t * 256;
+        const uint2 a = tr(at), b = tr(at + KB8);
+        vf[s][t] = __builtin_bit_cast(bf16x8_t, u32x4_t{a.x, a.y, b.x, b.y});
+      }
+  };
+  auto max_of = [&](const f32x16_t& v) {
+    float r = v[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) r = fmaxf(r, v[i]);
+    return r;
+  };
+  // masks, and the running maximum moved where it has to be (keys key .. key + 31)
+  auto bounds = [&](auto blk, int key, uint32_t nan) {
+    constexpr int n = decltype(blk)::value;
+    if (key + 32 > limmin || nan) {
+      asm volatile("");                    // a branch: the selects must not run in every step
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[n][i] = key + 8 * (i / 4) + 4 * hh + i % 4 < lim[n] ? z[n][i] : -INFINITY;
+      if (nan) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = 8 * (i / 4) + 4 * hh + i % 4;
+          if (key + at < lim[n] && ((nan >> at) & 1u)) z[n][i] = NAN;
+        }
+      }
+      mx[n] = max_of(z[n]);
     }
+    if (__ballot(mx[n] * cq > m[n] + kLag)) {
+      float v = mx[n] * cq;
+      v = fmaxf(v, __shfl_xor(v, 32));
+      v = v > m[n] + kLag ? v : m[n];      // a row's maximum moves by its own logits only
+      const float f = v == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - v);
+      m[n] = v;
+      l[n] *= f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = cvt_pk_bf16(z[2 * e], z[2 * e + 1]);
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[n][t][i] *= f;
+    }
+  };
+  // One turn: the softmax of block n against the products of the other block,
+  // logits first, so that their maximum is there when the turn ends.
+  auto turn = [&](auto soft, auto reads, auto&& after_s, auto&& after_pv) {
+    constexpr int n = decltype(soft)::value, o = 1 - n;
+    const float base = m[n] == -INFINITY ? 0.f : m[n];
+    float pv[16];
+    f32x16_t zn;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zn[i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) zn = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], qf[o][s], zn, 0, 0, 0);
+    after_s();
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < DT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            *reinterpret_cast<const bf16x8_t*>(vs + (32 * t + col) * VP + 16 * s + 8 * hh), __builtin_bit_cast(bf16x8_t, w[s]),
-            acc[t], 0, 0, 0);
-  }
-  l += __shfl_xor(l, 32);
-  if (row0 + wave * 32 + col >= rows) return;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const int64_t o = (s0 + tok) * p.o_stride + (int64_t)(h * p.group + g) * D;
+        acc[o][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[s][t], __builtin_bit_cast(bf16x8_t, pw[o][s]), acc[o][t], 0, 0, 0);
+    after_pv();
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = 32 * t + 8 * e + 4 * hh;
-      f32x4_t v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = acc[t][4 * e + i] * inv;
-      if (p.out_f32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + o + d) = v;
-      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o + d) = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+    for (int i = 0; i < 16; ++i) {
+      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq, -base));
+      l[n] += pv[i];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pw[n][e / 4][e % 4] = cvt_pk_bf16(pv[2 * e], pv[2 * e + 1]);
+    z[o] = zn;
+    mx[o] = max_of(zn);
+    // the weights and the maximum are made here, not where they are used
+    asm volatile("" : "+v"(pw[n][0]), "+v"(pw[n][1]), "+v"(l[n]), "+v"(mx[o]));
+    sched_turn<decltype(reads)::value>(STEPS + 2 * DT);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using A = std::integral_constant<int, 0>;
+  using B = std::integral_constant<int, 1>;
+  auto none = [] {};
+
+  __builtin_amdgcn_s_waitcnt(kNoLoads);
+  __syncthreads();
+  if (KT > sure) {
+    clean(0);
+    __syncthreads();
+  }
+  read_k(0, 0);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) vf[s][t] = bf16x8_t{};
+  int buf = 0;
+  uint32_t before = 0;                     // keys of the 32 before whose values are not finite
+  for (int key = 0; key < k1; key += KT, buf ^= 1) {
+    const bool more = key + KT < k1;
+    if (more) fetch(key + KT, buf ^ 1);
+    uint32_t nans[KBS];
+#pragma unroll
+    for (int i = 0; i < KBS; ++i) nans[i] = 0;
+    if (key + KT > sure) {
+#pragma unroll
+      for (int i = 0; i < KBS; ++i) nans[i] = __builtin_amdgcn_readfirstlane(bad[buf][i]);
+    }
+#pragma unroll
+    for (int kb = 0; kb < KBS; ++kb) {
+      const int k = key + 32 * kb;
+      if (kb > 0 && k >= k1) break;        // the last step's keys may end early
+      bounds(B{}, k - 32, before);
+      before = nans[kb];
+      turn(B{}, std::integral_constant<int, 1>{}, none, none);
+      bounds(A{}, k, before);
+      turn(A{}, std::integral_constant<int, 2>{}, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); }, [&] { read_v(buf, kb); });
+    }
+    __builtin_amdgcn_s_waitcnt(kNoLoads);
+    __syncthreads();
+    if (more) {
+      if (key + 2 * KT > sure) {
+        clean(buf ^ 1);
+        __syncthreads();
+      }
+      read_k(buf ^ 1, 0);
+    }
+  }
+  // what is left: the last keys' products and block B's softmax
+  bounds(B{}, (k1 + 31) / 32 * 32 - 32, before);
+  turn(B{}, std::integral_constant<int, 1>{}, none, none);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+      acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[s][t], __builtin_bit_cast(bf16x8_t, pw[1][s]), acc[1][t], 0, 0, 0);
+
+  // Register i of tile t is the tile's row 8 (i / 4) + 4 hh + i % 4, which holds
+  // coordinate 32 t + 16 (i / 8) + 8 hh + i % 8 by the choice above.
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    l[n] += __shfl_xor(l[n], 32);
+    const int row = w.row0 + wave * 64 + n * 32 + col;
+    if (row >= w.rows) continue;
+    const int tok = row / p.group, g = row - tok * p.group;
+    const float inv = l[n] == 0.f ? 0.f : 1.0f / l[n];
+    const int64_t at = (int64_t)(w.s0 + tok) * p.o_stride + (int64_t)(h * p.group + g) * D + 8 * hh;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[n][t][8 * e + i] * inv;
+        const int d = 32 * t + 16 * e;
+        if (p.out_f32) {
+          f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at + d);
+          o[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+          o[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+        } else {
+          u32x4_t u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[i] = cvt_pk_bf16(v[2 * i], v[2 * i + 1]);
+          *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + at + d) = u;
+        }
+      }
+  }
+  // the last step's barrier has freed the LDS for the next tile
+  }
 }
 
 }  // namespace
@@ -151,10 +467,12 @@ __global__ __launch_bounds__(256) void prompt_kernel(Prompt p) {
 size_t prompt_ws_bytes(int head_dim, int heads, int group, int64_t B, int64_t T) { return 0; }
 
 hipError_t launch_prompt(const Prompt& p, void* ws, hipStream_t st) {
-  const int64_t tiles = (int64_t)p.T * p.group / kRows + p.B;
-  const dim3 grid((unsigned)(tiles * p.heads));
-  if (p.head_dim == 128) hipLaunchKernelGGL((prompt_kernel<128>), grid, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((prompt_kernel<64>), grid, dim3(256), 0, st, p);
+  constexpr int NW = 4;
+  const int64_t tiles = (int64_t)p.T * p.group / (64 * NW) + p.B;
+  const int64_t most = (1 << 22) / p.heads;
+  const dim3 grid((unsigned)((tiles < most ? tiles : most) * p.heads));
+  if (p.head_dim == 128) hipLaunchKernelGGL((prompt_kernel<128, NW>), grid, dim3(64 * NW), 0, st, p, tiles);
+  else hipLaunchKernelGGL((prompt_kernel<64, NW>), grid, dim3(64 * NW), 0, st, p, tiles);
   return hipGetLastError();
 }
 
