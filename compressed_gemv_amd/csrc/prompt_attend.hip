@@ -14,27 +14,28 @@ namespace qg {
 namespace {
 
 // Keys and values lie in LDS as they come from memory, 1 KB a wave and
-// instruction (4 keys of 128 values, 8 of 64), the 16-byte pieces of four keys
-// side by side: piece c of keys 4q .. 4q + 3 is one run of 64 bytes.  The runs of
-// a KB follow each other, with 64 (128) bytes between KBs, so that what a product
-// reads of 16 neighbouring keys lies in all banks once, and what a transposing
-// read takes of 4 keys and 32 coordinates (64 bytes of each) is 256 bytes in a
-// row; every address of the inner loop is one register plus a constant.
-// (64: the second four keys of a KB swap neighbouring pieces, for the same.)
+// instruction: 4 keys of 128 values (8 of 64), of which four lanes fetch 64
+// bytes in a row.  Those 64 bytes of four neighbouring keys follow each other, so
+// that a transposing read of 4 keys and 32 coordinates takes 256 bytes in a row,
+// and 16 (32) bytes between the KBs let a piece of 16 neighbouring keys lie in
+// all banks once; every address of the inner loop is one register plus a
+// constant.  (64: the second four keys of a KB swap neighbouring pieces.)
 template <int D>
 struct Image {
   static constexpr int KPB = 512 / D;                       // keys in a KB
-  static constexpr int PITCH = D == 128 ? 1024 + 64 : 1024 + 128;
+  static constexpr int PITCH = D == 128 ? 1024 + 16 : 1024 + 32;
   static constexpr int bytes(int keys) { return keys / KPB * PITCH; }
-  // of key (a multiple of 16 added later is a constant) and piece
+  // of a key and its 16-byte piece c; 16 keys or 2 pieces (S, even c) more are a constant
   static __device__ __forceinline__ int at(int key, int c) {
-    if constexpr (D == 128) return key / 4 * PITCH + c * 64 + (key & 3) * 16;
-    const int q = (key >> 2) & 1;
-    return key / 8 * PITCH + q * 512 + (c ^ q) * 64 + (key & 3) * 16;
+    const int q = D == 128 ? 0 : (key >> 2) & 1;
+    return key / KPB * PITCH + q * 512 + c / 4 * 256 + (key & 3) * 64 + ((c & 3) ^ q) * 16;
   }
-  // the key and piece that lane of a KB holds
-  static __device__ __forceinline__ int key_of(int lane) { return D == 128 ? lane & 3 : 4 * (lane >> 5) + (lane & 3); }
-  static __device__ __forceinline__ int piece_of(int lane) { return D == 128 ? lane >> 2 : ((lane >> 2) & 7) ^ (lane >> 5); }
+  static constexpr int two(int s) { return s / 2 * 256 + s % 2 * 32; }
+  // the key and piece that a lane of a KB holds
+  static __device__ __forceinline__ int key_of(int lane) { return (D == 128 ? 0 : 4 * (lane >> 5)) + ((lane >> 2) & 3); }
+  static __device__ __forceinline__ int piece_of(int lane) {
+    return D == 128 ? 4 * (lane >> 4) + (lane & 3) : 4 * ((lane >> 4) & 1) + ((lane & 3) ^ (lane >> 5));
+  }
 };
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -188,13 +189,18 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
 
   const uint16_t* const kp = p.K + (int64_t)w.s0 * p.k_stride + (int64_t)h * D + Im::piece_of(lane) * 8;
   const uint16_t* const vp = p.V + (int64_t)w.s0 * p.v_stride + (int64_t)h * D + Im::piece_of(lane) * 8;
-  auto fetch = [&](int key0, int buf) {
+  // The wave's KBs `from` .. `to` - 1 of a step's keys and values.  They are fetched
+  // in four parts over the step before: 16 loads at once hold up the products
+  // behind them (16000 tokens: 4017 -> 3986 us).
+  constexpr int SHARE = LOADS / NW;
+  auto fetch = [&](int key0, int buf, int from, int to) {
     auto put = [&](const void* from, uint8_t* to) {
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                        (__attribute__((address_space(3))) void*)to, 16, 0, 0);
     };
 #pragma unroll
-    for (int i = 0; i < LOADS / NW; ++i) {
+    for (int i = 0; i < SHARE; ++i) {
+      if (i < from || i >= to) continue;
       const int kb = wave + i * NW;
       int key = key0 + kb * Im::KPB + Im::key_of(lane);
       key = key < k1 ? key : k1 - 1;                        // behind the last key it is repeated, and masked
@@ -224,7 +230,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     }
   };
   if (tid < 2 * KBS) bad[tid / KBS][tid % KBS] = 0;
-  fetch(0, 0);
+  fetch(0, 0, 0, SHARE);
 
   bf16x8_t qf[2][STEPS];
   int lim[2], limmin = k1;
@@ -289,7 +295,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
   bf16x8_t kf[STEPS], vf[2][DT];
   auto read_k = [&](int buf, int kb) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const bf16x8_t*>(kread + buf * BUF + kb * KB32 + s * 128);
+    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const bf16x8_t*>(kread + buf * BUF + kb * KB32 + Im::two(s));
   };
   auto tr = [&](const uint8_t* at) {
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at));
@@ -391,7 +397,6 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
   uint32_t before = 0;                     // keys of the 32 before whose values are not finite
   for (int key = 0; key < k1; key += KT, buf ^= 1) {
     const bool more = key + KT < k1;
-    if (more) fetch(key + KT, buf ^ 1);
     uint32_t nans[KBS];
 #pragma unroll
     for (int i = 0; i < KBS; ++i) nans[i] = 0;
@@ -403,6 +408,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     for (int kb = 0; kb < KBS; ++kb) {
       const int k = key + 32 * kb;
       if (kb > 0 && k >= k1) break;        // the last step's keys may end early
+      if (more) fetch(key + KT, buf ^ 1, kb * SHARE / KBS, (kb + 1) * SHARE / KBS);
       bounds(B{}, k - 32, before);
       before = nans[kb];
       turn(B{}, std::integral_constant<int, 1>{}, none, none);
