@@ -1100,59 +1100,63 @@ def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, start
         raise ValueError("Q and K: both missing")
     if first.dim() != 3:
         raise ValueError(f"rows must be [T][heads][D], got shape {tuple(first.shape)}")
-    place, (T, _, D) = _Place(first), first.shape
-    heads, strides = [], []
-    for t, what in ((Q, "Q"), (K, "K")):
-        heads.append(0 if t is None else t.shape[1] if t.dim() == 3 else -1)
-        strides.append(0 if t is None else _cache_rows(t, heads[-1], D, (first.dtype,) if first.dtype in _OUT else _OUT, what))
-        if t is not None and t.shape[0] != T:
-            raise ValueError(f"{what}: {t.shape[0]} rows, Q has {T}")
+    place, (T, _, D), f32 = _Place(first), first.shape, first.dtype == torch.float32
     B = lens.numel()
-    _need_numel(lens, B, "lens", (torch.int32,))
+    if lens.dtype != torch.int32:
+        _need_numel(lens, B, "lens", (torch.int32,))
     if starts is None and B != T:
         raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} sequences")
     sp = _starts_of(starts, B)
-    rot = 0
-    if freqs is not None:
-        _need_numel(freqs, freqs.numel(), "freqs", (torch.float64,))
-        rot = 2 * freqs.numel()
-    wd = torch.float32
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_numel(w, D, what, _OUT)
-            wd = w.dtype
-    if q_weight is not None and q_weight.dtype != wd:
-        raise ValueError("q_weight and k_weight: one dtype for both")
-    given = [t.dtype for t in (Qo, Ko) if t is not None]
-    dt = given[0] if given else out_dtype
+    dt = Qo.dtype if Qo is not None else Ko.dtype if Ko is not None else out_dtype
     if dt not in _OUT:
         raise ValueError(f"out_dtype {dt}, expected one of {_OUT}")
+    q_heads, qs, qos = _rope_rows(Q, Qo, T, D, first.dtype, dt, "Q")
+    k_heads, ks, kos = _rope_rows(K, Ko, T, D, first.dtype, dt, "K")
+    rot = 0
+    if freqs is not None:
+        rot = 2 * freqs.numel()
+        if freqs.dtype != torch.float64:
+            raise ValueError(f"freqs: dtype {freqs.dtype}, expected torch.float64")
+    w = q_weight if q_weight is not None else k_weight
+    if w is not None:
+        _need_numel(w, D, "q_weight" if w is q_weight else "k_weight", _OUT)
+        if w is q_weight and k_weight is not None:
+            _need_numel(k_weight, D, "k_weight", (w.dtype,))
     _here(place, lens=lens, starts=starts, freqs=freqs, q_weight=q_weight, k_weight=k_weight)
     _on_device(place, False, Q, K, Qo, Ko)
-    outs, ostrides = [], []
-    for t, o, h, what in ((Q, Qo, heads[0], "Qo"), (K, Ko, heads[1], "Ko")):
-        if t is None:
-            if o is not None:
-                raise ValueError(f"{what}: given, and its input is missing")
-            ostrides.append(0)
-        elif o is None:
-            o = _fresh(place, stream, (T, h, D), dt, True)
-            ostrides.append(h * D)
-        else:
-            ostrides.append(_cache_rows(o, h, D, (dt,), what))
-            if o.shape[0] != T:
-                raise ValueError(f"{what}: {o.shape[0]} rows, its input has {T}")
-        outs.append(o)
+    if Q is not None and Qo is None:
+        Qo = _fresh(place, stream, (T, q_heads, D), dt, True)
+    if K is not None and Ko is None:
+        Ko = _fresh(place, stream, (T, k_heads, D), dt, True)
     if T == 0:
-        return tuple(outs)
-    p = qrope(D, heads[0], heads[1], rot, int(bool(pairs)), None if freqs is None else freqs.data_ptr(),
-              None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-              Q_F32 if wd == torch.float32 else Q_BF16, eps, offset)
-    _call_on(place, stream, "qnorm_rope", load().qnorm_rope, p, B, T, lens.data_ptr(), sp,
-             None if Q is None else Q.data_ptr(), strides[0], None if K is None else K.data_ptr(), strides[1],
-             Q_F32 if first.dtype == torch.float32 else Q_BF16, None if Q is None else outs[0].data_ptr(), ostrides[0],
-             None if K is None else outs[1].data_ptr(), ostrides[1], Q_F32 if dt == torch.float32 else Q_BF16)
-    return tuple(outs)
+        return Qo, Ko
+    p = qrope(D, q_heads, k_heads, rot, 1 if pairs else 0, _at(freqs), _at(q_weight), _at(k_weight),
+              Q_F32 if w is not None and w.dtype == torch.float32 else Q_BF16, eps, offset)
+    _call_on(place, stream, "qnorm_rope", load().qnorm_rope, p, B, T, lens.data_ptr(), sp, _at(Q), qs, _at(K), ks,
+             Q_F32 if f32 else Q_BF16, _at(Qo), qos, _at(Ko), kos, Q_F32 if dt == torch.float32 else Q_BF16)
+    return Qo, Ko
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rope_rows(t, out, T: int, D: int, dtype, out_dtype, what: str):
+    """(heads, stride, output's stride) of rows t (None: no heads) and of their output (None: a new one)."""
+    if t is None:
+        if out is not None:
+            raise ValueError(f"{what}o: given, and {what} is missing")
+        return 0, 0, 0
+    heads = t.shape[1] if t.dim() == 3 else -1
+    stride = _cache_rows(t, heads, D, (dtype,) if dtype in _OUT else _OUT, what)
+    if t.shape[0] != T:
+        raise ValueError(f"{what}: {t.shape[0]} rows, expected {T}")
+    if out is None:
+        return heads, stride, heads * D
+    o_stride = _cache_rows(out, heads, D, (out_dtype,), what + "o")
+    if out.shape[0] != T:
+        raise ValueError(f"{what}o: {out.shape[0]} rows, expected {T}")
+    return heads, stride, o_stride
 
 
 @functools.lru_cache(maxsize=1024)

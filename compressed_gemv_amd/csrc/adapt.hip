@@ -51,14 +51,18 @@ AdaptPlan plan_adapt(bool segments, int64_t seqs, int64_t T, int64_t K, int64_t 
     tiles = T / kTile + (seqs < 16 ? seqs : 16);
   } else {
     p.blocks = ceil_div(T, kTile);
-    p.slots = T <= 1024 ? (int)(T < kTile ? T : kTile) : 4;
-    tiles = p.blocks * (p.slots < 16 ? p.slots : 16);
+    // A workgroup without an adapter costs 3 us of its place: 64 rows with 12
+    // adapters take 49 us with 64 slots, 16 with 16.  Behind 1024 rows there are
+    // blocks enough.
+    p.slots = T <= 1024 ? (int)(T < 16 ? T : 16) : 4;
+    tiles = p.blocks * p.slots;
   }
-  int64_t s = ceil_div(512, tiles);
-  const int64_t most = ceil_div(K, 256);
+  const bool wide = segments && T >= 16 * seqs;
+  int64_t s = ceil_div(1024, tiles);       // (5 prompts of 77 .. 1500 rows: 256 workgroups 246 us, 512 202, 1024 199)
+  const int64_t most = ceil_div(K, 512);
   s = s > most ? most : s;
   s = s > 32 ? 32 : s;
-  p.kchunk = (int)(ceil_div(ceil_div(K, s), 128) * 128);
+  p.kchunk = (int)(ceil_div(ceil_div(K, s), wide ? 256 : 512) * (wide ? 256 : 512));
   p.splits = (int)ceil_div(K, p.kchunk);
   int64_t c = ceil_div(N * tiles, 1024);
   c = ceil_div(c, 256) * 256;
@@ -195,24 +199,27 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(Adapt p, int slots, int
     f32x4_t acc[QT];
 #pragma unroll
     for (int q = 0; q < QT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const int step = wide ? 32 : 128;
-    constexpr int U = 4;
-    for (int k = k0 + (wide ? 0 : 32 * wave); k < k1; k += U * step) {
-      u32x4_t xv[U], av[U][QT];
+    constexpr int U = 4;                   // steps of 32 inputs under way at a time
+    auto walk = [&](int from, int step) {
+      for (int k = from; k < k1; k += U * step) {
+        u32x4_t xv[U], av[U][QT];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int kk = k + u * step;
-        const bool in = kk + 8 * g < k1;                     // k1 is K, a multiple of 8, or of 32
-        xv[u] = load16(xb, in && row >= 0 ? xrow + 2u * kk : kOut);
+        for (int u = 0; u < U; ++u) {
+          const int kk = k + u * step;
+          const bool in = kk + 8 * g < k1;                   // k1 is K, a multiple of 8, or of 32
+          xv[u] = load16(xb, in && row >= 0 ? xrow + 2u * kk : kOut);
 #pragma unroll
-        for (int q = 0; q < QT; ++q) av[u][q] = load16(ab, in ? arow[q] + 2u * kk : kOut);
+          for (int q = 0; q < QT; ++q) av[u][q] = load16(ab, in ? arow[q] + 2u * kk : kOut);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(av[u][q]), frag(xv[u]), acc[q], 0, 0, 0);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < QT; ++q)
-          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(av[u][q]), frag(xv[u]), acc[q], 0, 0, 0);
-    }
+    };
+    if (wide) walk(k0, 32);
+    else walk(k0 + 32 * wave, 128);
     if (!wide) {
       if (wave > 0) {
 #pragma unroll
@@ -249,33 +256,78 @@ struct UpRows {
   int n, held;
 };
 
+// A wave's 64 outputs from n0 on: of B the first 32 ranks, fetched before h is there.
+template <bool F32>
+struct UpCols {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int n0, n1, held;
+  u32x4_t first[4];
+  // outputs relative to n0: product c's row m is output perm(c, m)
+  static __device__ __forceinline__ int perm(int c, int m) { return F32 ? 16 * c + m : 32 * (c / 2) + 8 * (m / 4) + 4 * (c % 2) + m % 4; }
+  __device__ __forceinline__ void begin(const Adapt& p, const Tile& t, int n0_, int n1_, int held_, int lane) {
+    n0 = n0_;
+    n1 = n1_;
+    held = held_;
+    rsrc = make_rsrc(p.B + ((int64_t)t.a * p.N + n0) * p.rank, (uint32_t)(n1 - n0) * (uint32_t)p.rank * 2u);
+    load(p.rank, 0, lane, first);
+  }
+  // ranks 32 J .. of B; a lane holds 8 (of ranks up to 16 the upper lanes the same again)
+  __device__ __forceinline__ void load(int rank, int J, int lane, u32x4_t (&v)[4]) const {
+    const int g = lane >> 4, j = held <= 16 ? 8 * (g & 1) : 32 * J + 8 * g;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = load16(rsrc, j < held ? (uint32_t)(perm(c, lane & 15) * rank + j) * 2u : kOut);
+  }
+  // what lies behind the adapter's own rank may be anything
+  __device__ __forceinline__ void mask(int J, int lane, u32x4_t (&v)[4]) const {
+    const int g = lane >> 4, c8 = held - (held <= 16 ? 8 * (g & 1) : 32 * J + 8 * g);
+    if (c8 >= 8) return;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t m = c8 >= 2 * w + 2 ? 0xFFFFFFFFu : (c8 == 2 * w + 1 ? 0xFFFFu : 0u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c][w] &= m;
+    }
+  }
+};
+
 template <bool F32, int RT>
-__device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpRows& u, int row_tile, int n0, int n1, int lane) {
-  const int r16 = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpRows& u, const UpCols<F32>& b, int row_tile, int lane) {
+  const int r16 = lane & 15, g = lane >> 4, n0 = b.n0, n1 = b.n1;
   const bool both = u.lo_at == 16;         // hi and lo in one block
-  const auto bb = make_rsrc(p.B + ((int64_t)t.a * p.N + n0) * p.rank, (uint32_t)(n1 - n0) * (uint32_t)p.rank * 2u);
-  // outputs of the wave, relative to n0: product c's row m is output perm(c, m)
-  auto perm = [](int c, int m) { return F32 ? 16 * c + m : 32 * (c / 2) + 8 * (m / 4) + 4 * (c % 2) + m % 4; };
+  // y comes while the products run
+  int64_t row[RT];
+  f32x4_t yv[RT][4];
+  u32x4_t yh[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int at = 16 * (row_tile + i) + r16;
+    row[i] = at < u.n ? t.row0 + u.rows[at] : -1;
+    if (row[i] < 0) continue;
+    const int64_t yo = row[i] * p.y_stride + n0;
+    if constexpr (F32) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n0 + 16 * c + 4 * g + 4 <= n1) yv[i][c] = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p.y) + yo + 16 * c + 4 * g);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (n0 + 32 * c + 8 * g + 8 <= n1) yh[i][c] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p.y) + yo + 32 * c + 8 * g);
+    }
+  }
   f32x4_t acc[RT][4];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int J = 0; J < u.blocks; ++J) {
-    const int j = both ? 8 * (g & 1) : 32 * J + 8 * g;       // ranks j .. j + 7 of the lane's operand
-    int c8 = u.held - j;
-    c8 = c8 < 0 ? 0 : (c8 > 8 ? 8 : c8);
     u32x4_t bv[4];
+    if (J == 0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) bv[c] = load16(bb, c8 > 0 ? (uint32_t)(perm(c, r16) * p.rank + j) * 2u : kOut);
-    if (c8 < 8) {                          // what lies behind the adapter's own rank may be anything
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t m = c8 >= 2 * w + 2 ? 0xFFFFFFFFu : (c8 == 2 * w + 1 ? 0xFFFFu : 0u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) bv[c][w] &= m;
-      }
+      for (int c = 0; c < 4; ++c) bv[c] = b.first[c];
+    } else {
+      b.load(p.rank, J, lane, bv);
     }
+    b.mask(J, lane, bv);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const uint16_t* hr = u.h + (16 * (row_tile + i) + r16) * u.pitch + 32 * J + 8 * g;
@@ -291,10 +343,8 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const int at = 16 * (row_tile + i) + r16;
-    if (at >= u.n) continue;
-    const int64_t row = t.row0 + u.rows[at];
-    const int64_t yo = row * p.y_stride + n0, oo = row * p.o_stride + n0;
+    if (row[i] < 0) continue;
+    const int64_t yo = row[i] * p.y_stride + n0, oo = row[i] * p.o_stride + n0;
     if constexpr (F32) {
       const float* y = static_cast<const float*>(p.y) + yo;
       float* o = static_cast<float*>(p.out) + oo;
@@ -302,7 +352,7 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
       for (int c = 0; c < 4; ++c) {
         const int n = 16 * c + 4 * g;
         if (n0 + n + 4 <= n1) {
-          *reinterpret_cast<f32x4_any*>(o + n) = *reinterpret_cast<const f32x4_any*>(y + n) + acc[i][c];
+          *reinterpret_cast<f32x4_any*>(o + n) = yv[i][c] + acc[i][c];
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -316,7 +366,7 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
       for (int c = 0; c < 4; c += 2) {
         const int n = 16 * c + 8 * g;
         if (n0 + n + 8 <= n1) {
-          const u32x4_t v = *reinterpret_cast<const u32x4_any*>(y + n);
+          const u32x4_t v = yh[i][c / 2];
           u32x4_t w;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -333,7 +383,7 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
   }
 }
 
-template <bool F32>
+template <bool F32, int RT>
 __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int splits, int nchunk, int R) {
   __shared__ uint8_t rows[kTile];
   extern __shared__ __align__(16) uint16_t hbuf[];
@@ -372,14 +422,25 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
     u.lo_at = deep;
     u.blocks = both ? 1 : deep / 32;
     u.pitch = 2 * deep + 8;                // 16 bytes more: neighbouring rows in other banks
-    const int tall = (t.n + 15) / 16 * 16, kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
+    const int tall = (t.n + 16 * RT - 1) / (16 * RT) * (16 * RT), kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
     const float scale = p.scales[t.a];
+    UpCols<F32> cols;
+    const int mine = first + 64 * wave;
+    if (mine < last) cols.begin(p, t, mine, last - mine < 64 ? last : mine + 64, u.held, lane);
     for (int i = threadIdx.x; i < tall * (deep / 4); i += 256) {
       const int at = i / (deep / 4), j = 4 * (i % (deep / 4));
       f32x4_t h = {0.f, 0.f, 0.f, 0.f};
       if (at < t.n && j < kept) {
         const float* from = p.part + ((int64_t)t.row0 + rows[at]) * R + j;
-        for (int s = 0; s < splits; ++s) h += *reinterpret_cast<const f32x4_t*>(from + (int64_t)s * p.T * R);
+        for (int s = 0; s < splits; s += 8) {                // 8 loads under way, added in their order
+          f32x4_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (s + e < splits) v[e] = *reinterpret_cast<const f32x4_t*>(from + (int64_t)(s + e) * p.T * R);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (s + e < splits) h += v[e];
+        }
         h *= scale;
       }
       uint32_t hi[2], lo[2];
@@ -393,14 +454,9 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
     }
     __syncthreads();
     const int tiles16 = tall / 16;
-    for (int n0 = first + 64 * wave; n0 < last; n0 += 256) {
-      const int n1 = last - n0 < 64 ? last : n0 + 64;
-      if (tiles16 == 1) up_tile<F32, 1>(p, t, u, 0, n0, n1, lane);
-      else
-        for (int i = 0; i < tiles16; i += 2) {
-          if (i + 1 < tiles16) up_tile<F32, 2>(p, t, u, i, n0, n1, lane);
-          else up_tile<F32, 1>(p, t, u, i, n0, n1, lane);
-        }
+    for (int n0 = mine; n0 < last; n0 += 256) {
+      if (n0 != mine) cols.begin(p, t, n0, last - n0 < 64 ? last : n0 + 64, u.held, lane);
+      for (int i = 0; i < tiles16; i += RT) up_tile<F32, RT>(p, t, u, cols, i, lane);
     }
   }
 }
@@ -422,11 +478,18 @@ hipError_t launch_adapt(const Adapt& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int deep = p.rank <= 16 ? 16 : (p.rank + 31) / 32 * 32;
-  const int64_t tall = p.T < kTile ? ceil_div(p.T, 16) * 16 : kTile;
+  const int64_t tall = p.T < kTile ? ceil_div(p.T, 32) * 32 : kTile;
   const size_t lds = (size_t)tall * (2 * deep + 8) * 2;
   const dim3 up((unsigned)(a.blocks * a.slots), (unsigned)ceil_div(p.N, a.nchunk));
-  if (p.f32) hipLaunchKernelGGL((adapt_up_kernel<true>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
-  else hipLaunchKernelGGL((adapt_up_kernel<false>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
+#define UP(F, RT) hipLaunchKernelGGL((adapt_up_kernel<F, RT>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R)
+  if (p.f32) {
+    if (p.starts) UP(true, 2);
+    else UP(true, 1);
+  } else {
+    if (p.starts) UP(false, 2);
+    else UP(false, 1);
+  }
+#undef UP
   return hipGetLastError();
 }
 
