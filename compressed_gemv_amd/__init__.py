@@ -971,23 +971,27 @@ class _Place:
     """The device of a call without a handle: that of its first tensor."""
     __slots__ = ("_device", "_index")
 
-    def __init__(self, t: torch.Tensor):
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA (HIP) tensors")
-        self._device, self._index = t.device, t.get_device()
+    def __init__(self, index: int):
+        self._device, self._index = torch.device("cuda", index), index
 
 
-def _here(place, **ts):
+@functools.lru_cache(maxsize=64)
+def _device_place(index: int) -> _Place:
+    return _Place(index)
+
+
+def _place_of(t: torch.Tensor) -> _Place:
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA (HIP) tensors")
+    return _device_place(t.get_device())
+
+
+def _here(place, *ts):
     """Every tensor is on place's device, and contiguous."""
-    for what, t in ts.items():
-        if t is None:
-            continue
-        if t.get_device() != place._index:
-            if not t.is_cuda:
-                raise ValueError("tensors must be CUDA (HIP) tensors")
-            raise ValueError(f"tensors on different devices: {place._device} and {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
+    for t in ts:
+        if t is not None and (t.get_device() != place._index or not t.is_contiguous()):
+            _on_device(place, False, t)
+            raise ValueError("all arguments but rows and outputs must be contiguous")
 
 
 def _matrix(t: torch.Tensor, T, width: int, dtypes, what: str) -> int:
@@ -1067,7 +1071,7 @@ def qadapt(adapters: qadapters, x: torch.Tensor, y: torch.Tensor, ids, starts=No
         raise ValueError(f"starts: missing, and {T} rows are not one for each of {B} requests")
     sp = _starts_of(starts, B)
     os_ = adapters.N if out is None else _matrix(out, T, adapters.N, (y.dtype,), "out")
-    _here(adapters, ids=ids, starts=starts, ws=ws)
+    _here(adapters, ids, starts, ws)
     _on_device(adapters, False, x, y, out)
     if out is None:
         out = _fresh(adapters, stream, (T, adapters.N), y.dtype, True)
@@ -1100,7 +1104,7 @@ def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, start
         raise ValueError("Q and K: both missing")
     if first.dim() != 3:
         raise ValueError(f"rows must be [T][heads][D], got shape {tuple(first.shape)}")
-    place, (T, _, D), f32 = _Place(first), first.shape, first.dtype == torch.float32
+    place, (T, _, D), dtype = _place_of(first), first.shape, first.dtype
     B = lens.numel()
     if lens.dtype != torch.int32:
         _need_numel(lens, B, "lens", (torch.int32,))
@@ -1110,8 +1114,8 @@ def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, start
     dt = Qo.dtype if Qo is not None else Ko.dtype if Ko is not None else out_dtype
     if dt not in _OUT:
         raise ValueError(f"out_dtype {dt}, expected one of {_OUT}")
-    q_heads, qs, qos = _rope_rows(Q, Qo, T, D, first.dtype, dt, "Q")
-    k_heads, ks, kos = _rope_rows(K, Ko, T, D, first.dtype, dt, "K")
+    q_heads, qs, qos = _rope_rows(Q, Qo, T, D, dtype, dt, "Q")
+    k_heads, ks, kos = _rope_rows(K, Ko, T, D, dtype, dt, "K")
     rot = 0
     if freqs is not None:
         rot = 2 * freqs.numel()
@@ -1122,7 +1126,7 @@ def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, start
         _need_numel(w, D, "q_weight" if w is q_weight else "k_weight", _OUT)
         if w is q_weight and k_weight is not None:
             _need_numel(k_weight, D, "k_weight", (w.dtype,))
-    _here(place, lens=lens, starts=starts, freqs=freqs, q_weight=q_weight, k_weight=k_weight)
+    _here(place, lens, starts, freqs, q_weight, k_weight)
     _on_device(place, False, Q, K, Qo, Ko)
     if Q is not None and Qo is None:
         Qo = _fresh(place, stream, (T, q_heads, D), dt, True)
@@ -1133,7 +1137,7 @@ def qnorm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], lens, start
     p = qrope(D, q_heads, k_heads, rot, 1 if pairs else 0, _at(freqs), _at(q_weight), _at(k_weight),
               Q_F32 if w is not None and w.dtype == torch.float32 else Q_BF16, eps, offset)
     _call_on(place, stream, "qnorm_rope", load().qnorm_rope, p, B, T, lens.data_ptr(), sp, _at(Q), qs, _at(K), ks,
-             Q_F32 if f32 else Q_BF16, _at(Qo), qos, _at(Ko), kos, Q_F32 if dt == torch.float32 else Q_BF16)
+             Q_F32 if dtype == torch.float32 else Q_BF16, _at(Qo), qos, _at(Ko), kos, Q_F32 if dt == torch.float32 else Q_BF16)
     return Qo, Ko
 
 
@@ -1147,10 +1151,11 @@ def _rope_rows(t, out, T: int, D: int, dtype, out_dtype, what: str):
         if out is not None:
             raise ValueError(f"{what}o: given, and {what} is missing")
         return 0, 0, 0
-    heads = t.shape[1] if t.dim() == 3 else -1
+    shape = t.shape
+    heads = shape[1] if len(shape) == 3 else -1
     stride = _cache_rows(t, heads, D, (dtype,) if dtype in _OUT else _OUT, what)
-    if t.shape[0] != T:
-        raise ValueError(f"{what}: {t.shape[0]} rows, expected {T}")
+    if shape[0] != T:
+        raise ValueError(f"{what}: {shape[0]} rows, expected {T}")
     if out is None:
         return heads, stride, heads * D
     o_stride = _cache_rows(out, heads, D, (out_dtype,), what + "o")
@@ -1183,7 +1188,7 @@ def qprompt_attend(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts=Non
     q_heads = Q.shape[1]
     if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads:
         raise ValueError(f"Q: {q_heads} heads, not a multiple of K's {kv_heads}")
-    place = _Place(Q)
+    place = _place_of(Q)
     strides = [_cache_rows(t, h, D, _Q16, what) for t, h, what in ((Q, q_heads, "Q"), (K, kv_heads, "K"), (V, kv_heads, "V"))]
     for t, what in ((Q, "Q"), (V, "V")):
         if t.shape[0] != T:
@@ -1200,7 +1205,7 @@ def qprompt_attend(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts=Non
         o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
         if out.shape[0] != T:
             raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
-    _here(place, starts=starts, ws=ws)
+    _here(place, starts, ws)
     _on_device(place, False, Q, K, V, out)
     if out is None:
         out = _fresh(place, stream, (T, q_heads, D), out_dtype, True)

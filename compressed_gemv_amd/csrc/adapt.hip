@@ -58,7 +58,7 @@ AdaptPlan plan_adapt(bool segments, int64_t seqs, int64_t T, int64_t K, int64_t 
     tiles = p.blocks * p.slots;
   }
   const bool wide = segments && T >= 16 * seqs;
-  int64_t s = ceil_div(1024, tiles);       // (5 prompts of 77 .. 1500 rows: 256 workgroups 246 us, 512 202, 1024 199)
+  int64_t s = ceil_div(1024, tiles);       // (5 prompts of 77 .. 1500 rows: 512 workgroups 164 us, 768 155, 1024 157)
   const int64_t most = ceil_div(K, 512);
   s = s > most ? most : s;
   s = s > 32 ? 32 : s;
@@ -239,6 +239,135 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(Adapt p, int slots, int
       for (int q = 0; q < QT; ++q)
         if (16 * q < held) *reinterpret_cast<f32x4_t*>(to + 16 * q) = acc[q];
     }
+  }
+}
+
+// The same for requests of many rows.  A product's operands lie in 16 different
+// rows, and fetched that way (four lanes, four lines) x arrives at 1.9
+// TB/s; here four neighbouring lanes fetch 64 bytes of a row, and the operands
+// pass through LDS, each wave's in a place of its own: no barrier.  The waves
+// share the range of K, so A is fetched once for all 64 rows.  (5 prompts of 77 ..
+// 1500 rows, 28672 inputs, rank 32: the call 206 -> 157 us.)
+template <int QT>
+__global__ __launch_bounds__(256) void adapt_down_tall_kernel(Adapt p, int kchunk, int R) {
+  constexpr int U = 2, KW = 32 * U, STEP = 4 * KW;          // inputs a wave and a workgroup take at a time
+  constexpr int STAGE = U * (4 + QT) * 1024;
+  __shared__ uint8_t rows[kTile];
+  __shared__ __align__(16) uint8_t stage[4 * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rank0 = blockIdx.z * 64;
+  const int k0 = blockIdx.y * kchunk, k1 = p.K - k0 < kchunk ? p.K : k0 + kchunk;
+  const int r16 = lane & 15, g = lane >> 4;
+  Tiles tiles(p, blockIdx.x, lane);
+  Tile t;
+  if (!tiles.next(p, blockIdx.x, 0, 1, lane, rows, t) || t.a < 0) return;
+  const int ranks = rank_of(p, t.a) - rank0;
+  if (ranks <= 0) return;
+  const int held = ranks < 16 * QT ? ranks : 16 * QT;
+  const int rt = (t.n + 15) / 16, qt = (held + 15) / 16;    // tiles of rows and of ranks
+  const uint16_t* const x = p.x + (int64_t)t.row0 * p.x_stride;
+  const uint16_t* const A = p.A + ((int64_t)t.a * p.rank + rank0) * p.K;
+  f32x4_t acc[QT][4];
+#pragma unroll
+  for (int q = 0; q < QT; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[q][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // a 16 x 32 block: lane l fetches piece (l % 4) ^ (l / 16) of row l / 4, so that
+  // reading piece g of 16 rows meets all banks once; rows behind the last one
+  // (and ranks behind the adapter's own) repeat it, and are not used
+  uint8_t* const mine = stage + wave * STAGE;
+  const int lrow = lane >> 2, lpiece = (lane & 3) ^ (lane >> 4);
+  const uint8_t* const read = mine + r16 * 64 + ((g ^ (r16 >> 2)) * 16);
+  const uint16_t* xl[4];
+  const uint16_t* al[QT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * i + lrow < t.n ? 16 * i + lrow : t.n - 1;
+    xl[i] = x + row * p.x_stride + 8 * lpiece;
+  }
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    const int row = 16 * q + lrow < held ? 16 * q + lrow : held - 1;
+    al[q] = A + (int64_t)row * p.K + 8 * lpiece;
+  }
+  auto put = [&](const uint16_t* from, uint8_t* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+  };
+  int k = k0;
+  for (; k + STEP <= k1; k += STEP) {
+    const int kk = k + wave * KW;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < rt) put(xl[i] + kk + 32 * u, mine + (u * (4 + QT) + i) * 1024);
+#pragma unroll
+      for (int q = 0; q < QT; ++q)
+        if (q < qt) put(al[q] + kk + 32 * u, mine + (u * (4 + QT) + 4 + q) * 1024);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                     // vmcnt(0)
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bf16x8_t av[QT];
+#pragma unroll
+      for (int q = 0; q < QT; ++q)
+        if (q < qt) av[q] = *reinterpret_cast<const bf16x8_t*>(read + (u * (4 + QT) + 4 + q) * 1024);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= rt) continue;
+        const bf16x8_t xv = *reinterpret_cast<const bf16x8_t*>(read + (u * (4 + QT) + i) * 1024);
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          if (q < qt) acc[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[q], xv, acc[q][i], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0): read before it is written again
+    asm volatile("" ::: "memory");
+  }
+  // what is left of K (of the last range only): operands straight from memory, zeros behind the end
+  if (k < k1) {
+    const int last = t.n - 1;
+    const auto xb = make_rsrc(x, (uint32_t)(last * p.x_stride + p.K) * 2u);
+    const auto ab = make_rsrc(A, (uint32_t)held * (uint32_t)p.K * 2u);
+    for (int kk = k + 32 * wave; kk < k1; kk += 128) {
+      const bool in = kk + 8 * g < k1;
+      u32x4_t av[QT], xv[4];
+#pragma unroll
+      for (int q = 0; q < QT; ++q) av[q] = load16(ab, in ? (uint32_t)((16 * q + r16) * p.K + 8 * g + kk) * 2u : kOut);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xv[i] = load16(xb, in && 16 * i + r16 < t.n ? (uint32_t)((16 * i + r16) * p.x_stride + 8 * g + kk) * 2u : kOut);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          acc[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(av[q]), frag(xv[i]), acc[q][i], 0, 0, 0);
+    }
+  }
+  // the waves' sums: wave i adds up row tile i, in the waves' order
+  float* const red = reinterpret_cast<float*>(stage);
+  __syncthreads();
+  for (int w = 0; w < 4; ++w) {            // one row tile at a time: 4 waves x QT KB
+    if (w >= rt) break;
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      f32x4_t v = acc[q][0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) v = w == i ? acc[q][i] : v;
+      *reinterpret_cast<f32x4_t*>(red + ((wave * QT + q) * 64 + lane) * 4) = v;
+    }
+    __syncthreads();
+    const int at = 16 * w + r16;
+    for (int q = wave; q < qt; q += 4) {
+      f32x4_t v = *reinterpret_cast<const f32x4_t*>(red + (q * 64 + lane) * 4);
+#pragma unroll
+      for (int o = 1; o < 4; ++o) v += *reinterpret_cast<const f32x4_t*>(red + ((o * QT + q) * 64 + lane) * 4);
+      if (at < t.n)
+        *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * p.T + t.row0 + at) * R + rank0 + 16 * q + 4 * g) = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -472,7 +601,11 @@ size_t adapt_ws_bytes(int64_t seqs, int64_t T, int64_t K, int rank) {
 hipError_t launch_adapt(const Adapt& p, hipStream_t st) {
   const AdaptPlan a = plan_adapt(p.starts != nullptr, p.seqs, p.T, p.K, p.N, p.rank);
   const dim3 down((unsigned)(a.blocks * a.slots), (unsigned)a.splits, (unsigned)((p.rank + 63) / 64));
-  if (p.rank <= 16) hipLaunchKernelGGL((adapt_down_kernel<1>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
+  if (p.starts && p.T >= 16 * (int64_t)p.seqs) {
+    if (p.rank <= 16) hipLaunchKernelGGL((adapt_down_tall_kernel<1>), down, dim3(256), 0, st, p, a.kchunk, a.R);
+    else if (p.rank <= 32) hipLaunchKernelGGL((adapt_down_tall_kernel<2>), down, dim3(256), 0, st, p, a.kchunk, a.R);
+    else hipLaunchKernelGGL((adapt_down_tall_kernel<4>), down, dim3(256), 0, st, p, a.kchunk, a.R);
+  } else if (p.rank <= 16) hipLaunchKernelGGL((adapt_down_kernel<1>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
   else if (p.rank <= 32) hipLaunchKernelGGL((adapt_down_kernel<2>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
   else hipLaunchKernelGGL((adapt_down_kernel<4>), down, dim3(256), 0, st, p, a.slots, a.kchunk, a.R);
   hipError_t e = hipGetLastError();
