@@ -2,8 +2,18 @@
 // with grouped heads.
 //
 // A KV head's rows of one sequence are its tokens times `group` query heads,
-// row = token * group + g; a workgroup takes a tile of 64 NW of them and walks
-// the keys that its last token sees, 32 NW at a time.
+// row = token * group + g; a workgroup takes a tile of 256 of them (128 or 64
+// where there are few tiles) and walks the keys that its last token sees, 128 at
+// a time.  Tiles go to workgroups in the order of what they cost, the long ones
+// first, so no workgroup is left with a long one at the end.
+//
+// Bound by what a SIMD's one wave issues.  Measured (8 KV heads of 128, 8 query
+// heads each): 1.06 PFLOP/s for one prompt of 16000 (3.95 ms; a large matrix
+// product reaches 1.2 here), 0.77 for three of 999 .. 2500 (218 us).  In copies
+// of the kernel with parts left out, 16000 tokens took 11 % less without the
+// fetches of the next keys, 4 % less without exponentials, 2 % without the
+// maximum and nothing less without the reads from LDS; other orders of the
+// products and more vector instructions between them cost 1 to 2 %.
 #include <type_traits>
 
 #include "kvcache_plan.hpp"
@@ -157,8 +167,8 @@ __device__ __forceinline__ void sched_turn(int products) {
   }
 }
 
-// A workgroup: NW waves of 64 rows (two blocks of 32), one wave per SIMD with
-// all its registers; 32 NW keys a step, two LDS buffers.  S^T = K Q^T on
+// A workgroup: four waves of 64 rows (two blocks of 32), one wave per SIMD with
+// all its registers; 128 keys a step, two LDS buffers.  S^T = K Q^T on
 // 32x32x16 products puts a row's logits of 16 keys into one lane; the weights go
 // back in as the other operand of O^T = V^T P^T without leaving the lane.  The
 // two blocks take turns, the products of one running while the vector unit does
@@ -167,18 +177,24 @@ __device__ __forceinline__ void sched_turn(int products) {
 //                       vector    softmax of S_B (the keys before)
 //   turn 2:             products  O_B += V P_B (the keys before), S_B (these)
 //                       vector    softmax of S_A (these)
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t tiles) {
-  constexpr int KT = 32 * NW, KBS = NW, RT = 64 * NW;
+//
+// KS: that many waves share 64 rows, each with its part of every step's keys, and
+// add up in LDS at the end: a tile's time is that of one wave's keys, and where
+// there are few tiles nothing else fills the card.
+template <int D, int KS>
+__global__ __launch_bounds__(256, 1) void prompt_kernel(Prompt p, int64_t tiles) {
+  constexpr int NW = 4, KT = 32 * NW, KBS = NW / KS, RT = 64 * NW / KS;
   constexpr int STEPS = D / 16, DT = D / 32;
   using Im = Image<D>;
   constexpr int BUF = Im::bytes(KT), KB32 = Im::bytes(32), KB16 = KB32 / 2, KB8 = KB32 / 4;
   constexpr int LOADS = KT * D * 2 / 1024;                  // KBs of a step's keys
-  __shared__ __align__(16) uint8_t ksh[2 * BUF];
-  __shared__ __align__(16) uint8_t vsh[2 * BUF];
-  __shared__ uint32_t bad[2][KBS];                          // of masked steps: keys whose values are not finite
+  __shared__ __align__(16) uint8_t lds[4 * BUF];
+  uint8_t* const ksh = lds;
+  uint8_t* const vsh = lds + 2 * BUF;
+  __shared__ uint32_t bad[2][NW];                           // of masked steps: keys whose values are not finite
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
+  const int part = wave % KS, row_wave = wave / KS;         // the wave's share of the keys, and its rows
   const int h = blockIdx.x % p.heads;
   for (int64_t j = blockIdx.x / p.heads; j < tiles; j += gridDim.x / p.heads) {
   const PromptTile w = tile_of<RT>(p, j, lane);
@@ -212,7 +228,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
   // infinity or a NaN, so they become zeros, and their key's logit NaN for the
   // rows that do see it.
   auto clean = [&](int buf) {
-    if (tid < KBS) bad[buf ^ 1][tid] = 0;
+    if (tid < NW) bad[buf ^ 1][tid] = 0;
     for (int i = tid; i < KT * D / 8; i += 64 * NW) {
       u32x4_t* at = reinterpret_cast<u32x4_t*>(vsh + buf * BUF + i / 64 * Im::PITCH + i % 64 * 16);
       u32x4_t v = *at;
@@ -229,14 +245,14 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
       }
     }
   };
-  if (tid < 2 * KBS) bad[tid / KBS][tid % KBS] = 0;
+  if (tid < 2 * NW) bad[tid / NW][tid % NW] = 0;
   fetch(0, 0, 0, SHARE);
 
   bf16x8_t qf[2][STEPS];
   int lim[2], limmin = k1;
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    int row = w.row0 + wave * 64 + n * 32 + col;
+    int row = w.row0 + row_wave * 64 + n * 32 + col;
     row = row < w.rows ? row : w.rows - 1;                  // behind the last row it is repeated, and not stored
     const int tok = row / p.group, g = row - tok * p.group;
     const uint16_t* q = p.Q + (int64_t)(w.s0 + tok) * p.q_stride + (int64_t)(h * p.group + g) * D + 8 * hh;
@@ -245,7 +261,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     for (int s = 0; s < STEPS; ++s) qf[n][s] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(q + 16 * s));
   }
   {
-    int row = w.row0 + wave * 64;                           // the wave's first row sees least
+    int row = w.row0 + row_wave * 64;                           // the wave's first row sees least
     row = row < w.rows ? row : w.rows - 1;
     limmin = row / p.group + 1;
   }
@@ -286,12 +302,12 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
   }
 
   // a lane's keys: row col of 32, values 16 s + 8 hh .. + 7
-  const uint8_t* const kread = ksh + Im::at(col, hh);
+  const uint8_t* const kread = ksh + part * KBS * KB32 + Im::at(col, hh);
   // a transposing read: 16 lanes take 4 keys and 16 coordinates; lane i brings 8
   // bytes of key i / 4 and gets coordinate i of all four.  Its 4 coordinates are
   // chosen so that a lane's results are runs of 8 (see the stores).
   const int li = lane & 15, dh = (lane >> 4) & 1;
-  const uint8_t* const vread = vsh + Im::at(4 * hh + (li >> 2), 2 * dh + (li & 1)) + ((li >> 1) & 1) * 8;
+  const uint8_t* const vread = vsh + part * KBS * KB32 + Im::at(4 * hh + (li >> 2), 2 * dh + (li & 1)) + ((li >> 1) & 1) * 8;
   bf16x8_t kf[STEPS], vf[2][DT];
   auto read_k = [&](int buf, int kb) {
 #pragma unroll
@@ -393,8 +409,8 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int t = 0; t < DT; ++t) vf[s][t] = bf16x8_t{};
-  int buf = 0;
-  uint32_t before = 0;                     // keys of the 32 before whose values are not finite
+  int buf = 0, prev = 0;                   // prev: the first of the 32 keys before
+  uint32_t before = 0;                     // those of them whose values are not finite
   for (int key = 0; key < k1; key += KT, buf ^= 1) {
     const bool more = key + KT < k1;
     uint32_t nans[KBS];
@@ -402,15 +418,16 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     for (int i = 0; i < KBS; ++i) nans[i] = 0;
     if (key + KT > sure) {
 #pragma unroll
-      for (int i = 0; i < KBS; ++i) nans[i] = __builtin_amdgcn_readfirstlane(bad[buf][i]);
+      for (int i = 0; i < KBS; ++i) nans[i] = __builtin_amdgcn_readfirstlane(bad[buf][part * KBS + i]);
     }
 #pragma unroll
     for (int kb = 0; kb < KBS; ++kb) {
-      const int k = key + 32 * kb;
-      if (kb > 0 && k >= k1) break;        // the last step's keys may end early
+      const int k = key + 32 * (part * KBS + kb);
+      if ((KS > 1 || kb > 0) && k >= k1) break;             // the last step's keys may end early
       if (more) fetch(key + KT, buf ^ 1, kb * SHARE / KBS, (kb + 1) * SHARE / KBS);
-      bounds(B{}, k - 32, before);
+      bounds(B{}, prev, before);
       before = nans[kb];
+      prev = k;
       turn(B{}, std::integral_constant<int, 1>{}, none, none);
       bounds(A{}, k, before);
       turn(A{}, std::integral_constant<int, 2>{}, [&] { if (kb + 1 < KBS) read_k(buf, kb + 1); }, [&] { read_v(buf, kb); });
@@ -426,7 +443,7 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     }
   }
   // what is left: the last keys' products and block B's softmax
-  bounds(B{}, (k1 + 31) / 32 * 32 - 32, before);
+  bounds(B{}, prev, before);
   turn(B{}, std::integral_constant<int, 1>{}, none, none);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
@@ -434,12 +451,53 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
     for (int t = 0; t < DT; ++t)
       acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[s][t], __builtin_bit_cast(bf16x8_t, pw[1][s]), acc[1][t], 0, 0, 0);
 
+  if constexpr (KS > 1) {
+    // every lane adds what the same lane of the waves that share its rows holds
+    constexpr int LANE = 2 * DT * 4, WAVE = (LANE + 1) * 1024;   // 16-byte pieces of a lane, bytes of a wave
+    static_assert(NW / KS * (KS - 1) * WAVE <= 4 * BUF, "the sums fit where the keys were");
+    auto at = [&](int o) { return lds + (row_wave * (KS - 1) + o - 1) * WAVE + lane * 16; };
+    if (part > 0) {                        // the last step's barrier has freed the LDS
+      uint8_t* to = at(part);
+#pragma unroll
+      for (int i = 0; i < LANE; ++i) {
+        const f32x16_t& v = acc[i / (4 * DT)][i / 4 % DT];
+        *reinterpret_cast<f32x4_t*>(to + i * 1024) = f32x4_t{v[4 * (i % 4)], v[4 * (i % 4) + 1], v[4 * (i % 4) + 2], v[4 * (i % 4) + 3]};
+      }
+      *reinterpret_cast<f32x4_t*>(to + LANE * 1024) = f32x4_t{m[0], m[1], l[0], l[1]};
+    }
+    __syncthreads();
+    if (part == 0) {
+      for (int o = 1; o < KS; ++o) {
+        const uint8_t* from = at(o);
+        const f32x4_t ml = *reinterpret_cast<const f32x4_t*>(from + LANE * 1024);
+        float fa[2], fb[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float M = fmaxf(m[n], ml[n]);
+          fa[n] = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[n] - M);
+          fb[n] = ml[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[n] - M);
+          m[n] = M;
+          l[n] = l[n] * fa[n] + ml[2 + n] * fb[n];          // a NaN sum (a NaN key was seen) stays one
+        }
+#pragma unroll
+        for (int i = 0; i < LANE; ++i) {
+          const f32x4_t u = *reinterpret_cast<const f32x4_t*>(from + i * 1024);
+          f32x16_t& v = acc[i / (4 * DT)][i / 4 % DT];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[4 * (i % 4) + e] = v[4 * (i % 4) + e] * fa[i / (4 * DT)] + u[e] * fb[i / (4 * DT)];
+        }
+      }
+    }
+    __syncthreads();
+    if (part > 0) continue;
+  }
   // Register i of tile t is the tile's row 8 (i / 4) + 4 hh + i % 4, which holds
   // coordinate 32 t + 16 (i / 8) + 8 hh + i % 8 by the choice above.
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     l[n] += __shfl_xor(l[n], 32);
-    const int row = w.row0 + wave * 64 + n * 32 + col;
+    const int row = w.row0 + row_wave * 64 + n * 32 + col;
     if (row >= w.rows) continue;
     const int tok = row / p.group, g = row - tok * p.group;
     const float inv = l[n] == 0.f ? 0.f : 1.0f / l[n];
@@ -470,15 +528,49 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(Prompt p, int64_t ti
 
 }  // namespace
 
+namespace {
+
+// How many waves share a tile's rows, from sizes alone (the lengths are the
+// device's): the one with the least time by what was measured, in us: starting
+// and ending a tile, 8, 10 and 13 for 1, 2 and 4 waves, once for every 256
+// workgroups; and a step of 128 keys, 4.2 (2.1 for heads of 64), over the waves
+// for the longest tile, or all tiles' over the card.  8 heads, 1 / 2 / 4 waves:
+// one prompt of 77 tokens, group 8, 11.0 / 12.0 / 13.0; of 300 18.1 / 16.5 / 25.3;
+// of 2000 83 / 111 / 179; of 4096, group 1, 129 / 81 / 71.
+int sharers(const Prompt& p) {
+  const double tiles = ((double)p.T * p.group / 256 + 0.5 * p.B) * p.heads, len = (double)p.T / p.B;
+  const double step = p.head_dim == 128 ? 4.2 : 2.1, spread = tiles * len / (256.0 * 256.0);
+  const double fixed[3] = {8, 10, 13};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const double wgs = tiles * (1 << i), longest = len / (128 << i);
+    const double t = fixed[i] * (wgs > 256 ? wgs / 256 : 1) + step * (longest > spread ? longest : spread);
+    if (i == 0 || t < least) { best = i; least = t; }
+  }
+  return 1 << best;
+}
+
+}  // namespace
+
 size_t prompt_ws_bytes(int head_dim, int heads, int group, int64_t B, int64_t T) { return 0; }
 
 hipError_t launch_prompt(const Prompt& p, void* ws, hipStream_t st) {
-  constexpr int NW = 4;
-  const int64_t tiles = (int64_t)p.T * p.group / (64 * NW) + p.B;
+  const int ks = sharers(p);
+  const int64_t tiles = (int64_t)p.T * p.group / (256 / ks) + p.B;
   const int64_t most = (1 << 22) / p.heads;
   const dim3 grid((unsigned)((tiles < most ? tiles : most) * p.heads));
-  if (p.head_dim == 128) hipLaunchKernelGGL((prompt_kernel<128, NW>), grid, dim3(64 * NW), 0, st, p, tiles);
-  else hipLaunchKernelGGL((prompt_kernel<64, NW>), grid, dim3(64 * NW), 0, st, p, tiles);
+#define GO(D, KS) hipLaunchKernelGGL((prompt_kernel<D, KS>), grid, dim3(256), 0, st, p, tiles)
+#define GO_D(D)            \
+  do {                     \
+    if (ks == 1) GO(D, 1); \
+    else if (ks == 2) GO(D, 2); \
+    else GO(D, 4);         \
+  } while (0)
+  if (p.head_dim == 128) GO_D(128);
+  else GO_D(64);
+#undef GO_D
+#undef GO
   return hipGetLastError();
 }
 

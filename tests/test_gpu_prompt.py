@@ -117,6 +117,51 @@ def test_rows_before_a_value_that_is_not_finite(gpu, D, H, G, value, which, at):
         assert bool(got[sees].isnan().all())
 
 
+# sizes whose tiles' rows one wave has to itself (many heads), or shares with one other or three (few heads, long)
+SHARED = [(64, 32, 8, [300, 0, 50]), (128, 24, 6, [280, 1, 60]), (128, 2, 4, [400, 90]), (64, 1, 1, [1500, 200]), (128, 1, 2, [1, 1700])]
+
+
+@pytest.mark.parametrize("D,H,G,lens", SHARED)
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_one_or_several_waves(gpu, D, H, G, lens, out_dtype):
+    starts = starts_of(lens, 2)
+    T = starts[-1] + 3
+    Q, K, V = qkv(T, H * G, H, D, 30)
+    out = torch.full((T, H * G, D), 3.0, dtype=out_dtype, device=DEV)
+    gpu.qprompt_attend(Q, K, V, i32(starts), out=out)
+    verify(out, Q, K, V, starts)
+    assert bool((out[:2] == 3.0).all()) and bool((out[-3:] == 3.0).all())
+
+
+@pytest.mark.parametrize("D,H,G,lens", SHARED)
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("at", [0, 31, 100, 128, 250])
+def test_values_that_are_not_finite_by_waves(gpu, D, H, G, lens, value, which, at):
+    starts = starts_of(lens)
+    T = starts[-1]
+    Q, K, V = qkv(T, H * G, H, D, 31)
+    clean = gpu.qprompt_attend(Q, K, V, i32(starts))
+    (K if which == "k" else V)[at, H - 1, 5] = value
+    got = gpu.qprompt_attend(Q, K, V, i32(starts))
+    sees = torch.zeros((T, H * G), dtype=torch.bool, device=DEV)
+    sees[at:next(s for s in starts if s > at), (H - 1) * G:] = True
+    assert torch.equal(got[~sees], clean[~sees])
+    if which == "v":
+        assert bool((~got[sees][:, 5].isfinite()).all())
+    elif math.isnan(value):
+        assert bool(got[sees].isnan().all())
+
+
+@pytest.mark.parametrize("D,H,G,lens", SHARED)
+def test_rising_logits_by_waves(gpu, D, H, G, lens):
+    starts = starts_of(lens)
+    Q, K, V = qkv(starts[-1], H * G, H, D, 32)
+    Q[..., 0] = 8.0
+    K[..., 0] = (torch.arange(starts[-1], device=DEV) % 300).bfloat16()[:, None]
+    verify(gpu.qprompt_attend(Q, K, V, i32(starts), scale=0.5, out_dtype=torch.float32), Q, K, V, starts, 0.5)
+
+
 @pytest.mark.parametrize("lens", [[300], [40, 500, 3]])
 def test_the_same_every_time(gpu, lens):
     starts = starts_of(lens)
