@@ -105,7 +105,8 @@ int qprompt_attend_ws(int head_dim, int q_heads, int kv_heads, int64_t B, int64_
  * of one token contiguous, strides in elements between tokens, 16-byte aligned
  * and a multiple of 16 bytes.  out overlaps no input.  scale is finite and of
  * magnitude 2^45 at most (else Q_EUNSUPPORTED); |scale| sum_i |Q_i K_i| has to
- * stay below 2^120 and sum_i |Q_i K_i| below 2^126.  1 <= B <= 65536,
+ * stay below 2^120, sum_i |Q_i K_i| below 2^126, and |V| times the keys of a
+ * sequence below 2^118.  1 <= B <= 65536,
  * 1 <= T <= 2^27, T * q_heads / kv_heads at most 2^30.
  * A row that sees a key or value that holds an infinity or a NaN comes out as
  * NaN or infinite, in that component at least; the rows before it do not.

@@ -90,6 +90,17 @@ def test_ranks_of_their_own(gpu, starts):
     c.verify(c.run(gpu))
 
 
+@pytest.mark.parametrize("B", [300, 5000])
+@pytest.mark.parametrize("long", [0, 700])
+def test_many_requests(gpu, B, long):
+    """Requests of 0 to 4 rows, one of them long."""
+    starts = [0]
+    for b in range(B):
+        starts.append(starts[-1] + b % 5 + (long * B // 10 if b == 77 else 0))
+    c = Case(72, 50, 16, 9, [(b * 3) % 11 - 1 for b in range(B)], starts, starts[-1], seed=16)
+    c.verify(c.run(gpu))
+
+
 def test_ids_outside_the_set(gpu):
     c = Case(64, 40, 8, 3, [-1, 3, 2 ** 31 - 1, -2 ** 31, 2], seed=6)
     got = c.run(gpu)

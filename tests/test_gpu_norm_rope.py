@@ -71,6 +71,18 @@ def test_ragged_rows(gpu, new, lead, tail):
     assert bool((qo[nobody] == 9.0).all()) and bool((ko[nobody] == 9.0).all())
 
 
+@pytest.mark.parametrize("B", [300, 5000])
+def test_many_sequences(gpu, B):
+    new = [b % 4 for b in range(B)]
+    starts = [0]
+    for n in new:
+        starts.append(starts[-1] + n)
+    lens = [n + (b * 37) % 1000 for b, n in enumerate(new)]
+    Q, K, fr = randn((starts[-1], 9, 64), 1), randn((starts[-1], 1, 64), 2), freqs_of(32)
+    outs = gpu.qnorm_rope(Q, K, i32(lens), i32(starts), freqs=fr, pairs=True)
+    verify(outs, (Q, K), (None, None), 1e-6, fr, True, positions(lens, starts, starts[-1], 0))
+
+
 @pytest.mark.parametrize("offset", [0, 2 ** 20 - 1, 2 ** 31 - 1, -(2 ** 31) + 1])
 def test_far_positions(gpu, offset):
     """Angles of positions of 31 bits; lens shorter than the new rows give negative ones."""

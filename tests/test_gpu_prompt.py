@@ -68,6 +68,17 @@ def test_more_tiles_than_workgroups(gpu):
     verify(gpu.qprompt_attend(Q, K, V, i32(starts)), Q, K, V, starts)
 
 
+@pytest.mark.parametrize("B", [64, 65, 256, 257, 1000])
+def test_many_sequences(gpu, B):
+    lens = [(b * 7) % 23 + (130 if b % 50 == 3 else 0) for b in range(B)]
+    starts = starts_of(lens, 1)
+    Q, K, V = qkv(starts[-1] + 2, 4, 2, 64, 33)
+    out = torch.full((starts[-1] + 2, 4, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    gpu.qprompt_attend(Q, K, V, i32(starts), out=out)
+    verify(out, Q, K, V, starts)
+    assert bool((out[:1] == 3.0).all()) and bool((out[-2:] == 3.0).all())
+
+
 @pytest.mark.parametrize("scale", [0.0, 1e-30, 0.01, -0.2, 1.0, 30.0])
 def test_scales(gpu, scale):
     Q, K, V = qkv(150, 4, 2, 64, 4)
