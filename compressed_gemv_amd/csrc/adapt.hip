@@ -64,7 +64,9 @@ AdaptPlan plan_adapt(bool segments, int64_t seqs, int64_t T, int64_t K, int64_t 
   s = s > 32 ? 32 : s;
   p.kchunk = (int)(ceil_div(ceil_div(K, s), wide ? 256 : 512) * (wide ? 256 : 512));
   p.splits = (int)ceil_div(K, p.kchunk);
-  int64_t c = ceil_div(N * tiles, 1024);
+  // every workgroup adds up h again (16 single rows, N = 28672: 256 outputs each 26 us,
+  // 512 19.5, 1024 14.8; 5 prompts, N = 8192: 256 152 us, 768 149, 1024 160)
+  int64_t c = ceil_div(N * tiles, segments ? 1024 : 512);
   c = ceil_div(c, 256) * 256;
   p.nchunk = (int)(c < 256 ? 256 : (c > 1024 ? 1024 : c));
   return p;
@@ -375,7 +377,8 @@ __global__ __launch_bounds__(256) void adapt_down_tall_kernel(Adapt p, int kchun
 // One workgroup: a tile and a range of N.  h (all splits added, times scale)
 // lies in LDS as bf16, hi and lo: 32-deep blocks of hi, then those of lo, or for
 // ranks up to 16 both in one block, so that one product does.  A wave forms 64
-// outputs of 16 RT rows at a time: the four 16 x 16 products of a row tile give a
+// outputs of 16 rows at a time (of 32 with twice the registers: the call 149 -> 156
+// us for 5 prompts of 77 .. 1500 rows): the four 16 x 16 products of a row tile give a
 // lane four neighbouring outputs of a row each (fp32: 16-byte accesses), or,
 // with the outputs of two products interleaved, eight (bf16).
 struct UpRows {
@@ -419,35 +422,32 @@ struct UpCols {
   }
 };
 
-template <bool F32, int RT>
+template <bool F32>
 __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpRows& u, const UpCols<F32>& b, int row_tile, int lane) {
   const int r16 = lane & 15, g = lane >> 4, n0 = b.n0, n1 = b.n1;
   const bool both = u.lo_at == 16;         // hi and lo in one block
+  const int at = 16 * row_tile + r16;
+  const bool on = at < u.n;
+  const int64_t row = t.row0 + (on ? u.rows[at] : 0);
+  const float* const yf = static_cast<const float*>(p.y) + (F32 ? row * p.y_stride + n0 : 0);
+  const uint16_t* const yh = static_cast<const uint16_t*>(p.y) + (F32 ? 0 : row * p.y_stride + n0);
   // y comes while the products run
-  int64_t row[RT];
-  f32x4_t yv[RT][4];
-  u32x4_t yh[RT][2];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int at = 16 * (row_tile + i) + r16;
-    row[i] = at < u.n ? t.row0 + u.rows[at] : -1;
-    if (row[i] < 0) continue;
-    const int64_t yo = row[i] * p.y_stride + n0;
+  f32x4_t y4[4];
+  u32x4_t y8[2];
+  if (on) {
     if constexpr (F32) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n0 + 16 * c + 4 * g + 4 <= n1) yv[i][c] = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p.y) + yo + 16 * c + 4 * g);
+        if (n0 + 16 * c + 4 * g + 4 <= n1) y4[c] = *reinterpret_cast<const f32x4_any*>(yf + 16 * c + 4 * g);
     } else {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        if (n0 + 32 * c + 8 * g + 8 <= n1) yh[i][c] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p.y) + yo + 32 * c + 8 * g);
+        if (n0 + 32 * c + 8 * g + 8 <= n1) y8[c] = *reinterpret_cast<const u32x4_any*>(yh + 32 * c + 8 * g);
     }
   }
-  f32x4_t acc[RT][4];
+  f32x4_t acc[4];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int J = 0; J < u.blocks; ++J) {
     u32x4_t bv[4];
     if (J == 0) {
@@ -457,62 +457,53 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
       b.load(p.rank, J, lane, bv);
     }
     b.mask(J, lane, bv);
+    const uint16_t* hr = u.h + at * u.pitch + 32 * J + 8 * g;
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(hr);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint16_t* hr = u.h + (16 * (row_tile + i) + r16) * u.pitch + 32 * J + 8 * g;
-      const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(hr);
+    for (int c = 0; c < 4; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(hi), acc[c], 0, 0, 0);
+    if (!both) {
+      const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(hr + u.lo_at);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(hi), acc[i][c], 0, 0, 0);
-      if (!both) {
-        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(hr + u.lo_at);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(lo), acc[i][c], 0, 0, 0);
-      }
+      for (int c = 0; c < 4; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(lo), acc[c], 0, 0, 0);
     }
   }
+  if (!on) return;
+  const int64_t to = row * p.o_stride + n0;
+  if constexpr (F32) {
+    float* o = static_cast<float*>(p.out) + to;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if (row[i] < 0) continue;
-    const int64_t yo = row[i] * p.y_stride + n0, oo = row[i] * p.o_stride + n0;
-    if constexpr (F32) {
-      const float* y = static_cast<const float*>(p.y) + yo;
-      float* o = static_cast<float*>(p.out) + oo;
+    for (int c = 0; c < 4; ++c) {
+      const int n = 16 * c + 4 * g;
+      if (n0 + n + 4 <= n1) {
+        *reinterpret_cast<f32x4_any*>(o + n) = y4[c] + acc[c];
+      } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = 16 * c + 4 * g;
-        if (n0 + n + 4 <= n1) {
-          *reinterpret_cast<f32x4_any*>(o + n) = yv[i][c] + acc[i][c];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (n0 + n + k < n1) o[n + k] = y[n + k] + acc[i][c][k];
-        }
+        for (int k = 0; k < 4; ++k)
+          if (n0 + n + k < n1) o[n + k] = yf[n + k] + acc[c][k];
       }
-    } else {
-      const uint16_t* y = static_cast<const uint16_t*>(p.y) + yo;
-      uint16_t* o = static_cast<uint16_t*>(p.out) + oo;
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + to;
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        const int n = 16 * c + 8 * g;
-        if (n0 + n + 8 <= n1) {
-          const u32x4_t v = yh[i][c / 2];
-          u32x4_t w;
+    for (int c = 0; c < 4; c += 2) {
+      const int n = 16 * c + 8 * g;
+      if (n0 + n + 8 <= n1) {
+        const u32x4_t v = y8[c / 2];
+        u32x4_t w;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = cvt_pk_bf16(bf16_lo_to_f32(v[k]) + acc[i][c + k / 2][2 * (k % 2)],
-                               bf16_hi_to_f32(v[k]) + acc[i][c + k / 2][2 * (k % 2) + 1]);
-          *reinterpret_cast<u32x4_any*>(o + n) = w;
-        } else {
+        for (int k = 0; k < 4; ++k)
+          w[k] = cvt_pk_bf16(bf16_lo_to_f32(v[k]) + acc[c + k / 2][2 * (k % 2)], bf16_hi_to_f32(v[k]) + acc[c + k / 2][2 * (k % 2) + 1]);
+        *reinterpret_cast<u32x4_any*>(o + n) = w;
+      } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (n0 + n + k < n1) o[n + k] = (uint16_t)cvt_pk_bf16(bf16_bits_to_f32(y[n + k]) + acc[i][c + k / 4][k % 4], 0.f);
-        }
+        for (int k = 0; k < 8; ++k)
+          if (n0 + n + k < n1) o[n + k] = (uint16_t)cvt_pk_bf16(bf16_bits_to_f32(yh[n + k]) + acc[c + k / 4][k % 4], 0.f);
       }
     }
   }
 }
 
-template <bool F32, int RT>
+template <bool F32>
 __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int splits, int nchunk, int R) {
   __shared__ uint8_t rows[kTile];
   extern __shared__ __align__(16) uint16_t hbuf[];
@@ -551,7 +542,7 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
     u.lo_at = deep;
     u.blocks = both ? 1 : deep / 32;
     u.pitch = 2 * deep + 8;                // 16 bytes more: neighbouring rows in other banks
-    const int tall = (t.n + 16 * RT - 1) / (16 * RT) * (16 * RT), kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
+    const int tall = (t.n + 15) / 16 * 16, kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
     const float scale = p.scales[t.a];
     UpCols<F32> cols;
     const int mine = first + 64 * wave;
@@ -585,7 +576,7 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
     const int tiles16 = tall / 16;
     for (int n0 = mine; n0 < last; n0 += 256) {
       if (n0 != mine) cols.begin(p, t, n0, last - n0 < 64 ? last : n0 + 64, u.held, lane);
-      for (int i = 0; i < tiles16; i += RT) up_tile<F32, RT>(p, t, u, cols, i, lane);
+      for (int i = 0; i < tiles16; ++i) up_tile<F32>(p, t, u, cols, i, lane);
     }
   }
 }
@@ -611,18 +602,11 @@ hipError_t launch_adapt(const Adapt& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int deep = p.rank <= 16 ? 16 : (p.rank + 31) / 32 * 32;
-  const int64_t tall = p.T < kTile ? ceil_div(p.T, 32) * 32 : kTile;
+  const int64_t tall = p.T < kTile ? ceil_div(p.T, 16) * 16 : kTile;
   const size_t lds = (size_t)tall * (2 * deep + 8) * 2;
   const dim3 up((unsigned)(a.blocks * a.slots), (unsigned)ceil_div(p.N, a.nchunk));
-#define UP(F, RT) hipLaunchKernelGGL((adapt_up_kernel<F, RT>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R)
-  if (p.f32) {
-    if (p.starts) UP(true, 2);
-    else UP(true, 1);
-  } else {
-    if (p.starts) UP(false, 2);
-    else UP(false, 1);
-  }
-#undef UP
+  if (p.f32) hipLaunchKernelGGL((adapt_up_kernel<true>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
+  else hipLaunchKernelGGL((adapt_up_kernel<false>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
   return hipGetLastError();
 }
 
