@@ -26,7 +26,7 @@ __all__ = [
     "qstream_read", "qgemm_prefill_ws", "qgemm_prefill", "Q_F32", "Q_BF16", "Q_FMT_GROUP", "Q_FMT_BINLR",
     "qcache_sizes", "make_qcache", "qcache_write", "qcache_read", "qcache_attend_ws", "qcache_attend",
     "qcache_attend_shared",
-    "make_qadapters", "qadapt_ws", "qadapt", "qnorm_rope", "qprompt_attend_ws", "qprompt_attend",
+    "make_qadapters", "qadapt_ws", "qadapt", "qnorm_rope", "qprompt_attend",
 ]
 
 Q_OK, Q_EINVAL, Q_EALIGN, Q_EUNSUPPORTED, Q_ERANGE, Q_EWORKSPACE, Q_EHIP = 0, -1, -2, -3, -4, -5, -6
@@ -153,8 +153,7 @@ def load() -> ctypes.CDLL:
         "qadapt_ws": (I32, [AD, I64, I64, SZ]),
         "qadapt": (I32, [AD, I64, I64, P, P, P, I64, P, I64, P, I64, I32, P, U64, P]),
         "qnorm_rope": (I32, [RP, I64, I64, P, P, P, I64, P, I64, I32, P, I64, P, I64, I32, P]),
-        "qprompt_attend_ws": (I32, [I32, I32, I32, I64, I64, SZ]),
-        "qprompt_attend": (I32, [I32, I32, I32, I64, I64, P, P, I64, P, I64, P, I64, F32, P, I64, I32, P, U64, P]),
+        "qprompt_attend": (I32, [I32, I32, I32, I64, I64, P, P, I64, P, I64, P, I64, F32, P, I64, I32, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -1164,24 +1163,14 @@ def _rope_rows(t, out, T: int, D: int, dtype, out_dtype, what: str):
     return heads, stride, o_stride
 
 
-@functools.lru_cache(maxsize=1024)
-def qprompt_attend_ws(head_dim: int, q_heads: int, kv_heads: int, B: int, T: int) -> int:
-    """Workspace bytes for B packed prompts of T tokens in all."""
-    n = ctypes.c_size_t()
-    _check(load().qprompt_attend_ws(head_dim, q_heads, kv_heads, B, T, ctypes.byref(n)), "qprompt_attend_ws")
-    return n.value
-
-
 def qprompt_attend(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts=None, scale: Optional[float] = None,
-                   out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None,
-                   stream=None):
+                   out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
     """out [T][q_heads][D] (bf16 or fp32): causal attention of packed prompts over
     their own keys and values: Q bf16 [T][q_heads][D], K and V bf16
     [T][kv_heads][D], sequence b's tokens are rows starts[b] .. starts[b+1]-1
     (int32 [B+1]; one sequence of T tokens without it).  scale: D^-1/2 by
-    default.  Calls that may overlap need a workspace each.  An output that is
-    allocated here belongs to `stream`: another stream waits for it first; rows
-    that no sequence owns are not written."""
+    default.  An output that is allocated here belongs to `stream`: another
+    stream waits for it first; rows that no sequence owns are not written."""
     if K.dim() != 3 or Q.dim() != 3:
         raise ValueError(f"Q and K must be [T][heads][D], got shapes {tuple(Q.shape)} and {tuple(K.shape)}")
     T, kv_heads, D = K.shape
@@ -1205,19 +1194,13 @@ def qprompt_attend(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts=Non
         o_stride = _cache_rows(out, q_heads, D, _OUT, "out")
         if out.shape[0] != T:
             raise ValueError(f"out: {out.shape[0]} rows, Q has {T}")
-    _here(place, starts, ws)
+    _here(place, starts)
     _on_device(place, False, Q, K, V, out)
     if out is None:
         out = _fresh(place, stream, (T, q_heads, D), out_dtype, True)
     if T == 0:
         return out
-    need = qprompt_attend_ws(D, q_heads, kv_heads, B, T)
-    if ws is not None:
-        _need_bytes(ws, need, "ws")
-    elif need:
-        ws = _fresh(place, stream, need, torch.uint8, False)
     _call_on(place, stream, "qprompt_attend", load().qprompt_attend, D, q_heads, kv_heads, B, T, sp, Q.data_ptr(), strides[0],
              K.data_ptr(), strides[1], V.data_ptr(), strides[2], D ** -0.5 if scale is None else scale, out.data_ptr(),
-             o_stride, Q_F32 if out.dtype == torch.float32 else Q_BF16, None if ws is None else ws.data_ptr(),
-             0 if ws is None else _nbytes(ws))
+             o_stride, Q_F32 if out.dtype == torch.float32 else Q_BF16)
     return out

@@ -58,7 +58,6 @@ struct Prompt {
   void* out;
   bool out_f32;
 };
-size_t prompt_ws_bytes(int head_dim, int heads, int group, int64_t B, int64_t T);
-hipError_t launch_prompt(const Prompt& p, void* ws, hipStream_t st);
+hipError_t launch_prompt(const Prompt& p, hipStream_t st);
 
 }  // namespace qg

@@ -160,22 +160,14 @@ int qnorm_rope(const qrope* p, int64_t B, int64_t T, const int32_t* lens, const 
   return hip_status(qg::launch_norm_rope(r, stream));
 }
 
-int qprompt_attend_ws(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T, size_t* ws_bytes) {
-  int st = heads_ok(head_dim, q_heads, kv_heads);
-  if (st != Q_OK) return st;
-  if (!ws_bytes || B > kMaxSeqs) return Q_EINVAL;
-  if ((st = batch_ok(B, T)) != Q_OK) return st;
-  if (T * (q_heads / kv_heads) > ((int64_t)1 << 30)) return Q_EUNSUPPORTED;
-  *ws_bytes = qg::prompt_ws_bytes(head_dim, kv_heads, q_heads / kv_heads, B, T);
-  return Q_OK;
-}
-
 int qprompt_attend(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T, const int32_t* starts, const void* Q,
                    int64_t q_stride, const void* K, int64_t k_stride, const void* V, int64_t v_stride, float scale,
-                   void* out, int64_t o_stride, int out_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
-  size_t need = 0;
-  int st = qprompt_attend_ws(head_dim, q_heads, kv_heads, B, T, &need);
+                   void* out, int64_t o_stride, int out_dtype, hipStream_t stream) {
+  int st = heads_ok(head_dim, q_heads, kv_heads);
   if (st != Q_OK) return st;
+  if (B > kMaxSeqs) return Q_EINVAL;
+  if ((st = batch_ok(B, T)) != Q_OK) return st;
+  if (T * (q_heads / kv_heads) > ((int64_t)1 << 30)) return Q_EUNSUPPORTED;
   if ((!starts && B != 1) || !isfinite(scale) || !float_dtype(out_dtype)) return Q_EINVAL;
   if (fabsf(scale) > 0x1p45f) return Q_EUNSUPPORTED;
   if (!aligned(starts, 4)) return Q_EALIGN;
@@ -184,8 +176,6 @@ int qprompt_attend(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T
   if ((st = rows_ok(K, k_stride, kw, 2)) != Q_OK) return st;
   if ((st = rows_ok(V, v_stride, kw, 2)) != Q_OK) return st;
   if ((st = rows_ok(out, o_stride, qw, size_of(out_dtype))) != Q_OK) return st;
-  if (need && (!ws || ws_bytes < need)) return Q_EWORKSPACE;
-  if (!aligned(ws, 16)) return Q_EALIGN;
   qg::Prompt p;
   p.head_dim = head_dim;
   p.heads = kv_heads;
@@ -203,7 +193,7 @@ int qprompt_attend(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T
   p.scale = scale;
   p.out = out;
   p.out_f32 = out_dtype == Q_F32;
-  return hip_status(qg::launch_prompt(p, ws, stream));
+  return hip_status(qg::launch_prompt(p, stream));
 }
 
 }  // extern "C"

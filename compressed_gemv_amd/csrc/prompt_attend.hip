@@ -553,9 +553,7 @@ int sharers(const Prompt& p) {
 
 }  // namespace
 
-size_t prompt_ws_bytes(int head_dim, int heads, int group, int64_t B, int64_t T) { return 0; }
-
-hipError_t launch_prompt(const Prompt& p, void* ws, hipStream_t st) {
+hipError_t launch_prompt(const Prompt& p, hipStream_t st) {
   const int ks = sharers(p);
   const int64_t tiles = (int64_t)p.T * p.group / (256 / ks) + p.B;
   const int64_t most = (1 << 22) / p.heads;

@@ -10,7 +10,7 @@
  * reentrant).
  *
  * Rows: T rows of a batch of B sequences (or requests).  starts[B+1]
- * (nondecreasing, device): sequence b owns rows starts[b] .. starts[b+1]-1.
+ * (nondecreasing, starts[B] <= T, device): sequence b owns rows starts[b] .. starts[b+1]-1.
  * Rows that no sequence owns (below starts[0], at or behind starts[B]) are
  * left as they were.  Everything that depends on device data is read on the
  * device, so a captured call follows it.
@@ -93,10 +93,7 @@ int qnorm_rope(const qrope* p, int64_t B, int64_t T, const int32_t* lens, const 
                int64_t ko_stride, int out_dtype, hipStream_t stream);
 
 /* --------------------------------------------------------- whole prompts
- * Workspace bytes of qprompt_attend (host only). */
-int qprompt_attend_ws(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T, size_t* ws_bytes);
-
-/* Causal attention of B packed prompts over their own, unquantized keys and
+ * Causal attention of B packed prompts over their own, unquantized keys and
  * values: for row t of a sequence that begins at row s,
  *   out[t][hq][:] = sum_{j = s..t} softmax_j(scale <Q[t][hq][:], K[j][hk][:]>) V[j][hk][:],
  * hk = hq / (q_heads / kv_heads); q_heads a multiple of kv_heads, at most 64
@@ -112,12 +109,10 @@ int qprompt_attend_ws(int head_dim, int q_heads, int kv_heads, int64_t B, int64_
  * NaN or infinite, in that component at least; the rows before it do not.
  * Precision: products of bf16 values in fp32, sums, maxima and the softmax
  * statistics fp32, weights rounded to bf16 before they meet V, also where the
- * output is fp32.
- * ws: device, 16-byte aligned, >= the qprompt_attend_ws value; calls that may
- * overlap need one each. */
+ * output is fp32.  No workspace: calls may overlap. */
 int qprompt_attend(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T, const int32_t* starts, const void* Q,
                    int64_t q_stride, const void* K, int64_t k_stride, const void* V, int64_t v_stride, float scale,
-                   void* out, int64_t o_stride, int out_dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+                   void* out, int64_t o_stride, int out_dtype, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -84,12 +84,9 @@ void norm(int D, int hq, int hk, int64_t B, int64_t T, bool starts, bool must) {
 }
 
 void prompt(int D, int hq, int hk, int64_t B, int64_t T, bool starts, bool must) {
-  size_t ws = 0;
-  const int st = qprompt_attend_ws(D, hq, hk, B, T, &ws);
-  CHECK(!must || st == Q_OK, "qprompt_attend_ws: %d", st);
   drive("qprompt_attend", must, [&] {
     return qprompt_attend(D, hq, hk, B, T, starts ? dpt<int32_t>(1) : nullptr, dp(2), (int64_t)hq * D, dp(3), (int64_t)hk * D, dp(4),
-                          (int64_t)hk * D, 0.1f, dp(5), (int64_t)hq * D, Q_BF16, dp(6), ws, nullptr);
+                          (int64_t)hk * D, 0.1f, dp(5), (int64_t)hq * D, Q_BF16, nullptr);
   });
 }
 

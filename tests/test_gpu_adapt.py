@@ -54,7 +54,8 @@ def test_one_row_each(gpu, K, N, r, T, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K,N,r", SIZES)
-@pytest.mark.parametrize("lens", [[1], [64], [65], [5, 0, 0, 130], [1] * 70, [0, 17, 16, 1, 63, 64, 200, 0]])
+@pytest.mark.parametrize("lens", [[1], [64], [65], [5, 0, 0, 130], [1] * 70, [0, 17, 16, 1, 63, 64, 200, 0],
+                                  [100] + [1] * 40])
 def test_segments(gpu, K, N, r, lens, dtype):
     starts = [0]
     for n in lens:

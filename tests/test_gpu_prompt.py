@@ -186,15 +186,13 @@ def test_graph_follows_starts(gpu):
     T = 500
     Q, K, V = qkv(T, 8, 2, 64, 9)
     starts, out = i32([0, 0, 0, T]), torch.zeros((T, 8, 64), dtype=torch.bfloat16, device=DEV)
-    need = gpu.qprompt_attend_ws(64, 8, 2, 3, T)
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
     st = torch.cuda.Stream()
     with torch.cuda.stream(st):
-        gpu.qprompt_attend(Q, K, V, starts, out=out, ws=ws)
+        gpu.qprompt_attend(Q, K, V, starts, out=out)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=st):
-        gpu.qprompt_attend(Q, K, V, starts, out=out, ws=ws)
+        gpu.qprompt_attend(Q, K, V, starts, out=out)
     for now in ([0, 10, 200, 500], [0, 499, 499, 500], [100, 200, 300, 400], [0, 0, 500, 500]):
         starts.copy_(i32(now))
         V.copy_(randn((T, 2, 64), now[1]))
@@ -208,7 +206,7 @@ def test_graph_follows_starts(gpu):
         assert torch.equal(gpu.qprompt_attend(Q, K, V, starts, out=again), out)
 
 
-def test_streams_and_workspaces_of_their_own(gpu):
+def test_calls_at_once(gpu):
     sets = [qkv(900, 8, 2, 128, s) for s in (10, 20)]
     want = [gpu.qprompt_attend(*s) for s in sets]
     torch.cuda.synchronize()

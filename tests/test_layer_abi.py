@@ -24,7 +24,7 @@ def lib():
 def test_every_declared_symbol_is_exported(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"^\s*int\s+([a-z_]+)\s*\(", text, flags=re.M)))
-    assert names == ["qadapt", "qadapt_ws", "qnorm_rope", "qprompt_attend", "qprompt_attend_ws"]
+    assert names == ["qadapt", "qadapt_ws", "qnorm_rope", "qprompt_attend"]
     for n in names:
         assert hasattr(lib, n), n
 
@@ -132,10 +132,10 @@ def test_rope_without_a_description(lib):
 # ------------------------------------------------------------------- prompts
 def call_prompt(lib, **kw):
     d = dict(D=64, hq=4, h=2, B=2, T=9, starts=GOOD, Q=GOOD, qs=256, K=GOOD, ks=128, V=GOOD, vs=128, scale=0.1, out=GOOD * 2,
-             os=256, o=cg.Q_BF16, ws=GOOD, n=BIG)
+             os=256, o=cg.Q_BF16)
     d.update(kw)
     return lib.qprompt_attend(d["D"], d["hq"], d["h"], d["B"], d["T"], d["starts"], d["Q"], d["qs"], d["K"], d["ks"], d["V"], d["vs"],
-                              d["scale"], d["out"], d["os"], d["o"], d["ws"], d["n"], None)
+                              d["scale"], d["out"], d["os"], d["o"], None)
 
 
 SIZES = [(dict(D=0), cg.Q_EINVAL), (dict(D=96), cg.Q_EUNSUPPORTED), (dict(hq=5), cg.Q_EINVAL), (dict(hq=0), cg.Q_EINVAL),
@@ -151,11 +151,3 @@ SIZES = [(dict(D=0), cg.Q_EINVAL), (dict(D=96), cg.Q_EUNSUPPORTED), (dict(hq=5),
     (dict(scale=float("inf")), cg.Q_EINVAL), (dict(scale=1e14), cg.Q_EUNSUPPORTED), (dict(o=cg.Q_F16), cg.Q_EINVAL)])
 def test_prompt_refuses(lib, kw, status):
     assert call_prompt(lib, **kw) == status
-
-
-@pytest.mark.parametrize("kw,status", SIZES)
-def test_prompt_sizes_refused(lib, kw, status):
-    d = dict(D=64, hq=4, h=2, B=2, T=9)
-    d.update(kw)
-    n = ctypes.c_size_t()
-    assert lib.qprompt_attend_ws(d["D"], d["hq"], d["h"], d["B"], d["T"], ctypes.byref(n)) == status
