@@ -181,8 +181,11 @@ __device__ __forceinline__ void sched_turn(int products) {
 // KS: that many waves share 64 rows, each with its part of every step's keys, and
 // add up in LDS at the end: a tile's time is that of one wave's keys, and where
 // there are few tiles nothing else fills the card.
-template <int D, int KS>
-__global__ __launch_bounds__(256, 1) void prompt_kernel(Prompt p, int64_t tiles) {
+//
+// PER_CU: workgroups a CU holds at once.  Two, with half the registers each, for
+// heads of 64 and many tiles: one starts and ends its tiles while the other works.
+template <int D, int KS, int PER_CU>
+__global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t tiles) {
   constexpr int NW = 4, KT = 32 * NW, KBS = NW / KS, RT = 64 * NW / KS;
   constexpr int STEPS = D / 16, DT = D / 32;
   using Im = Image<D>;
@@ -261,7 +264,7 @@ __global__ __launch_bounds__(256, 1) void prompt_kernel(Prompt p, int64_t tiles)
     for (int s = 0; s < STEPS; ++s) qf[n][s] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(q + 16 * s));
   }
   {
-    int row = w.row0 + row_wave * 64;                           // the wave's first row sees least
+    int row = w.row0 + row_wave * 64;                       // the wave's first row sees least
     row = row < w.rows ? row : w.rows - 1;
     limmin = row / p.group + 1;
   }
@@ -537,8 +540,7 @@ namespace {
 // for the longest tile, or all tiles' over the card.  8 heads, 1 / 2 / 4 waves:
 // one prompt of 77 tokens, group 8, 11.0 / 12.0 / 13.0; of 300 18.1 / 16.5 / 25.3;
 // of 2000 83 / 111 / 179; of 4096, group 1, 129 / 81 / 71.
-int sharers(const Prompt& p) {
-  const double tiles = ((double)p.T * p.group / 256 + 0.5 * p.B) * p.heads, len = (double)p.T / p.B;
+int sharers(const Prompt& p, double tiles, double len) {
   const double step = p.head_dim == 128 ? 4.2 : 2.1, spread = tiles * len / (256.0 * 256.0);
   const double fixed[3] = {8, 10, 13};
   int best = 0;
@@ -554,18 +556,25 @@ int sharers(const Prompt& p) {
 }  // namespace
 
 hipError_t launch_prompt(const Prompt& p, hipStream_t st) {
-  const int ks = sharers(p);
+  const double about = ((double)p.T * p.group / 256 + 0.5 * p.B) * p.heads, len = (double)p.T / p.B;
+  const int ks = sharers(p, about, len);
+  // Two workgroups a CU against one, heads of 64, us: 64 prompts of 1 .. 100 (656
+  // tiles) 18.8 against 23.4, 32 of 1 .. 333 (400) 16.8 against 20.0, one of 8000
+  // (1000) 313 against 337; but one of 4096 (512) 103 against 97, 16 of 1 .. 1000
+  // (266) 28.7 against 27.0.
+  const bool two = p.head_dim == 64 && ks == 1 && (about > 512 || (about > 256 && len <= 256));
   const int64_t tiles = (int64_t)p.T * p.group / (256 / ks) + p.B;
   const int64_t most = (1 << 22) / p.heads;
   const dim3 grid((unsigned)((tiles < most ? tiles : most) * p.heads));
-#define GO(D, KS) hipLaunchKernelGGL((prompt_kernel<D, KS>), grid, dim3(256), 0, st, p, tiles)
-#define GO_D(D)            \
-  do {                     \
-    if (ks == 1) GO(D, 1); \
-    else if (ks == 2) GO(D, 2); \
-    else GO(D, 4);         \
+#define GO(D, KS, N) hipLaunchKernelGGL((prompt_kernel<D, KS, N>), grid, dim3(256), 0, st, p, tiles)
+#define GO_D(D)                   \
+  do {                            \
+    if (ks == 1) GO(D, 1, 1);      \
+    else if (ks == 2) GO(D, 2, 1); \
+    else GO(D, 4, 1);              \
   } while (0)
   if (p.head_dim == 128) GO_D(128);
+  else if (two) GO(64, 1, 2);
   else GO_D(64);
 #undef GO_D
 #undef GO

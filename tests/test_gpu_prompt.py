@@ -128,8 +128,9 @@ def test_rows_before_a_value_that_is_not_finite(gpu, D, H, G, value, which, at):
         assert bool(got[sees].isnan().all())
 
 
-# sizes whose tiles' rows one wave has to itself (many heads), or shares with one other or three (few heads, long)
-SHARED = [(64, 32, 8, [300, 0, 50]), (128, 24, 6, [280, 1, 60]), (128, 2, 4, [400, 90]), (64, 1, 1, [1500, 200]), (128, 1, 2, [1, 1700])]
+# sizes whose tiles' rows one wave has to itself (many heads; of 64 also with two workgroups a CU), or shares with one
+# other or three (few heads, long)
+SHARED = [(64, 96, 8, [300, 0, 50]), (64, 40, 2, [260, 30, 1] * 8), (64, 32, 8, [300, 0, 50]), (128, 24, 6, [280, 1, 60]), (128, 2, 4, [400, 90]), (64, 1, 1, [1500, 200]), (128, 1, 2, [1, 1700])]
 
 
 @pytest.mark.parametrize("D,H,G,lens", SHARED)
