@@ -560,7 +560,7 @@ hipError_t launch_prompt(const Prompt& p, hipStream_t st) {
   const int ks = sharers(p, about, len);
   // Two workgroups a CU against one, heads of 64, us: 64 prompts of 1 .. 100 (656
   // tiles) 18.8 against 23.4, 32 of 1 .. 333 (400) 16.8 against 20.0, one of 8000
-  // (1000) 313 against 337; but one of 4096 (512) 103 against 97, 16 of 1 .. 1000
+  // (1000) 297 against 337; but one of 4096 (512) 103 against 97, 16 of 1 .. 1000
   // (266) 28.7 against 27.0.
   const bool two = p.head_dim == 64 && ks == 1 && (about > 512 || (about > 256 && len <= 256));
   const int64_t tiles = (int64_t)p.T * p.group / (256 / ks) + p.B;
