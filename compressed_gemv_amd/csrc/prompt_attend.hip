@@ -51,6 +51,7 @@ struct Image {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLag = 8.0f;               // the running maximum may lag so far: weights up to 2^8
+constexpr float kFar = 1024.0f;            // a maximum (times log2 e) beyond which exponents are formed in two steps
 constexpr int kNoLoads = 0x0F70;           // s_waitcnt vmcnt(0), the other counters as they are
 
 __device__ __forceinline__ int wave_sum_i32(int v) {
@@ -289,6 +290,8 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
 
   f32x16_t acc[2][DT], z[2];
   float m[2], l[2], mx[2];
+  // of exponents, and what a logit passes before the maximum is looked at: m and m + kLag, or beyond kFar 0 and -inf
+  float base[2], lim_m[2];
   u32x4_t pw[2][2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
@@ -299,7 +302,8 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
     // before the first keys: weights of zero, logits that add nothing
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[n][i] = -INFINITY;
-    mx[n] = m[n] = -INFINITY;
+    mx[n] = m[n] = lim_m[n] = -INFINITY;
+    base[n] = 0.f;
     l[n] = 0.f;
     pw[n][0] = pw[n][1] = u32x4_t{0u, 0u, 0u, 0u};
   }
@@ -338,7 +342,7 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
   // masks, and the running maximum moved where it has to be (keys key .. key + 31)
   auto bounds = [&](auto blk, int key, uint32_t nan) {
     constexpr int n = decltype(blk)::value;
-    if (key + 32 > limmin || nan) {
+    if (__builtin_expect(key + 32 > limmin || nan, 0)) {
       asm volatile("");                    // a branch: the selects must not run in every step
 #pragma unroll
       for (int i = 0; i < 16; ++i) z[n][i] = key + 8 * (i / 4) + 4 * hh + i % 4 < lim[n] ? z[n][i] : -INFINITY;
@@ -351,7 +355,7 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
       }
       mx[n] = max_of(z[n]);
     }
-    if (__ballot(mx[n] * cq > m[n] + kLag)) {
+    if (__builtin_expect(__ballot(mx[n] * cq > lim_m[n]) != 0, 0)) {
       float v = mx[n] * cq;
       v = fmaxf(v, __shfl_xor(v, 32));
       v = v > m[n] + kLag ? v : m[n];      // a row's maximum moves by its own logits only
@@ -362,13 +366,27 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
       for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[n][t][i] *= f;
+      // An exponent z cq - m of one rounding is off by half a step of m: beyond 2^24
+      // the largest logit's own would leave 0 and take every weight with it.  The
+      // rounded product minus m is 0 there; it goes on as a z for a base of 0.
+      const bool far = fabsf(v) > kFar && v != -INFINITY;
+      lim_m[n] = far ? -INFINITY : v + kLag;
+      base[n] = fabsf(v) > kFar ? 0.f : v;  // where nothing is seen yet too
+      if (__builtin_expect(__ballot(far) != 0, 0)) {
+        const float up = 1.0f / cq;        // finite: logits below 2^126 pass kFar by a cq above 2^-116 only
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float e = z[n][i] * cq;
+          asm volatile("" : "+v"(e));      // rounded
+          z[n][i] = far ? (e - v) * up : z[n][i];
+        }
+      }
     }
   };
   // One turn: the softmax of block n against the products of the other block,
   // logits first, so that their maximum is there when the turn ends.
   auto turn = [&](auto soft, auto reads, auto&& after_s, auto&& after_pv) {
     constexpr int n = decltype(soft)::value, o = 1 - n;
-    const float base = m[n] == -INFINITY ? 0.f : m[n];
     float pv[16];
     f32x16_t zn;
 #pragma unroll
@@ -385,7 +403,7 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
     after_pv();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq, -base));
+      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq, -base[n]));
       l[n] += pv[i];
     }
 #pragma unroll

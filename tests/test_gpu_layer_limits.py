@@ -1,0 +1,71 @@
+"""The steps between projections and cache at the ends of their arguments'
+ranges, and over values that are not finite (include/qlayer.h)."""
+import math
+
+import pytest
+import torch
+
+from layer_util import DEV, check, i32, prompt_ref, randn
+from test_gpu_prompt import SHARED, qkv, starts_of, verify
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- prompts
+def peaks(starts, H, G, D, top, scale):
+    """Q, K, V whose logits are single products of 8 bits around +-2^top, and the result: of logits that far apart the
+    largest takes all the weight, and equal ones share it.  out = V of it (the mean of their V) with 2^-23 of each
+    addition and the quotient: n < 2^12 equal ones, added 16 at a time, stay below 2^-14."""
+    T = starts[-1]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(top)
+    sign = lambda *s: torch.randint(0, 2, s, generator=g, device=DEV).double() * 2 - 1
+    up = round(top - math.log2(abs(scale))) // 2
+    q = torch.zeros((T, H * G, D), dtype=torch.float64, device=DEV)
+    k = torch.zeros((T, H, D), dtype=torch.float64, device=DEV)
+    q[..., 3] = sign(T, H * G) * 2.0 ** up
+    k[..., 3] = sign(T, H) * (1 + torch.randint(0, 128, (T, H), generator=g, device=DEV) / 128.0) * 2.0 ** (top - round(math.log2(abs(scale))) - up)
+    V = randn((T, H, D), top + 1)
+    want = torch.empty((T, H * G, D), dtype=torch.float64, device=DEV)
+    for s, e in zip(starts, starts[1:]):
+        later = torch.ones((e - s, e - s), dtype=torch.bool, device=DEV).triu(1)
+        for h in range(H * G if e > s else 0):
+            z = (q[s:e, h, 3:4] * k[s:e, h // G, 3] * scale).masked_fill(later, -math.inf)
+            w = (z == z.amax(-1, keepdim=True)).double()
+            want[s:e, h] = w / w.sum(-1, keepdim=True) @ V[s:e, h // G].double()
+    return q.bfloat16(), k.bfloat16(), V, want
+
+
+@pytest.mark.parametrize("D,H,G,lens", [(128, 1, 1, [1]), (64, 2, 3, [70, 1, 300])] + SHARED)
+@pytest.mark.parametrize("top", [17, 24, 31, 40, 80, 118])
+@pytest.mark.parametrize("scale", [1.0, -0.3, 2.0 ** 45])
+def test_far_logits(gpu, D, H, G, lens, top, scale):
+    starts = starts_of(lens)
+    Q, K, V, want = peaks(starts, H, G, D, top, scale)
+    got = gpu.qprompt_attend(Q, K, V, i32(starts), scale=scale, out_dtype=torch.float32)
+    tol = torch.full_like(want, float(V.float().abs().max()) * 2.0 ** -14)
+    check(got, want, tol, (top, scale))
+
+
+@pytest.mark.parametrize("D,H,G,lens", SHARED)
+def test_far_logits_beside_others(gpu, D, H, G, lens):
+    """Rows of ordinary logits in the tiles of rows with far ones: the same bits as without them."""
+    starts = starts_of(lens)
+    T = starts[-1]
+    Q, K, V = qkv(T, H * G, H, D, 40)
+    K[..., 3] = (1 + torch.arange(T, device=DEV) % 60).bfloat16()[:, None]
+    Q[..., 3] = 0
+    alone = gpu.qprompt_attend(Q, K, V, i32(starts))
+    verify(alone, Q, K, V, starts)
+    far = (torch.arange(T * H * G, device=DEV) % 7 == 2).view(T, H * G)
+    Q[far] = 0                               # their logits are that one product
+    Q[..., 3] = torch.where(far, 2.0 ** 60, 0.0).bfloat16()
+    got = gpu.qprompt_attend(Q, K, V, i32(starts))
+    assert torch.equal(got[~far], alone[~far])
+    for s, e in zip(starts, starts[1:]):
+        for t in range(s, e, 23):
+            for h in range(0, H * G, max(1, H * G // 8)):
+                if far[t, h]:
+                    seen = K[s:t + 1, h // G, 3].float()
+                    want = V[s:t + 1, h // G][seen == seen.max()].double().mean(0)
+                    check(got[t, h], want, torch.full_like(want, 2.0 ** -14 * float(V.float().abs().max())), (t, h))
