@@ -521,7 +521,7 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
     const int row = w.row0 + row_wave * 64 + n * 32 + col;
     if (row >= w.rows) continue;
     const int tok = row / p.group, g = row - tok * p.group;
-    const float inv = l[n] == 0.f ? 0.f : 1.0f / l[n];
+    const float inv = 1.0f / l[n];          // every logit -inf: 0 / 0
     const int64_t at = (int64_t)(w.s0 + tok) * p.o_stride + (int64_t)(h * p.group + g) * D + 8 * hh;
 #pragma unroll
     for (int t = 0; t < DT; ++t)

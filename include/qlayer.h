@@ -105,8 +105,10 @@ int qnorm_rope(const qrope* p, int64_t B, int64_t T, const int32_t* lens, const 
  * stay below 2^120, sum_i |Q_i K_i| below 2^126, and |V| times the keys of a
  * sequence below 2^118.  1 <= B <= 65536,
  * 1 <= T <= 2^27, T * q_heads / kv_heads at most 2^30.
- * A row that sees a key or value that holds an infinity or a NaN comes out as
- * NaN or infinite, in that component at least; the rows before it do not.
+ * A row that sees a logit of NaN or +inf is NaN; a logit of -inf weighs nothing,
+ * and a row that sees no other is NaN.  A row that sees a value that is not
+ * finite comes out as NaN or infinite, in that component at least.  The rows
+ * before such keys and values do not change.
  * Precision: products of bf16 values in fp32, sums, maxima and the softmax
  * statistics fp32, weights rounded to bf16 before they meet V, also where the
  * output is fp32.  No workspace: calls may overlap. */

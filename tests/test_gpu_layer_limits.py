@@ -69,3 +69,22 @@ def test_far_logits_beside_others(gpu, D, H, G, lens):
                     seen = K[s:t + 1, h // G, 3].float()
                     want = V[s:t + 1, h // G][seen == seen.max()].double().mean(0)
                     check(got[t, h], want, torch.full_like(want, 2.0 ** -14 * float(V.float().abs().max())), (t, h))
+
+
+@pytest.mark.parametrize("D,H,G,lens", [(64, 2, 1, [1, 70]), (128, 1, 8, [40, 200])] + SHARED)
+def test_logits_of_minus_infinity(gpu, D, H, G, lens):
+    """A key whose products are all -inf weighs nothing; a row that sees no other key is NaN."""
+    starts = starts_of(lens)
+    Q, K, V = qkv(starts[-1], H * G, H, D, 41)
+    Q[..., 5] = Q[..., 5].abs() + 0.5
+    cut = []                                 # of every sequence the first few keys
+    for s, e in zip(starts, starts[1:]):
+        n = min(e - s, 3 + (e - s) // 3)
+        K[s:s + n, :, 5] = -math.inf
+        cut.append(n)
+    got = gpu.qprompt_attend(Q, K, V, i32(starts), out_dtype=torch.float32)
+    for s, e, n in zip(starts, starts[1:], cut):
+        assert bool(got[s:s + n].isnan().all())
+        if e > s + n:                        # the others see only what comes behind
+            want, tol = prompt_ref(Q[s + n:e], K[s + n:e], V[s + n:e], None, D ** -0.5)
+            check(got[s + n:e], want, tol)
