@@ -280,7 +280,9 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
         qf[n][s] = __builtin_bit_cast(bf16x8_t, v);
       }
   }
-  const float cq = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);   // positive also for a scale of 0: -inf stays -inf
+  // Positive also for a scale of 0, so that -inf stays -inf: the least there is, by
+  // which logits below 2^126 are 2^-23 at most and all weights 1.
+  const float cq = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 0x1p-149f);
   // The queries never change and only products read them: accumulation
   // registers hold them, the vector unit's stay free.
 #pragma unroll

@@ -88,3 +88,16 @@ def test_logits_of_minus_infinity(gpu, D, H, G, lens):
         if e > s + n:                        # the others see only what comes behind
             want, tol = prompt_ref(Q[s + n:e], K[s + n:e], V[s + n:e], None, D ** -0.5)
             check(got[s + n:e], want, tol)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-42, -1e-40, 1e-38])
+@pytest.mark.parametrize("D,H,G,lens", [(64, 2, 2, [1, 90, 300]), (128, 1, 8, [150]), (128, 1, 2, [1, 1700])])
+def test_scales_near_zero(gpu, D, H, G, lens, scale):
+    """Over products up to the largest there may be: a scale of 0 makes all weights equal."""
+    starts = starts_of(lens)
+    Q, K, V = qkv(starts[-1], H * G, H, D, 42)
+    Q = (Q.float().clamp(-3.9, 3.9) * 2.0 ** 55).bfloat16()
+    K = (K.float().clamp(-3.9, 3.9) * 2.0 ** 60).bfloat16()
+    assert float((Q.double().abs().amax((0, 1)) * K.double().abs().amax((0, 1))).sum()) < 2.0 ** 126
+    got = gpu.qprompt_attend(Q, K, V, i32(starts), scale=scale, out_dtype=torch.float32)
+    verify(got, Q, K, V, starts, torch.tensor(scale, dtype=torch.float32).item())
