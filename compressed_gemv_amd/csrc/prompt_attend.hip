@@ -406,8 +406,13 @@ __global__ __launch_bounds__(256, PER_CU) void prompt_kernel(Prompt p, int64_t t
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq, -base[n]));
-      l[n] += pv[i];
     }
+    // 16 weights are added up before they meet the sum, as in the products: by
+    // itself a weight below 2^-24 of the sum would be lost there and not here
+    float ps[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ps[i] = pv[2 * i] + pv[2 * i + 1];
+    l[n] += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
 #pragma unroll
     for (int e = 0; e < 8; ++e) pw[n][e / 4][e % 4] = cvt_pk_bf16(pv[2 * e], pv[2 * e + 1]);
     z[o] = zn;

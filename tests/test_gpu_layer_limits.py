@@ -101,3 +101,18 @@ def test_scales_near_zero(gpu, D, H, G, lens, scale):
     assert float((Q.double().abs().amax((0, 1)) * K.double().abs().amax((0, 1))).sum()) < 2.0 ** 126
     got = gpu.qprompt_attend(Q, K, V, i32(starts), scale=scale, out_dtype=torch.float32)
     verify(got, Q, K, V, starts, torch.tensor(scale, dtype=torch.float32).item())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_large_weight_and_many_small_ones(gpu, D):
+    """Weights of 2^-24.17 beside one of 1: each is lost if it is added to a sum by itself.  All values are 1, and so is
+    the result.  Sums between 1 and 1.01: the numerator takes at most n / 16 additions off by 2^-23 each, the sum of the
+    weights n / 32 in each of two lanes, off by 2^-24, and the rounding of the small weights (2^-8) is 2^-8 * 0.007."""
+    T = 1 << 17
+    Q = torch.zeros((T, 1, D), dtype=torch.bfloat16, device=DEV)
+    K, V = torch.zeros_like(Q), torch.ones_like(Q)
+    Q[..., 0] = 1.0
+    K[0, 0, 0] = 16.75
+    out = gpu.qprompt_attend(Q, K, V, scale=1.0, out_dtype=torch.float32)
+    off = float((out.double() - 1).abs().max())
+    assert off <= T / 16 * 2.0 ** -23 + T / 32 * 2.0 ** -24 + 2.0 ** -8 * 0.007 + 2.0 ** -20, off
