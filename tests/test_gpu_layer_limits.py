@@ -116,3 +116,37 @@ def test_one_large_weight_and_many_small_ones(gpu, D):
     out = gpu.qprompt_attend(Q, K, V, scale=1.0, out_dtype=torch.float32)
     off = float((out.double() - 1).abs().max())
     assert off <= T / 16 * 2.0 ** -23 + T / 32 * 2.0 ** -24 + 2.0 ** -8 * 0.007 + 2.0 ** -20, off
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_workgroup_with_a_second_tile(gpu, D):
+    """More tiles than the grid holds (2^22 over the heads): the workgroups of the first tiles, some of them long and
+    with values that are not finite, go on with the last sequences."""
+    H, lens = 1024, [300] * 8 + [1 + b % 2 for b in range(4300)] + [150] * 8
+    starts = starts_of(lens)
+    T, n = starts[-1], len(lens)
+    assert T // 256 + n > (1 << 22) // H + 200
+    Q, K, V = qkv(T, H, H, D, 43)
+    for b in range(1, 250, 2):               # in the tiles before those of the last sequences
+        V[starts[b], :, 5] = math.inf if b % 4 == 1 else math.nan
+    got = gpu.qprompt_attend(Q, K, V, i32(starts))
+    first = torch.tensor(starts[:-1], device=DEV)
+    sick = torch.zeros(n, dtype=torch.bool, device=DEV)
+    sick[1:250:2] = True
+    # a sequence's first row sees itself only
+    assert torch.equal(got[first[~sick]], V[first[~sick]])
+    assert bool((~got[first[sick]][..., 5].isfinite()).all())
+    second = first[8:8 + 4300][1::2] + 1
+    second = second[~sick[8:8 + 4300][1::2]]
+    for part in second.split(256):
+        q, k0, k1 = Q[part].double(), K[part - 1].double(), K[part].double()
+        z0, z1 = (q * k0).sum(-1, keepdim=True) * D ** -0.5, (q * k1).sum(-1, keepdim=True) * D ** -0.5
+        w = torch.sigmoid(z1 - z0)
+        v0, v1 = V[part - 1].double(), V[part].double()
+        # weights off by 2^-8 of themselves (rounded to bf16), and by 2^-16 (logits and exponentials: prompt_ref's terms)
+        check(got[part], v0 + (v1 - v0) * w, (v0.abs() * (1 - w) + v1.abs() * w) * (2.0 ** -8 + 2.0 ** -14))
+    for b in (0, 2, n - 8, n - 1):
+        s, e = starts[b], starts[b + 1]
+        for h in (0, 517, H - 1):
+            want, tol = prompt_ref(Q[s:e, h:h + 1], K[s:e, h:h + 1], V[s:e, h:h + 1], None, D ** -0.5)
+            check(got[s:e, h:h + 1], want, tol, (b, h))
