@@ -563,11 +563,16 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
         }
         h *= scale;
       }
+      // ranks behind the adapter's own: infinities of x have made them NaN or infinite
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = j + k < u.held ? h[k] : 0.f;
       uint32_t hi[2], lo[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         hi[k] = cvt_pk_bf16(h[2 * k], h[2 * k + 1]);
-        lo[k] = cvt_pk_bf16(h[2 * k] - bf16_lo_to_f32(hi[k]), h[2 * k + 1] - bf16_hi_to_f32(hi[k]));
+        const float a = bf16_lo_to_f32(hi[k]), b = bf16_hi_to_f32(hi[k]);
+        // an infinity leaves nothing (its difference would be NaN)
+        lo[k] = cvt_pk_bf16(fabsf(a) < INFINITY ? h[2 * k] - a : 0.f, fabsf(b) < INFINITY ? h[2 * k + 1] - b : 0.f);
       }
       *reinterpret_cast<uint2*>(hbuf + at * u.pitch + j) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(hbuf + at * u.pitch + deep + j) = make_uint2(lo[0], lo[1]);

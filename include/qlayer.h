@@ -50,9 +50,11 @@ int qadapt_ws(const qadapters* a, int64_t B, int64_t T, size_t* ws_bytes);
  * x 16-byte aligned and its stride a multiple of 8, below 2^24; y and out aligned
  * to their elements.
  * Precision: sums in fp32; A_a x enters the second product as bf16 hi + lo, 16
- * bits and more of it.  A row's result depends neither on the other rows' values
- * nor on when the call runs, its last bits on how many rows and requests there
- * are.
+ * bits and more of it (sums of 2^128 - 2^119 or more as infinities).  Values of x
+ * and A that are not finite come out as the formula has them; an infinity in B or
+ * in a scale may come out as NaN.  A row's result depends neither on the other
+ * rows' values nor on when the call runs, its last bits on how many rows and
+ * requests there are and on which adapters they name.
  * ws: device, 16-byte aligned, >= the qadapt_ws value; calls that may overlap
  * need one each. */
 int qadapt(const qadapters* a, int64_t B, int64_t T, const int32_t* ids, const int32_t* starts, const void* x,

@@ -150,3 +150,32 @@ def test_a_workgroup_with_a_second_tile(gpu, D):
         for h in (0, 517, H - 1):
             want, tol = prompt_ref(Q[s:e, h:h + 1], K[s:e, h:h + 1], V[s:e, h:h + 1], None, D ** -0.5)
             check(got[s:e, h:h + 1], want, tol, (b, h))
+
+
+# ------------------------------------------------------------------ adapters
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rank,own", [(8, 8), (8, 3), (16, 5), (24, 24), (40, 33), (128, 100)])
+@pytest.mark.parametrize("kind", ["few", "many", "requests", "tall"])
+def test_infinities_through_an_adapter(gpu, kind, rank, own, dtype):
+    """Infinities in x and A come out as the formula's: of the sign of B times them where all terms agree, else NaN."""
+    K, N, n = 264, 70, 2
+    T = {"few": 9, "many": 50, "requests": 40, "tall": 150}[kind]
+    starts = {"few": None, "many": None, "requests": [0] + list(range(9, 41)), "tall": [0, 100, 150]}[kind]
+    ids = [0] * T if starts is None else [0] * (len(starts) - 1)
+    A, B = randn((n, rank, K), 1).abs() + 0.125, randn((n, N, rank), 2)
+    B[:, ::2] = B[:, ::2].abs() + 0.125
+    B[:, 1::4] = -B[:, 1::4].abs() - 0.125
+    A[:, own:], B[:, :, own:] = math.nan, math.inf          # behind the adapter's rank: anything
+    x, y = randn((T, K), 3), randn((T, N), 4, dtype)
+    rows = list(range(1, T, 4))
+    x[rows[0::2], 7] = math.inf
+    x[rows[1::2], K - 1] = -math.inf
+    scales = torch.tensor([-0.5, 1.0], device=DEV)
+    a = gpu.make_qadapters(A, B, scales, i32([own, own]))
+    got = gpu.qadapt(a, x, y, i32(ids), None if starts is None else i32(starts))
+    h = (x.double()[:, None] * A[0, :own].double()).sum(-1)
+    want = y.double() - 0.5 * (h[:, None] * B[0, :, :own].double()).sum(-1)
+    assert bool((want[rows][:, ::2].isinf()).all()) and bool(want[rows][:, 1::4].isinf().all())
+    assert torch.equal(got[rows].double().nan_to_num(7.0, 1e300, -1e300), want[rows].nan_to_num(7.0, 1e300, -1e300))
+    rest = [t for t in range(T) if t not in rows]
+    assert bool(got[rest].isfinite().all())
