@@ -54,6 +54,7 @@ __device__ __forceinline__ uint32_t cvt_pk_f16(float lo, float hi) {
 // keys of weight 2^-25 would count as nothing; that was 1 to 2 % faster.  A lag
 // of 2 moves the maximum often: prompts of 999 .. 2500 281 us, against 263.
 constexpr float kLift = 9.0f, kLag = 6.0f;
+constexpr float kFar = 1024.0f;            // a maximum (times log2 e) beyond which exponents are formed in two steps
 constexpr int kNoLoads = 0x0F70;           // s_waitcnt vmcnt(0), the other counters as they are
 constexpr uint32_t k1024 = 0x64006400u, kM1024 = 0xE400E400u;   // fp16 pairs 1024, -1024
 
@@ -329,6 +330,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
 
   f32x16_t acc[2][DT], z[2];
   float m[2], l[2];
+  // of exponents, and what a logit passes before the maximum is looked at: m - kLift and m + kLag, or beyond kFar
+  // -kLift and -inf
+  float base[2], lim_m[2];
   u32x4_t p[2][2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
@@ -336,8 +340,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[n][t][i] = 0.f;
-    m[n] = -INFINITY;
-    l[n] = 0.f;
+    m[n] = lim_m[n] = -INFINITY;
+    base[n] = l[n] = 0.f;
     p[n][0] = p[n][1] = u32x4_t{0u, 0u, 0u, 0u};
   }
 
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
   // masks, and the running maximum moved where it has to be (keys key .. key + 31)
   auto bounds = [&](auto blk, int key, uint32_t holes) {
     constexpr int n = decltype(blk)::value;
-    if (key + 32 > limmin || holes) {
+    if (__builtin_expect(key + 32 > limmin || holes, 0)) {
       asm volatile("");                    // a branch: the selects must not run in every step
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -374,7 +378,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       }
       mx[n] = max_of(z[n]);
     }
-    if (__ballot(mx[n] * cq[n] > m[n] + kLag)) {
+    if (__builtin_expect(__ballot(mx[n] * cq[n] > lim_m[n]) != 0, 0)) {
       float v = mx[n] * cq[n];
       v = fmaxf(v, __shfl_xor(v, 32));
       v = fmaxf(v, m[n]);
@@ -385,13 +389,27 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
       for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[n][t][i] *= f;
+      // An exponent z cq - m of one rounding is off by half a step of m: beyond 2^24
+      // the largest logit's own would leave 0 and take every weight with it.  The
+      // rounded product minus m is 0 there; it goes on as a z.
+      const bool far = fabsf(v) > kFar && v != -INFINITY;
+      lim_m[n] = far ? -INFINITY : v + kLag;
+      base[n] = far ? -kLift : (v == -INFINITY ? 0.f : v - kLift);
+      if (__builtin_expect(__ballot(far) != 0, 0)) {
+        const float up = 1.0f / cq[n];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float e = z[n][i] * cq[n];
+          asm volatile("" : "+v"(e));      // rounded
+          z[n][i] = far ? (e - v) * up : z[n][i];
+        }
+      }
     }
   };
   // One turn: the softmax of block n against the products of the other block,
   // logits first, so that their maximum is there when the turn ends.
   auto turn = [&](auto soft, auto&& after_s, auto&& after_pv) {
     constexpr int n = decltype(soft)::value, o = 1 - n;
-    const float base = m[n] == -INFINITY ? 0.f : m[n] - kLift;
     float pv[16];
     f32x16_t zn;
 #pragma unroll
@@ -408,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kv_tile_kernel(AttendArgs x) {
     after_pv();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq[n], -base));
+      pv[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i], cq[n], -base[n]));
       l[n] += pv[i];
     }
 #pragma unroll
