@@ -27,6 +27,7 @@
 
 namespace qg {
 
+constexpr float kFar = 0x1p20f;                     // maxima (times log2 e) beyond it are taken off first
 constexpr float kUp = 0x1p64f, kDown = 0x1p-64f;   // scale of the query and weight operands
 constexpr float kCode = 0x1p69f;                   // product of a scaled operand and a code, undone
 
@@ -82,11 +83,14 @@ __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
   while (next_work<false, false, SPREAD>(x, pieces, w, lane)) {
   f32x4_t acc[NT][TILES];
   float m[NT], l[NT], po[NT];              // maximum, sum of weights, sum of weights times offsets
+  // of exponents, and what a logit passes before the maximum moves: m - 64 and m + 8, or beyond kFar -64 and -inf
+  float base[NT], lim_m[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) acc[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    m[n] = -INFINITY;
+    m[n] = lim_m[n] = -INFINITY;
+    base[n] = 0.f;
     l[n] = po[n] = 0.f;
   }
 
@@ -268,7 +272,7 @@ __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) mx = fmaxf(mx, t[n][j]);
-      grow |= mx > m[n] + 8.0f;
+      grow |= mx > lim_m[n];
       z[n][0][0] = mx;
     }
     // The maximum may lag by 8 (weights up to 2^8): it moves only when some
@@ -288,12 +292,19 @@ __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
         for (int q = 0; q < TILES; ++q)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][q][i] *= f;
+        // far from zero m - 64 is not 64 below m: the weights' factor would be 2^128, or 1
+        const bool far = fabsf(mx) > kFar && mx != -INFINITY;
+        lim_m[n] = far ? -INFINITY : mx + 8.0f;
+        base[n] = far ? -64.0f : (mx == -INFINITY ? 0.f : mx - 64.0f);
+        if (__builtin_expect(__ballot(far) != 0, 0)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[n][j] = far ? t[n][j] - mx : t[n][j];
+        }
       }
     }
     u32x4_t wh[NT], wl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float base = m[n] == -INFINITY ? 0.f : m[n] - 64.0f;
       uint32_t vm[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) vm[j] = vmr[j / 4][j % 4];
@@ -305,7 +316,7 @@ __device__ __forceinline__ void rows_body(const AttendArgs& x, unsigned block) {
       float wv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float p = exp2_hw(t[n][j] - base);   // 2^64 times the weight
+        const float p = exp2_hw(t[n][j] - base[n]);   // 2^64 times the weight
         wv[j] = mix_mul(f16_lo(vm[j]), p);
         po[n] = __builtin_fmaf(f16_hi(vm[j]), p, po[n]);
         l[n] += p;

@@ -75,3 +75,30 @@ def far_logits(gpu, D, H, G, lens, new, bits, scale, top):
                                             (128, 2, 8, [1500], [1100]), (128, 1, 4, [5000], [60])])
 def test_far_logits_of_many_rows(gpu, D, H, G, lens, new, bits, scale, top):
     far_logits(gpu, D, H, G, lens, new, bits, scale, top)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("scale,top", RANGE)
+@pytest.mark.parametrize("D,H,G,lens,new", [(128, 1, 4, [300, 33], [1, 1]), (64, 2, 8, [40, 517], [1, 4]), (128, 2, 4, [6000], [1]),
+                                            (64, 1, 3, [900] * 9, [2] * 9)])
+def test_far_logits_of_few_rows(gpu, D, H, G, lens, new, bits, scale, top):
+    far_logits(gpu, D, H, G, lens, new, bits, scale, top)
+
+
+@pytest.mark.parametrize("scale,top", RANGE)
+@pytest.mark.parametrize("new", [1, 40])
+def test_far_logits_behind_a_prefix(gpu, scale, top, new):
+    """The first sequence is the prefix of the others."""
+    D, H, G, lens, bits = 128, 1, 8, [701, 60, 90, 200], 8
+    cache, pages, starts, kc, vc, up = far_cache(gpu, lens, H, D, bits, top, scale)
+    q = queries(3 * new, H * G, D, up)
+    out = gpu.qcache_attend_shared(cache, q.bfloat16(), pages[0].contiguous(), 701, pages[1:].contiguous(), i32(lens[1:]),
+                                   i32([0, new, 2 * new, 3 * new]), scale=scale, out_dtype=torch.float32)
+    for b, n in enumerate(lens[1:]):
+        own = slice(starts[b + 1], starts[b + 2])
+        k, v = torch.cat((kc[:701], kc[own]))[:, 0], torch.cat((vc[:701], vc[own]))[:, 0]
+        sees = torch.arange(701 + n, device=DEV)[None] <= torch.arange(701 + n - new, 701 + n, device=DEV)[:, None]
+        for h in range(H * G):
+            want = winners(q[b * new:(b + 1) * new, h], k, v, scale, sees)
+            tol = torch.full_like(want, float(v.abs().max()) * (2.0 ** -10 + 2.0 ** -14))
+            check(out[b * new:(b + 1) * new, h], want, tol, (b, h))
