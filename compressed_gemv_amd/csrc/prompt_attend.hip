@@ -16,7 +16,7 @@
 // products and more vector instructions between them cost 1 to 2 %.
 #include <type_traits>
 
-#include "kvcache_plan.hpp"
+#include "common.hpp"
 #include "layer.hpp"
 
 namespace qg {
