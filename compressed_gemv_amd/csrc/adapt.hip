@@ -6,8 +6,9 @@
 // rows are bound by reading A and B of each adapter once, many by reading x and y
 // and writing out; the products are small beside either, so both run on
 // v_mfma_f32_16x16x32_bf16 with operands straight from memory.  h goes in as bf16
-// hi + lo (bf16 alone would lose 2^-9 of it), which doubles a product of depth
-// `rank` only.
+// parts, each the rounded rest of those before: three where y is fp32, which hold
+// all of it, and two where the result is rounded to bf16 (16 bits; one would lose
+// 2^-9).  They multiply a product of depth `rank` only.
 //
 // Rows meet an adapter in tiles of up to 64.  With starts, tile k of request b is
 // number starts[b] / 64 + b + k of T / 64 + B: numbers that need no sum over the
@@ -375,16 +376,20 @@ __global__ __launch_bounds__(256) void adapt_down_tall_kernel(Adapt p, int kchun
 
 // --------------------------------------------------------------------- up
 // One workgroup: a tile and a range of N.  h (all splits added, times scale)
-// lies in LDS as bf16, hi and lo: 32-deep blocks of hi, then those of lo, or for
-// ranks up to 16 both in one block, so that one product does.  A wave forms 64
+// lies in LDS as its bf16 parts: 32-deep blocks of the first, then those of the
+// next, or for ranks up to 16 two parts in one block, so that one product does.
+// A wave forms 64
 // outputs of 16 rows at a time (of 32 with twice the registers: the call 149 -> 156
 // us for 5 prompts of 77 .. 1500 rows): the four 16 x 16 products of a row tile give a
 // lane four neighbouring outputs of a row each (fp32: 16-byte accesses), or,
 // with the outputs of two products interleaved, eight (bf16).
+template <bool F32>
+constexpr int kParts = F32 ? 3 : 2;
+
 struct UpRows {
   const uint8_t* rows;
   const uint16_t* h;
-  int pitch, lo_at, blocks;                // of h: values per row, where lo begins, 32-deep blocks
+  int pitch, deep, blocks;                 // of h: values per row and per part, 32-deep blocks of a part
   int n, held;
 };
 
@@ -425,7 +430,7 @@ struct UpCols {
 template <bool F32>
 __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpRows& u, const UpCols<F32>& b, int row_tile, int lane) {
   const int r16 = lane & 15, g = lane >> 4, n0 = b.n0, n1 = b.n1;
-  const bool both = u.lo_at == 16;         // hi and lo in one block
+  const bool both = u.deep == 16;          // two parts in one block
   const int at = 16 * row_tile + r16;
   const bool on = at < u.n;
   const int64_t row = t.row0 + (on ? u.rows[at] : 0);
@@ -458,13 +463,13 @@ __device__ __forceinline__ void up_tile(const Adapt& p, const Tile& t, const UpR
     }
     b.mask(J, lane, bv);
     const uint16_t* hr = u.h + at * u.pitch + 32 * J + 8 * g;
-    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(hr);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(hi), acc[c], 0, 0, 0);
-    if (!both) {
-      const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(hr + u.lo_at);
+    for (int part = 0; part < kParts<F32>; ++part) {
+      if (both && part == 1) continue;
+      u32x4_t h = {0u, 0u, 0u, 0u};        // both: the third part has nothing beside it
+      if (!both || part == 0 || g < 2) h = *reinterpret_cast<const u32x4_t*>(hr + part * u.deep);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(lo), acc[c], 0, 0, 0);
+      for (int c = 0; c < 4; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(bv[c]), frag(h), acc[c], 0, 0, 0);
     }
   }
   if (!on) return;
@@ -539,9 +544,9 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
     u.held = rank_of(p, t.a);
     const bool both = u.held <= 16;
     const int deep = both ? 16 : (u.held + 31) / 32 * 32;
-    u.lo_at = deep;
+    u.deep = deep;
     u.blocks = both ? 1 : deep / 32;
-    u.pitch = 2 * deep + 8;                // 16 bytes more: neighbouring rows in other banks
+    u.pitch = kParts<F32> * deep + 8;      // 16 bytes more: neighbouring rows in other banks
     const int tall = (t.n + 15) / 16 * 16, kept = (u.held + 15) / 16 * 16;   // down wrote so many ranks
     const float scale = p.scales[t.a];
     UpCols<F32> cols;
@@ -566,16 +571,19 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(Adapt p, int slots, int s
       // ranks behind the adapter's own: infinities of x have made them NaN or infinite
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = j + k < u.held ? h[k] : 0.f;
-      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        hi[k] = cvt_pk_bf16(h[2 * k], h[2 * k + 1]);
-        const float a = bf16_lo_to_f32(hi[k]), b = bf16_hi_to_f32(hi[k]);
-        // an infinity leaves nothing (its difference would be NaN)
-        lo[k] = cvt_pk_bf16(fabsf(a) < INFINITY ? h[2 * k] - a : 0.f, fabsf(b) < INFINITY ? h[2 * k + 1] - b : 0.f);
+      for (int part = 0; part < kParts<F32>; ++part) {
+        uint32_t v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          v[k] = cvt_pk_bf16(h[2 * k], h[2 * k + 1]);
+          const float a = bf16_lo_to_f32(v[k]), b = bf16_hi_to_f32(v[k]);
+          // an infinity leaves nothing (its difference would be NaN)
+          h[2 * k] = fabsf(a) < INFINITY ? h[2 * k] - a : 0.f;
+          h[2 * k + 1] = fabsf(b) < INFINITY ? h[2 * k + 1] - b : 0.f;
+        }
+        *reinterpret_cast<uint2*>(hbuf + at * u.pitch + part * deep + j) = make_uint2(v[0], v[1]);
       }
-      *reinterpret_cast<uint2*>(hbuf + at * u.pitch + j) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(hbuf + at * u.pitch + deep + j) = make_uint2(lo[0], lo[1]);
     }
     __syncthreads();
     const int tiles16 = tall / 16;
@@ -608,7 +616,7 @@ hipError_t launch_adapt(const Adapt& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   const int deep = p.rank <= 16 ? 16 : (p.rank + 31) / 32 * 32;
   const int64_t tall = p.T < kTile ? ceil_div(p.T, 16) * 16 : kTile;
-  const size_t lds = (size_t)tall * (2 * deep + 8) * 2;
+  const size_t lds = (size_t)tall * ((p.f32 ? kParts<true> : kParts<false>) * deep + 8) * 2;
   const dim3 up((unsigned)(a.blocks * a.slots), (unsigned)ceil_div(p.N, a.nchunk));
   if (p.f32) hipLaunchKernelGGL((adapt_up_kernel<true>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);
   else hipLaunchKernelGGL((adapt_up_kernel<false>), up, dim3(256), lds, st, p, a.slots, a.splits, a.nchunk, a.R);

@@ -49,8 +49,9 @@ int qadapt_ws(const qadapters* a, int64_t B, int64_t T, size_t* ws_bytes);
  * starts 1 <= B <= 65536.  Strides in elements from row to row;
  * x 16-byte aligned and its stride a multiple of 8, below 2^24; y and out aligned
  * to their elements.
- * Precision: sums in fp32; A_a x enters the second product as bf16 hi + lo, 16
- * bits and more of it (sums of 2^128 - 2^119 or more as infinities).  Values of x
+ * Precision: sums in fp32; A_a x enters the second product in bf16 parts, all of
+ * it where y is fp32 and 16 bits and more where it is bf16 (sums of 2^128 - 2^119
+ * or more as infinities).  Values of x
  * and A that are not finite come out as the formula has them; an infinity in B or
  * in a scale may come out as NaN.  A row's result depends neither on the other
  * rows' values nor on when the call runs, its last bits on how many rows and

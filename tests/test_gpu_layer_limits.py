@@ -179,3 +179,30 @@ def test_infinities_through_an_adapter(gpu, kind, rank, own, dtype):
     assert torch.equal(got[rows].double().nan_to_num(7.0, 1e300, -1e300), want[rows].nan_to_num(7.0, 1e300, -1e300))
     rest = [t for t in range(T) if t not in rows]
     assert bool(got[rest].isfinite().all())
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("kind", ["few", "many", "tall"])
+def test_the_inner_product_keeps_its_bits(gpu, kind, rank):
+    """A x of 24 bits (three products 2^8 apart, below 2 in all) handed through a B of ones: every step is exact, so the
+    fp32 result is A x itself, times the scale's power of two."""
+    T, n, K, N = {"few": 5, "many": 70, "tall": 150}[kind], 2, 72, rank + 5
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rank)
+    A = torch.zeros((n, rank, K), device=DEV)
+    A[..., 3:6] = 1 + torch.randint(0, 124, (n, rank, 3), generator=g, device=DEV) / 128.0
+    x = torch.zeros((T, K), device=DEV)
+    up = (2.0 ** torch.randint(-20, 20, (T,), generator=g, device=DEV).double()).float()
+    assert bool((up.frexp()[0] == 0.5).all())
+    x[:, 3], x[:, 4], x[:, 5] = up, -up * 2.0 ** -8, up * 2.0 ** -16
+    B = torch.zeros((n, N, rank), device=DEV)
+    out_of = torch.arange(N, device=DEV) % rank
+    B[:, torch.arange(N, device=DEV), out_of] = 1.0
+    ids = [t % 3 - 1 for t in range(T)] if kind != "tall" else [1, 0]
+    starts = None if kind != "tall" else [0, 90, T]
+    a = gpu.make_qadapters(A.bfloat16(), B.bfloat16(), torch.tensor([0.25, 2.0], device=DEV))
+    got = gpu.qadapt(a, x.bfloat16(), torch.zeros((T, N), device=DEV), i32(ids), None if starts is None else i32(starts))
+    of = torch.tensor(ids if starts is None else [1] * 90 + [0] * (T - 90), device=DEV)
+    h = (A[of.clamp(min=0)].double() * x[:, None].double()).sum(-1)[:, out_of]
+    want = torch.where(of[:, None] >= 0, h * torch.tensor([0.25, 2.0], device=DEV).double()[of.clamp(min=0)][:, None], 0.0)
+    assert torch.equal(got.double(), want)
