@@ -8,7 +8,7 @@
 // v_mfma_f32_16x16x32_bf16 with operands straight from memory.  h goes in as bf16
 // parts, each the rounded rest of those before: three where y is fp32, which hold
 // all of it, and two where the result is rounded to bf16 (16 bits; one would lose
-// 2^-9).  They multiply a product of depth `rank` only.
+// 2^-8).  They multiply a product of depth `rank` only.
 //
 // Rows meet an adapter in tiles of up to 64.  With starts, tile k of request b is
 // number starts[b] / 64 + b + k of T / 64 + B: numbers that need no sum over the

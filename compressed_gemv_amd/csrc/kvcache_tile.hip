@@ -8,13 +8,12 @@
 // row by row, values transposed.  fp16 and not bf16 for values and weights: the
 // roundings of both then stay an eighth of the output's own.
 //
-// Measured (8 KV heads of 128, 8 query heads each): 1.00 PFLOP/s for 1024 tokens
-// that see 33000 cached ones (0.93 over the call; a large matrix product reaches
-// 1.2 here).  A product then takes 75 clocks of its SIMD, of which the matrix core
-// works 32 (counted: 43 % busy), at 2.24 GHz; with all numbers zero the clocks are
-// the same, at 2.39 GHz.  A prompt of 16000 0.90 over the call.  Shorter calls
-// pay for starting and ending a tile, 7 us or so: 0.80 for chunks of 700 .. 1024
-// behind 4500 .. 6001, 0.63 for prompts of 999 .. 2500.
+// Measured (8 KV heads of 128, 8 query heads each): 1.07 PFLOP/s for 1024 tokens
+// that see 33000 cached ones (0.99 over the call; a large matrix product reaches
+// 1.2 here).  A product then takes 68 clocks of its SIMD, of which the matrix core
+// works 32 (counted: 49 % busy).  A prompt of 16000 0.93 over the call.  Shorter
+// calls pay for starting and ending a tile, 7 us or so: 0.83 for chunks of 700 ..
+// 1024 behind 4500 .. 6001, 0.65 for prompts of 999 .. 2500.
 #include <type_traits>
 
 #include "common.hpp"

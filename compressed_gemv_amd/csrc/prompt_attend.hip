@@ -7,13 +7,19 @@
 // a time.  Tiles go to workgroups in the order of what they cost, the long ones
 // first, so no workgroup is left with a long one at the end.
 //
-// Bound by what a SIMD's one wave issues.  Measured (8 KV heads of 128, 8 query
-// heads each): 1.06 PFLOP/s for one prompt of 16000 (3.95 ms; a large matrix
-// product reaches 1.2 here), 0.77 for three of 999 .. 2500 (218 us).  In copies
-// of the kernel with parts left out, 16000 tokens took 11 % less without the
-// fetches of the next keys, 4 % less without exponentials, 2 % without the
-// maximum and nothing less without the reads from LDS; other orders of the
-// products and more vector instructions between them cost 1 to 2 %.
+// Bound by what a SIMD's one wave issues.  Measured on several cards (8 KV heads
+// of 128, 8 query heads each): 0.98 to 1.06 PFLOP/s for one prompt of 16000 (3.95
+// to 4.28 ms; a large matrix product reaches 1.2 here), 0.70 to 0.78 for three of
+// 999 .. 2500 (216 to 243 us).  In copies of the kernel with parts left out, 16000
+// tokens took 11 % less without the fetches of the next keys, 4 % less without
+// exponentials, 2 % without the maximum and nothing less without the reads from
+// LDS; other orders of the products and more vector instructions between them cost
+// 1 to 2 %.
+//
+// Weights meet V as bf16: the products' operands are of one type, V's is bf16, and
+// a second part of each weight would take half as many products again.  It leaves
+// 2^-8 of a weight at most, what a bf16 output's own rounding does; the sum of the
+// weights is of the unrounded ones, in fp32.
 #include <type_traits>
 
 #include "common.hpp"
@@ -563,8 +569,9 @@ namespace {
 // and ending a tile, 8, 10 and 13 for 1, 2 and 4 waves, once for every 256
 // workgroups; and a step of 128 keys, 4.2 (2.1 for heads of 64), over the waves
 // for the longest tile, or all tiles' over the card.  8 heads, 1 / 2 / 4 waves:
-// one prompt of 77 tokens, group 8, 11.0 / 12.0 / 13.0; of 300 18.1 / 16.5 / 25.3;
-// of 2000 83 / 111 / 179; of 4096, group 1, 129 / 81 / 71.
+// one prompt of 77 tokens, group 8, 11.7 / 12.6 / 13.4; of 300 19.3 / 17.7 / 26.0;
+// of 2000 95 / 116 / 182; of 4096, group 1, 133 / 81 / 73.  The host knows the mean
+// length only: a long prompt among many short ones is shared as if all were short.
 int sharers(const Prompt& p, double tiles, double len) {
   const double step = p.head_dim == 128 ? 4.2 : 2.1, spread = tiles * len / (256.0 * 256.0);
   const double fixed[3] = {8, 10, 13};
@@ -583,10 +590,12 @@ int sharers(const Prompt& p, double tiles, double len) {
 hipError_t launch_prompt(const Prompt& p, hipStream_t st) {
   const double about = ((double)p.T * p.group / 256 + 0.5 * p.B) * p.heads, len = (double)p.T / p.B;
   const int ks = sharers(p, about, len);
-  // Two workgroups a CU against one, heads of 64, us: 64 prompts of 1 .. 100 (656
-  // tiles) 18.8 against 23.4, 32 of 1 .. 333 (400) 16.8 against 20.0, one of 8000
-  // (1000) 297 against 337; but one of 4096 (512) 103 against 97, 16 of 1 .. 1000
-  // (266) 28.7 against 27.0.
+  // Two workgroups a CU against one, heads of 64, us (in brackets `about`): 64
+  // prompts of 1 .. 100 (328) 12.5 against 15.9, 32 of 1 .. 333 (397) 16.6 against
+  // 20.2, 32 of 1 .. 500 (564) 25.5 against 31.6, one of 8000 (1004) 298 against
+  // 328; but 16 of 1 .. 1000 (266) 29.4 against 28.2, one of 3000 (379) 68.3 against
+  // 63.4, 8 of 500 .. 1100 (415) 31.7 against 30.6.  One of 4096 is either's: 8 KV
+  // heads (516) 101 against 104, 4 (514) 99 against 96, 32 (528) 103 against 102.
   const bool two = p.head_dim == 64 && ks == 1 && (about > 512 || (about > 256 && len <= 256));
   const int64_t tiles = (int64_t)p.T * p.group / (256 / ks) + p.B;
   const int64_t most = (1 << 22) / p.heads;

@@ -51,11 +51,14 @@ int qadapt_ws(const qadapters* a, int64_t B, int64_t T, size_t* ws_bytes);
  * to their elements.
  * Precision: sums in fp32; A_a x enters the second product in bf16 parts, all of
  * it where y is fp32 and 16 bits and more where it is bf16 (sums of 2^128 - 2^119
- * or more as infinities).  Values of x
- * and A that are not finite come out as the formula has them; an infinity in B or
- * in a scale may come out as NaN.  A row's result depends neither on the other
- * rows' values nor on when the call runs, its last bits on how many rows and
- * requests there are and on which adapters they name.
+ * or more as infinities).  Values of x and A that are not finite come out as the
+ * formula has them; an infinity in B or in a scale may come out as NaN.  A row's
+ * result depends neither on the other rows' values nor on when the call runs, its
+ * last bits on how many rows and requests there are and on which adapters they
+ * name.
+ * Speed: which kernels run is chosen on the host from B and T, so a long request
+ * among many single rows (fewer than 16 rows each on average) is faster in a call
+ * of its own.
  * ws: device, 16-byte aligned, >= the qadapt_ws value; calls that may overlap
  * need one each. */
 int qadapt(const qadapters* a, int64_t B, int64_t T, const int32_t* ids, const int32_t* starts, const void* x,
@@ -114,7 +117,9 @@ int qnorm_rope(const qrope* p, int64_t B, int64_t T, const int32_t* lens, const 
  * before such keys and values do not change.
  * Precision: products of bf16 values in fp32, sums, maxima and the softmax
  * statistics fp32, weights rounded to bf16 before they meet V, also where the
- * output is fp32.  No workspace: calls may overlap. */
+ * output is fp32.  No workspace: calls may overlap.
+ * Speed: how a tile's keys are shared is chosen on the host from T and B, so one
+ * long prompt is faster in a call of its own than among many short or empty ones. */
 int qprompt_attend(int head_dim, int q_heads, int kv_heads, int64_t B, int64_t T, const int32_t* starts, const void* Q,
                    int64_t q_stride, const void* K, int64_t k_stride, const void* V, int64_t v_stride, float scale,
                    void* out, int64_t o_stride, int out_dtype, hipStream_t stream);
