@@ -90,6 +90,22 @@ def test_logits_of_minus_infinity(gpu, D, H, G, lens):
             check(got[s + n:e], want, tol)
 
 
+@pytest.mark.parametrize("D,H,G,lens", [(64, 2, 1, [1, 70]), (128, 1, 8, [40, 200])] + SHARED)
+def test_logits_of_plus_infinity(gpu, D, H, G, lens):
+    """A row that sees one is NaN; the others do not feel it."""
+    starts = starts_of(lens)
+    Q, K, V = qkv(starts[-1], H * G, H, D, 44)
+    Q[..., 5] = Q[..., 5].abs() + 0.5
+    clean = gpu.qprompt_attend(Q, K, V, i32(starts))
+    sees = torch.zeros(starts[-1], dtype=torch.bool, device=DEV)
+    for s, e in zip(starts, starts[1:]):
+        if e > s:
+            K[s + (e - s) // 2, :, 5] = math.inf
+            sees[s + (e - s) // 2:e] = True
+    got = gpu.qprompt_attend(Q, K, V, i32(starts))
+    assert bool(got[sees].isnan().all()) and torch.equal(got[~sees], clean[~sees])
+
+
 @pytest.mark.parametrize("scale", [0.0, 1e-42, -1e-40, 1e-38])
 @pytest.mark.parametrize("D,H,G,lens", [(64, 2, 2, [1, 90, 300]), (128, 1, 8, [150]), (128, 1, 2, [1, 1700])])
 def test_scales_near_zero(gpu, D, H, G, lens, scale):
