@@ -990,7 +990,7 @@ def _here(place, *ts):
     for t in ts:
         if t is not None and (t.get_device() != place._index or not t.is_contiguous()):
             _on_device(place, False, t)
-            raise ValueError("all arguments but rows and outputs must be contiguous")
+            raise ValueError("ids, lens, starts, freqs, weights and ws must be contiguous")
 
 
 def _matrix(t: torch.Tensor, T, width: int, dtypes, what: str) -> int:
@@ -1048,7 +1048,7 @@ def _adapt_ws(n, K, N, rank, B, T) -> int:
 
 
 def qadapt_ws(adapters: qadapters, B: int, T: int) -> int:
-    """Workspace bytes for B requests with T rows in all."""
+    """Workspace bytes for B requests with T rows in all (not always more for more rows)."""
     return _adapt_ws(adapters.n, adapters.K, adapters.N, adapters.rank, B, T)
 
 

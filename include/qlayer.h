@@ -38,7 +38,9 @@ typedef struct qadapters {
                                 What lies behind it in A and B may be anything. */
 } qadapters;
 
-/* Workspace bytes of qadapt (host only; reads n, K, N and rank). */
+/* Workspace bytes of qadapt (host only; reads n, K, N and rank).  Fewer rows may
+ * need more (A_a x is divided further), so a workspace for calls of several sizes
+ * has the largest of their values. */
 int qadapt_ws(const qadapters* a, int64_t B, int64_t T, size_t* ws_bytes);
 
 /* out[t][:] = y[t][:] + scale[a] * B_a (A_a x[t][:]) with a = ids[b] for the
